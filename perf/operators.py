@@ -294,7 +294,7 @@ def _plain_norm(s):
     a = t.abs().amax(-1)
     step = torch.where(a > 0, a / torch.full((), 127.0, device=DEV), 1.0)
     code = (t / step[:, None]).round().clamp(-127, 127)
-    s_a = step * r
+    s_a = torch.where(a > 0, step * r, 1.0)
     return {"h": h.bfloat16(), "value": (code * s_a[:, None]).bfloat16(), "s_a": s_a}
 
 
