@@ -331,6 +331,214 @@ BI_API bi_status bi_attention_verify(const uint16_t *q, const uint16_t *k, const
                                      bi_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Decoder-step operators: what stands between the linears of a decode or
+ * verify step when it serves a model with normalised layers, rotary positions
+ * and a shared cache.  Like everything above, a row's result does not depend
+ * on the rows beside it: the same bits for any M, T, B and any other sequences
+ * in the call.
+ * ---------------------------------------------------------------------------
+ *
+ * bi_rmsnorm_quantize: the residual's addition, the root-mean-square norm and
+ * the activation quantisation of the linear that reads it.  Per row, fp32:
+ *   h'  = bf16_rne(h + y)                 (h itself when y is NULL)
+ *   t_k = h'_k * w_k                      (exact: two bf16 factors)
+ *   r   = 1 / sqrt(sum_k h'_k^2 / K + eps)
+ *   a   = max_k |t_k|;  st = a / 127 (IEEE division)
+ *   q_k = clamp(rne(t_k / st), -127, 127);  s_a = st * r
+ * An all-zero t gives q = 0 and s_a = 1.  The normalised row is t * r, and
+ * per-row absmax quantisation is invariant to a row's factor, so the codes are
+ * those of the normalised row, without the rounding of r in them; r's sum is
+ * taken in an order that depends on K alone.
+ *   h    bf16 [M, ldh], read only;  y bf16 [M, ldy], read only, or NULL
+ *   w    bf16 [K], the norm's weight;  eps >= 0
+ *   h_out bf16 [M, ldo] receives h'; it may be h (ldo == ldh) but not overlap
+ *        it otherwise.  Given exactly when y is given.
+ *   q    int8 [M, K] out, s_a fp32 [M] out, for bi_linear_w8a8
+ * 16-byte aligned h, y, w, h_out and q; row strides multiples of 8 elements;
+ * K as for bi_quantize_act.  Products t and the sum of squares must be finite
+ * in fp32.  With BI_FLAG_PDL the kernel waits for the preceding kernel first.
+ */
+BI_API bi_status bi_rmsnorm_quantize(const uint16_t *h, int64_t ldh, const uint16_t *y, int64_t ldy, const uint16_t *w,
+                                     float eps, int M, int K, uint16_t *h_out, int64_t ldo, int8_t *q, float *s_a,
+                                     unsigned flags, bi_stream_t stream);
+
+/*
+ * A paged key/value cache held in 4 bits.  Page p of the pool starts at byte
+ * p * page_stride and holds page_size positions of every kv head; the block of
+ * kv head g starts bi_kv4_block_bytes(page_size, D) * g bytes into its page.
+ * Every 64 consecutive elements of a head's key (or value) at one position
+ * form a group with a scale s and a minimum z, both bf16, and 4-bit codes:
+ *   z = min x;  s = bf16_rne((max x - min x) / 15)  (fp32, IEEE division)
+ *   c = clamp(rne((x - z) / s), 0, 15)  (fp32, IEEE division; 0 when s = 0)
+ *   the value held is z + s * c.
+ * x are bf16 values, so z is exact.  Finite x only (other values give codes and
+ * parameters without meaning, in their own group).
+ * Inside a block, P = page_size, G = D / 64, all words little-endian:
+ *   keys       [P][4 segments][G][2 words], position-major: element d of a key
+ *              is in segment (d % 64) / 16, group d / 64, word (d % 16) / 8,
+ *              nibble (d % 8) / 2 + 4 (d % 2);
+ *   values     [P / 2][8 segments][G][2 words], after P D / 2 bytes: positions
+ *              2 i and 2 i + 1 share words, the even one in the low half;
+ *              element d is in segment (d % 64) / 8, group d / 64, word
+ *              (d % 8) / 4, nibble d % 4 of its half;
+ *   parameters [P][2][G] words, after P D bytes: s in the low and z in the
+ *              high half, keys then values.
+ * The order of the nibbles is that of tensor-core fragments, so that the
+ * attention needs one AND for two codes.
+ */
+typedef struct {
+    void *pool;          /* device, 16-byte aligned */
+    int64_t page_stride; /* bytes, a multiple of 16, >= Hkv * bi_kv4_block_bytes(page_size, D) */
+    int num_pages;
+    int page_size;       /* positions a page: 16, 32, 64 or 128 */
+    int Hkv;             /* kv heads, 1 .. 1024 */
+    int D;               /* head size, 64 or 128 */
+} bi_kv4_cache;
+
+/*
+ * A batch of sequences with new tokens, as the append, the gather and the
+ * attention read it.  Token rows cu_q[b] .. cu_q[b + 1] - 1 are the newest of
+ * sequence b: the last of them is at position kv_len[b] - 1.  Position p of
+ * sequence b is kept in page pages[b * ld_pages + p / page_size] of the pool,
+ * at p % page_size.  The arrays are read on the device, so a captured graph
+ * can be replayed with other lengths and pages; T, max_q and max_kv are bounds
+ * that the host knows.  Rows from T on, tokens of a sequence past max_q and
+ * positions past max_kv are left out, like positions whose page index lies
+ * outside the table or whose page is not in 0 .. num_pages - 1: they are not
+ * written, not attended to, and gathered as zeros; a token so left out has
+ * zeros for its outputs.  Token rows from cu_q[B] on belong to no sequence:
+ * their outputs are not touched.
+ */
+typedef struct {
+    const int32_t *cu_q;   /* [B + 1], non-decreasing, cu_q[0] = 0 */
+    const int32_t *kv_len; /* [B], new tokens included */
+    const int32_t *pages;  /* [B, ld_pages] */
+    int64_t ld_pages;
+    int B;                 /* sequences, 1 .. 65535 */
+    int T;                 /* rows of the token arrays, 1 .. 2^20 */
+    int max_q;             /* most new tokens of a sequence, 1 .. 65535 */
+    int max_kv;            /* longest sequence, 1 .. 2^22 */
+} bi_kv4_batch;
+
+/* Bytes of one kv head of one page; 0 for a page size or head size that is not supported. */
+BI_API size_t bi_kv4_block_bytes(int page_size, int D);
+
+/*
+ * Table of rotations: rope[p][i] = (cos, sin)(p * inv_freq[i]) * amp as fp32
+ * pairs, p < n_pos, i < n_freq, the angle and its functions in fp64.  Long
+ * contexts scale inv_freq (interpolation by a common factor or per frequency)
+ * and amp (the amplitude that goes with it); both are the caller's.
+ *   inv_freq  fp64 [n_freq], device;  rope fp32 [n_pos, n_freq, 2] out, 8-byte aligned
+ */
+BI_API bi_status bi_rope_table(const double *inv_freq, int n_freq, float amp, int n_pos, float *rope,
+                               bi_stream_t stream);
+
+/*
+ * New tokens' heads: optional RMS norm of every q and k head, rotation, q out
+ * in bf16, k and v appended to the cache.  Per head x[D] of q or k, fp32, every
+ * operation rounded once:
+ *   norm (q_norm / k_norm given): n_d = (x_d * r) * w_d,
+ *        r = 1 / sqrt(S / D + eps), S = the squares added as halves (d and
+ *        d + D / 2), then neighbours, then halves again down to one;
+ *   rotation of the first `rot` elements by rope[position]: a pair (a, b)
+ *        becomes (a c - b s, b c + a s); pair i is (i, i + rot / 2) with
+ *        BI_ROPE_HALF and (2 i, 2 i + 1) with BI_ROPE_INTERLEAVED;
+ *   bf16_rne; k and v (v as given) are then quantised as bi_kv4_cache says.
+ * A token at a negative position or one past n_pos has q_out 0 and is not
+ * appended.
+ *   q  bf16, row t and head h at q + t ldq + h D, Hq heads (read only)
+ *   k, v  bf16, rows of Hkv heads with strides ldk, ldv
+ *        (the three may be parts of one packed projection output)
+ *   rope  fp32 [n_pos, rot / 2, 2];  rot a multiple of 4, 0 .. D
+ *   q_norm, k_norm  bf16 [D] or NULL;  eps >= 0
+ *   q_out bf16 [T, Hq, D], must not overlap the inputs
+ * 16-byte aligned pointers; strides multiples of 8 elements.  Hq, Hkv <= 1024.
+ * With BI_FLAG_PDL the kernel waits for the preceding kernel first.
+ */
+enum { BI_ROPE_HALF = 0, BI_ROPE_INTERLEAVED = 1 };
+BI_API bi_status bi_rope_append_kv4(const uint16_t *q, int64_t ldq, int Hq, const uint16_t *k, int64_t ldk,
+                                    const uint16_t *v, int64_t ldv, const uint16_t *q_norm, const uint16_t *k_norm,
+                                    float eps, const float *rope, int n_pos, int rot, int layout, uint16_t *q_out,
+                                    const bi_kv4_cache *cache, const bi_kv4_batch *batch, unsigned flags,
+                                    bi_stream_t stream);
+
+/*
+ * The cached keys and values of the batch's token rows, as bf16_rne(z + s c):
+ * what an append wrote, or, with cu_q counting whole sequences, a cached prefix.
+ *   k_out, v_out  bf16 [T, Hkv, D] out, 16-byte aligned, not overlapping.
+ */
+BI_API bi_status bi_kv4_gather(const bi_kv4_cache *cache, const bi_kv4_batch *batch, uint16_t *k_out, uint16_t *v_out,
+                               bi_stream_t stream);
+
+/*
+ * Attention of the batch's new tokens over the 4-bit cache.  The token at
+ * position p of sequence b sees that sequence's positions 0 .. p; q head h
+ * reads kv head h / (Hq / Hkv):
+ *   o = sum_j softmax_j(scale q . k_j) v_j  over the values held.
+ * A token that sees no position (a sequence of length 0) has o = 0.
+ *   q  bf16, row t at q + t ldq, head h at h D (ldq >= Hq D, a multiple of 8)
+ *   o  bf16 [T, Hq, D] out, must not overlap q
+ *   scale  positive and finite
+ *   ws  workspace of at least bi_attention_kv4_workspace_size(...) bytes,
+ *       16-byte aligned, zero-filled before its first use; every call that
+ *       completes leaves it ready for the next.  Its layout depends on no
+ *       argument, so one workspace of the largest size serves calls of any
+ *       shape on one stream.
+ * Scores, softmax sums and outputs are fp32; the products run on the tensor
+ * cores with the codes exact and q exact but for elements 2^-24 below its
+ * head's largest, and the weights in f16 with 11 bits.  A query's result
+ * depends on its own positions only.
+ */
+BI_API size_t bi_attention_kv4_workspace_size(int Hq, const bi_kv4_cache *cache, const bi_kv4_batch *batch);
+BI_API bi_status bi_attention_kv4(const uint16_t *q, int64_t ldq, int Hq, const bi_kv4_cache *cache,
+                                  const bi_kv4_batch *batch, float scale, uint16_t *o, void *ws, size_t ws_bytes,
+                                  unsigned flags, bi_stream_t stream);
+
+/*
+ * Rules applied to logits before the argmax or a sampler reads them.  Row m of
+ * M, element v, fp32, every operation rounded once, in this order:
+ *   x = logits[m][v]
+ *   if v is in the row's history:    x = x > 0 ? x / repetition : x * repetition
+ *   if it is there c > 0 times as a generated token:
+ *                                    x = (x - frequency * c) - presence
+ *   if the row has a bias for v:     x = x + bias
+ *   if the row's mask forbids v:     x = -inf
+ * out[m][v] = x, and argmax[m] = the lowest v with the largest x (NaN counts as
+ * -inf), or -1 when every x is -inf: nothing is allowed.
+ * The history of row m is ids[begin[m]] .. ids[end[m] - 1]; those from mid[m] on
+ * are generated, the others the prompt's.  Rows of one verify pass share ids
+ * and differ in `end`.  Ids outside 0 .. V - 1 are ignored.
+ */
+typedef struct {
+    const int32_t *ids;        /* all rows' histories, or NULL: none */
+    const int32_t *begin, *mid, *end; /* [M] each, given with ids */
+    const float *repetition;   /* [M], > 0, or NULL: 1 */
+    const float *presence;     /* [M] or NULL: 0 */
+    const float *frequency;    /* [M] or NULL: 0 */
+    const int32_t *bias_ids;   /* [M, n_bias] or NULL; of equal ids in a row the last applies */
+    const float *bias;         /* [M, n_bias], given with bias_ids */
+    int n_bias;                /* 0 .. 65536 */
+    const uint32_t *mask;      /* [M, ld_mask] words, bit v % 32 of word v / 32 set = allowed; or NULL: all */
+    int64_t ld_mask;           /* >= ceil(V / 32) */
+} bi_logits_rules;
+
+/*
+ *   logits  bf16 [M, ldl] (read only), ldl >= V
+ *   out     fp32 [M, ldo], ldo >= V, or NULL;  argmax int32 [M] or NULL (not
+ *           both NULL)
+ *   ws      workspace of at least bi_logits_workspace_size(M) bytes, 16-byte
+ *           aligned, zero-filled before its first use; every call that completes
+ *           leaves it zero-filled
+ * 1 <= M <= 65535, 1 <= V <= 2^24.  Logits rows may start anywhere on 2 bytes,
+ * out rows on 4; rows on 16 bytes are faster.
+ */
+BI_API size_t bi_logits_workspace_size(int M);
+BI_API bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, int V, const bi_logits_rules *rules,
+                                   float *out, int64_t ldo, int32_t *argmax, void *ws, size_t ws_bytes, unsigned flags,
+                                   bi_stream_t stream);
+
+/*
  * Bandwidth probes, for measurement only: the device's own read-only and copy
  * ceilings with 16-byte streaming loads (8 in flight per thread) over a grid
  * of four 512-thread CTAs per SM.  A weight stream only reads, so the

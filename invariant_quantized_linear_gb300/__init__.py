@@ -71,6 +71,46 @@ lib.bi_attention_workspace_size.restype = _sz
 lib.bi_attention_verify.argtypes = [_vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _ci, ctypes.c_float, _vp, _vp, _sz,
                                     _vp]
 lib.bi_attention_verify.restype = _ci
+
+
+class bi_kv4_cache(ctypes.Structure):
+    """A paged 4-bit key/value cache (struct bi_kv4_cache of include/bi.h)."""
+    _fields_ = [("pool", _vp), ("page_stride", _i64), ("num_pages", _ci), ("page_size", _ci), ("Hkv", _ci), ("D", _ci)]
+
+
+class bi_kv4_batch(ctypes.Structure):
+    """Sequences with new tokens (struct bi_kv4_batch of include/bi.h)."""
+    _fields_ = [("cu_q", _vp), ("kv_len", _vp), ("pages", _vp), ("ld_pages", _i64), ("B", _ci), ("T", _ci),
+                ("max_q", _ci), ("max_kv", _ci)]
+
+
+class bi_logits_rules(ctypes.Structure):
+    """Rules applied to logits (struct bi_logits_rules of include/bi.h)."""
+    _fields_ = [("ids", _vp), ("begin", _vp), ("mid", _vp), ("end", _vp), ("repetition", _vp), ("presence", _vp),
+                ("frequency", _vp), ("bias_ids", _vp), ("bias", _vp), ("n_bias", _ci), ("mask", _vp), ("ld_mask", _i64)]
+
+
+_cache_p, _batch_p = ctypes.POINTER(bi_kv4_cache), ctypes.POINTER(bi_kv4_batch)
+lib.bi_rmsnorm_quantize.argtypes = [_vp, _i64, _vp, _i64, _vp, ctypes.c_float, _ci, _ci, _vp, _i64, _vp, _vp, _cu, _vp]
+lib.bi_rmsnorm_quantize.restype = _ci
+lib.bi_kv4_block_bytes.argtypes = [_ci, _ci]
+lib.bi_kv4_block_bytes.restype = _sz
+lib.bi_rope_table.argtypes = [_vp, _ci, ctypes.c_float, _ci, _vp, _vp]
+lib.bi_rope_table.restype = _ci
+lib.bi_rope_append_kv4.argtypes = [_vp, _i64, _ci, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_float, _vp, _ci, _ci, _ci,
+                                   _vp, _cache_p, _batch_p, _cu, _vp]
+lib.bi_rope_append_kv4.restype = _ci
+lib.bi_kv4_gather.argtypes = [_cache_p, _batch_p, _vp, _vp, _vp]
+lib.bi_kv4_gather.restype = _ci
+lib.bi_attention_kv4_workspace_size.argtypes = [_ci, _cache_p, _batch_p]
+lib.bi_attention_kv4_workspace_size.restype = _sz
+lib.bi_attention_kv4.argtypes = [_vp, _i64, _ci, _cache_p, _batch_p, ctypes.c_float, _vp, _vp, _sz, _cu, _vp]
+lib.bi_attention_kv4.restype = _ci
+lib.bi_logits_workspace_size.argtypes = [_ci]
+lib.bi_logits_workspace_size.restype = _sz
+lib.bi_logits_process.argtypes = [_vp, _i64, _ci, _ci, ctypes.POINTER(bi_logits_rules), _vp, _i64, _vp, _vp, _sz, _cu,
+                                  _vp]
+lib.bi_logits_process.restype = _ci
 lib.bi_probe_read.argtypes = [_vp, _sz, _vp, _vp]
 lib.bi_probe_read.restype = _ci
 lib.bi_probe_copy.argtypes = [_vp, _vp, _sz, _vp]
@@ -110,6 +150,8 @@ BI_ERR_UNSUPPORTED = 5
 BI_ERR_TIMEOUT = 6
 BI_ERR_CUDA = 7
 BI_FLAG_PDL = 1
+BI_ROPE_HALF = 0
+BI_ROPE_INTERLEAVED = 1
 
 
 class BiError(RuntimeError):
@@ -243,6 +285,123 @@ def bi_attention_verify(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, T0: i
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.bi_attention_verify(_ptr(q), _ptr(k), _ptr(v), M, Hq, Hkv, D, T0, S, scale, _ptr(o), _ptr(ws),
                                    nbytes, _stream(stream)), "bi_attention_verify")
+
+
+def bi_rmsnorm_quantize(h: torch.Tensor, y: torch.Tensor | None, w: torch.Tensor, eps: float,
+                        h_out: torch.Tensor | None, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0,
+                        stream=None) -> None:
+    """h, y: bf16 [M, >= K] (row strides h.stride(0), y.stride(0)); w: bf16 [K]; h_out: bf16 [M, >= K], given with y
+    (it may be h); q: int8 [M, K]; s_a: fp32 [M]."""
+    M, K = q.shape
+    _check(lib.bi_rmsnorm_quantize(h.data_ptr(), h.stride(0), _ptr(y), 0 if y is None else y.stride(0), w.data_ptr(), eps,
+                                   M, K, _ptr(h_out), 0 if h_out is None else h_out.stride(0), q.data_ptr(),
+                                   s_a.data_ptr(), flags, _stream(stream)), "bi_rmsnorm_quantize")
+
+
+def bi_kv4_block_bytes(page_size: int, D: int) -> int:
+    return int(lib.bi_kv4_block_bytes(page_size, D))
+
+
+def kv4_cache(pool: torch.Tensor, page_size: int, D: int) -> bi_kv4_cache:
+    """A cache over `pool`, uint8 [num_pages, Hkv, bi_kv4_block_bytes(page_size, D)] with any page stride (for
+    instance one layer of a pool of all layers).  The caller keeps the tensor alive."""
+    n, Hkv, block = pool.shape
+    assert pool.dtype == torch.uint8 and block == bi_kv4_block_bytes(page_size, D)
+    assert pool.stride(2) == 1 and pool.stride(1) == block
+    return bi_kv4_cache(pool.data_ptr(), pool.stride(0) if n > 1 else Hkv * block, n, page_size, Hkv, D)
+
+
+def new_kv4_pool(num_pages: int, Hkv: int, page_size: int, D: int, device="cuda") -> torch.Tensor:
+    """Device memory for a cache of num_pages pages."""
+    return torch.zeros((num_pages, Hkv, bi_kv4_block_bytes(page_size, D)), dtype=torch.uint8, device=device)
+
+
+def kv4_batch(cu_q: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, T: int, max_q: int,
+              max_kv: int) -> bi_kv4_batch:
+    """cu_q int32 [B + 1], kv_len int32 [B], pages int32 [B, n] (row stride pages.stride(0)); T, max_q, max_kv: bounds
+    known to the host.  The caller keeps the tensors alive."""
+    B = kv_len.shape[0]
+    assert cu_q.dtype == kv_len.dtype == pages.dtype == torch.int32
+    assert cu_q.shape[0] == B + 1 and cu_q.is_contiguous() and kv_len.is_contiguous()
+    assert pages.shape[0] == B and pages.is_contiguous()
+    return bi_kv4_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, T, max_q, max_kv)
+
+
+def bi_rope_table(inv_freq: torch.Tensor, rope: torch.Tensor, amp: float = 1.0, stream=None) -> None:
+    """inv_freq: fp64 [n]; rope: fp32 [positions, n, 2] out."""
+    assert inv_freq.dtype == torch.float64 and rope.dtype == torch.float32 and rope.is_contiguous()
+    assert rope.shape[1:] == (inv_freq.shape[0], 2)
+    _check(lib.bi_rope_table(_ptr(inv_freq), inv_freq.shape[0], amp, rope.shape[0], _ptr(rope), _stream(stream)),
+           "bi_rope_table")
+
+
+def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor, rot: int, layout: int,
+                       q_out: torch.Tensor, cache: bi_kv4_cache, batch: bi_kv4_batch, q_norm: torch.Tensor | None = None,
+                       k_norm: torch.Tensor | None = None, eps: float = 0.0, flags: int = 0, stream=None) -> None:
+    """q: bf16 [T, Hq, D], k, v: bf16 [T, Hkv, D] (row strides stride(0); parts of one packed tensor will do);
+    rope: fp32 [positions, rot / 2, 2]; q_norm, k_norm: bf16 [D] or None; q_out: bf16 [T, Hq, D]."""
+    _check(lib.bi_rope_append_kv4(q.data_ptr(), q.stride(0), q.shape[1], k.data_ptr(), k.stride(0), v.data_ptr(),
+                                  v.stride(0), _ptr(q_norm), _ptr(k_norm), eps, rope.data_ptr(), rope.shape[0], rot,
+                                  layout, q_out.data_ptr(), cache, batch, flags, _stream(stream)), "bi_rope_append_kv4")
+
+
+def bi_kv4_gather(cache: bi_kv4_cache, batch: bi_kv4_batch, k_out: torch.Tensor, v_out: torch.Tensor,
+                  stream=None) -> None:
+    """k_out, v_out: bf16 [T, Hkv, D], the cached values of the batch's token rows."""
+    _check(lib.bi_kv4_gather(cache, batch, k_out.data_ptr(), v_out.data_ptr(), _stream(stream)), "bi_kv4_gather")
+
+
+def bi_attention_kv4_workspace_size(Hq: int, cache: bi_kv4_cache, batch: bi_kv4_batch) -> int:
+    return int(lib.bi_attention_kv4_workspace_size(Hq, cache, batch))
+
+
+def new_attention_kv4_workspace(Hq: int, cache: bi_kv4_cache, batch: bi_kv4_batch, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for bi_attention_kv4 calls up to this size."""
+    return torch.zeros(bi_attention_kv4_workspace_size(Hq, cache, batch), dtype=torch.uint8, device=device)
+
+
+def bi_attention_kv4(q: torch.Tensor, cache: bi_kv4_cache, batch: bi_kv4_batch, scale: float, o: torch.Tensor,
+                     ws: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """q: bf16 [T, Hq, D] (row stride q.stride(0)); o: bf16 [T, Hq, D] out; ws: from new_attention_kv4_workspace."""
+    _check(lib.bi_attention_kv4(q.data_ptr(), q.stride(0), q.shape[1], cache, batch, scale, o.data_ptr(), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_attention_kv4")
+
+
+def logits_rules(ids: torch.Tensor | None = None, begin: torch.Tensor | None = None, mid: torch.Tensor | None = None,
+                 end: torch.Tensor | None = None, repetition: torch.Tensor | None = None,
+                 presence: torch.Tensor | None = None, frequency: torch.Tensor | None = None,
+                 bias_ids: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                 mask: torch.Tensor | None = None) -> bi_logits_rules:
+    """ids int32; begin, mid, end int32 [M]; repetition, presence, frequency fp32 [M]; bias_ids int32 [M, n] and bias
+    fp32 [M, n]; mask int32 words [M, >= ceil(V / 32)].  The caller keeps the tensors alive."""
+    for t in (ids, begin, mid, end, bias_ids, mask):
+        assert t is None or t.dtype == torch.int32
+    for t in (repetition, presence, frequency, bias):
+        assert t is None or t.dtype == torch.float32
+    for t in (ids, begin, mid, end, repetition, presence, frequency, bias_ids, bias):
+        assert t is None or t.is_contiguous()
+    n = 0 if bias_ids is None else bias_ids.shape[1]
+    return bi_logits_rules(_ptr(ids), _ptr(begin), _ptr(mid), _ptr(end), _ptr(repetition), _ptr(presence),
+                           _ptr(frequency), _ptr(bias_ids), _ptr(bias), n, _ptr(mask),
+                           0 if mask is None else max(mask.stride(0), mask.shape[1]))
+
+
+def bi_logits_workspace_size(M: int) -> int:
+    return int(lib.bi_logits_workspace_size(M))
+
+
+def new_logits_workspace(M: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for bi_logits_process on up to M rows."""
+    return torch.zeros(bi_logits_workspace_size(M), dtype=torch.uint8, device=device)
+
+
+def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.Tensor | None,
+                      argmax: torch.Tensor | None, ws: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """logits: bf16 [M, V] (row stride logits.stride(0)); out: fp32 [M, V] or None; argmax: int32 [M] or None."""
+    M, V = logits.shape
+    _check(lib.bi_logits_process(logits.data_ptr(), logits.stride(0), M, V, rules, _ptr(out),
+                                 0 if out is None else out.stride(0), _ptr(argmax), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_logits_process")
 
 
 def bi_probe_read(buf: torch.Tensor, out: torch.Tensor, stream=None) -> None:

@@ -22,22 +22,12 @@ using bi::host::aligned4;
 using bi::host::check_k;
 using bi::host::device_info;
 using bi::host::encode_int8_2d;
+using bi::host::from_cuda;
+using bi::host::overlaps;
 
 constexpr int kMaxAttnQueries = 4096;         // queries of one attention call
 constexpr int kMaxAttnPositions = 1 << 20;    // T0 + M: at most 4096 chunks (the merge stages 8 bytes a chunk)
 constexpr long long kMaxAttnRows = 65535LL * 32; // M * Hq / Hkv: 32-row blocks on one grid axis
-
-// [a, a + n) and [b, b + m) (bytes) share a byte
-bool overlaps(const void *a, size_t n, const void *b, size_t m)
-{
-    const char *pa = static_cast<const char *>(a), *pb = static_cast<const char *>(b);
-    return pa < pb + m && pb < pa + n;
-}
-
-bi_status from_cuda(cudaError_t e)
-{
-    return e == cudaSuccess ? BI_OK : BI_ERR_CUDA;
-}
 
 bi_status check_linear_args(const int8_t *q, const float *s_a, int M, int K, const int8_t *w_q, const float *s_w,
                             int N, void *ws, size_t ws_bytes)

@@ -20,6 +20,15 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// [a, a + n) and [b, b + m) (bytes) share a byte
+inline bool overlaps(const void *a, size_t n, const void *b, size_t m)
+{
+    const char *pa = static_cast<const char *>(a), *pb = static_cast<const char *>(b);
+    return pa < pb + m && pb < pa + n;
+}
+
+inline bi_status from_cuda(cudaError_t e) { return e == cudaSuccess ? BI_OK : BI_ERR_CUDA; }
+
 // K range shared by every entry point.
 inline bi_status check_k(int K)
 {

@@ -1,0 +1,144 @@
+// Residual addition, RMS norm and per-token int8 quantisation in one pass.
+//
+// t = h' w is exact in fp32 (two bf16 factors), and the codes rne(t / st),
+// st = max|t| / 127, are those of the normalised row t r for any r > 0: the
+// per-row absmax rule is invariant to a row's factor.  So the codes need no
+// rounding of r, and r enters the scale alone, s_a = st r.
+//
+// Bound: HBM; 7 bytes an element (h, y read; h', q written).  One CTA a row,
+// the row held in registers between the two reductions and the codes.
+#include "ptx.cuh"
+#include "row_ops.cuh"
+#include "step.cuh"
+
+namespace bi {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+
+__device__ __forceinline__ float2 block_sum_max(float s, float m, float2 *red)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[warp] = make_float2(s, m);
+    __syncthreads();
+    s = 0.0f;
+    m = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kNormThreads / 32; ++w) {
+        s = __fadd_rn(s, red[w].x);
+        m = fmaxf(m, red[w].y);
+    }
+    return make_float2(s, m);
+}
+
+// t = h w of 8 elements: adds their squares of h to s, their |t| to m.
+__device__ __forceinline__ void norm8(const uint4 &h, const uint4 &w, float (&t)[8], float &s, float &m)
+{
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w};
+    const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float x = bf16_lo(a[e]), y = bf16_hi(a[e]);
+        s = __fmaf_rn(x, x, s);
+        s = __fmaf_rn(y, y, s);
+        t[2 * e] = __fmul_rn(x, bf16_lo(b[e]));
+        t[2 * e + 1] = __fmul_rn(y, bf16_hi(b[e]));
+        m = fmaxf(m, fmaxf(fabsf(t[2 * e]), fabsf(t[2 * e + 1])));
+    }
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&t)[8], float st)
+{
+    uint32_t o[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e >> 2] |= code_byte(__fdiv_rn(t[e], st)) << (8 * (e & 3));
+    return make_uint2(o[0], o[1]);
+}
+
+__device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+// C chunks of 8 elements a thread in registers; C = 0: any K, the row read twice.
+template <int C>
+__global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(NormArgs a, int pdl)
+{
+    __shared__ float2 red[kNormThreads / 32];
+    if (pdl) {
+        pdl_launch_dependents();
+        pdl_wait();
+    }
+    const int64_t row = blockIdx.x;
+    const uint16_t *hr = a.h + row * a.ldh;
+    const uint16_t *yr = a.y ? a.y + row * a.ldy : nullptr;
+    const int K = a.K;
+    float s = 0.0f, m = 0.0f;
+    float t[C > 0 ? C : 1][8];
+    auto load = [&](int k) {
+        uint4 h = ldg16(hr + k);
+        return yr ? residual8(h, ldg16(yr + k)) : h;
+    };
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = (c * kNormThreads + threadIdx.x) * 8;
+            if (k < K) {
+                const uint4 h = load(k);
+                if (yr) *reinterpret_cast<uint4 *>(a.h_out + row * a.ldo + k) = h;
+                norm8(h, ldg16(a.w + k), t[c], s, m);
+            }
+        }
+    } else {
+        for (int k = threadIdx.x * 8; k < K; k += kNormThreads * 8) norm8(load(k), ldg16(a.w + k), t[0], s, m);
+    }
+    const float2 r = block_sum_max(s, m, red);
+    const float st = r.y == 0.0f ? 1.0f : __fdiv_rn(r.y, 127.0f);
+    int8_t *qr = a.q + row * K;
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = (c * kNormThreads + threadIdx.x) * 8;
+            if (k < K) *reinterpret_cast<uint2 *>(qr + k) = codes8(t[c], st);
+        }
+    } else {
+        for (int k = threadIdx.x * 8; k < K; k += kNormThreads * 8) {
+            const uint4 h = load(k);                  // h_out may be h: it is written after its last read
+            if (yr) *reinterpret_cast<uint4 *>(a.h_out + row * a.ldo + k) = h;
+            norm8(h, ldg16(a.w + k), t[0], s, m);
+            *reinterpret_cast<uint2 *>(qr + k) = codes8(t[0], st);
+        }
+    }
+    if (threadIdx.x == 0) {
+        const float rms = __fsqrt_rn(__fadd_rn(__fdiv_rn(r.x, static_cast<float>(K)), a.eps));
+        a.s_a[row] = r.y == 0.0f ? 1.0f : __fmul_rn(st, __fdiv_rn(1.0f, rms));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_quantize(const NormArgs &a, bool pdl, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.M));
+    cfg.blockDim = dim3(kNormThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    const int p = pdl ? 1 : 0;
+    switch ((a.K + kNormThreads * 8 - 1) / (kNormThreads * 8)) {
+    case 1: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<1>, a, p);
+    case 2: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<2>, a, p);
+    case 3: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<3>, a, p);
+    case 4: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<4>, a, p);
+    default: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<0>, a, p);
+    }
+}
+
+}  // namespace bi
