@@ -479,7 +479,7 @@ BI_API bi_status bi_kv4_gather(const bi_kv4_cache *cache, const bi_kv4_batch *ba
  * A token that sees no position (a sequence of length 0) has o = 0.
  *   q  bf16, row t at q + t ldq, head h at h D (ldq >= Hq D, a multiple of 8)
  *   o  bf16 [T, Hq, D] out, must not overlap q
- *   scale  positive and finite
+ *   scale  positive and finite;  max_q * (Hq / Hkv) <= 2^22
  *   ws  workspace of at least bi_attention_kv4_workspace_size(...) bytes,
  *       16-byte aligned, zero-filled before its first use; every call that
  *       completes leaves it ready for the next.  Its layout depends on no

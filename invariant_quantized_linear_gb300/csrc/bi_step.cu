@@ -19,6 +19,7 @@ using bi::host::overlaps;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxPositions = 1 << 22;
+constexpr int kMaxAttnRows = 1 << 22;   // query rows of a sequence and kv head
 constexpr int kMaxVocab = 1 << 24;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -211,7 +212,7 @@ size_t bi_attention_kv4_workspace_size(int Hq, const bi_kv4_cache *cache, const 
         !head_size_ok(cache->D) || batch->B < 1 || batch->B > 65535 || batch->T < 1 || batch->T > kMaxTokens ||
         batch->max_q < 1 || batch->max_q > 65535 || batch->max_kv < 1 || batch->max_kv > kMaxPositions)
         return 0;
-    return bi::attention_kv4_workspace(Hq, cache->Hkv, cache->D, batch->B, batch->T, batch->max_q, batch->max_kv);
+    return bi::attention_kv4_workspace(Hq, cache->D, batch->T, batch->max_kv);
 }
 
 bi_status bi_attention_kv4(const uint16_t *q, int64_t ldq, int Hq, const bi_kv4_cache *cache, const bi_kv4_batch *batch,
@@ -222,6 +223,7 @@ bi_status bi_attention_kv4(const uint16_t *q, int64_t ldq, int Hq, const bi_kv4_
     st = check_batch(batch);
     if (st != BI_OK) return st;
     const int64_t wq = static_cast<int64_t>(Hq) * cache->D;
+    if (static_cast<int64_t>(batch->max_q) * (Hq / cache->Hkv) > kMaxAttnRows) return BI_ERR_INVALID_ARG;
     if (!q || !o || Hq < 1 || Hq > kMaxHeads || Hq % cache->Hkv != 0 || ldq < wq || !(scale > 0.0f) ||
         !finite_at_least(scale, 0.0f))
         return BI_ERR_INVALID_ARG;

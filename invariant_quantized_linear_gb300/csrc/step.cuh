@@ -75,7 +75,7 @@ struct AttnKv4Args {
     int sms;
 };
 
-size_t attention_kv4_workspace(int Hq, int Hkv, int D, int B, int T, int max_q, int max_kv);
+size_t attention_kv4_workspace(int Hq, int D, int T, int max_kv);
 cudaError_t launch_attention_kv4(const AttnKv4Args &a, int D, bool pdl, cudaStream_t stream);
 
 struct LogitsArgs {

@@ -503,3 +503,20 @@ def test_logits(bi, M, V, ldl, ldo, kind):
         if want_am:
             same(host(am), best, "argmax")
     assert not ws.any()
+
+
+def test_attention_leaves_out_tokens_past_the_bound(bi):
+    """Tokens past max_q have zeros, those before it their result, also where T does not show that there are any."""
+    rng = np.random.default_rng(12)
+    seqs, Hq, Hkv, D, P = [(6, 1500), (0, 9), (1, 40)], 4, 2, 64, 32
+    b = Batch(bi, seqs, Hkv, D, P)
+    b.fill(0, *kv(rng, seqs, Hkv, D))
+    b.to_device()
+    q = bits(rng, (b.T, Hq, D))
+    whole = attend(bi, b, q, 0.1)
+    b.batch = bi.kv4_batch(*b.d, b.T, 3, b.max_kv)
+    o = attend(bi, b, q, 0.1)
+    assert torch.equal(o[:3], whole[:3]) and torch.equal(o[6], whole[6]) and not o[3:6].any()
+    b.batch = bi.kv4_batch(*b.d, 5, 6, b.max_kv)              # rows from T on are not touched
+    o = attend(bi, b, q, 0.1)
+    assert torch.equal(o[:5], whole[:5]) and (o[5:] == 7).all()
