@@ -27,18 +27,23 @@
 // be much larger than the value.  A group without a scale (all its elements
 // equal) has codes 0 and takes |z| / 8 in its place.
 //
-// Work: positions are cut into blocks of 64, chunks of 4 blocks and spans of 4
-// chunks, counted from position 0.  A block's result (maximum, sum, weighted
-// values) comes from one warp; a chunk folds its blocks in order, a span joins
-// its chunks' results under their common maximum, and a row joins its spans the
-// same way.  A row's result is this tree whatever else is in the call, since
-// neither maxima nor scales look at a position that the row does not see; which
-// warp computes what may therefore go by the size of the call:
-//   4 warps a CTA, a chunk each, the fold in registers: least work a position,
+// Both rank-one terms are products for the tensor cores too, one a tile and
+// group: z (bf16 as it stands in the cache) with sum(q) in three bf16 parts,
+// and the weights with z / s in two f16 parts, as two more rows of V^T.
+//
+// Work: positions are cut into blocks of 64 and spans of 32 blocks, counted from
+// position 0; every fourth block of a span makes a chunk.  A block's result
+// (maximum, sum, weighted values) comes from one warp; a chunk folds its blocks
+// in order, a span joins its four chunks' results under their common maximum,
+// and a row joins its spans the same way.  A row's result is this tree whatever
+// else is in the call, since neither maxima nor scales look at a position that
+// the row does not see; which warp computes what may therefore go by the size
+// of the call:
+//   a span a CTA, a chunk a warp, the fold in registers: least work a position,
 //     four CTAs a SM overlap one another's latencies;
-//   16 warps a CTA, a block each, the fold through shared memory: for calls
-//     of few CTAs, where a chunk's four blocks one after the other would be
-//     most of the time.
+//   a span a cluster of 8 CTAs, a block a warp, the fold over the cluster's
+//     shared memory: for calls that leave SMs idle, where a chunk's eight
+//     blocks one after the other would be most of the time.
 // The CTA that finishes a row block's last span joins the spans (a counter in
 // the workspace); a second launch does where a row has many spans or the
 // counters do not suffice.
@@ -53,15 +58,17 @@ namespace bi {
 namespace {
 
 constexpr int kBlock = 64;                          // positions of a block
-constexpr int kChunkBlocks = 4;
+constexpr int kChunkBlocks = 8;
 constexpr int kChunks = 4;                          // chunks of a span
 constexpr int kSpan = kBlock * kChunkBlocks * kChunks;
 constexpr int kTiles = kBlock / 16;
+constexpr int kThreads = 32 * kChunks;
+constexpr int kCluster = kChunkBlocks;              // CTAs that share a span
 constexpr int kMinExp = -100;                       // least exponent that value scales are normalised to
 constexpr int kMaxExp = 118;                        // largest that is undone again within fp32
 constexpr float kMinScale = 0x1p-110f;              // groups of smaller scale count as zeros
 constexpr int kCounters = 16384;                    // row blocks whose spans are counted in the workspace
-constexpr int kJoinSpans = 64;                      // spans that a CTA joins itself at most
+constexpr int kJoinSpans = 16;                      // spans that a CTA joins itself at most, and a run of the second launch
 constexpr size_t kCounterBytes = kCounters * sizeof(int);
 
 __device__ __forceinline__ float ex2(float x)
@@ -71,13 +78,15 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// BYTES bytes to shared memory, or zeros where `there` is false (the address is not read then).
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t smem, const void *gmem)
+__device__ __forceinline__ void cp_async(uint32_t smem, const void *gmem, bool there)
 {
+    const int n = there ? BYTES : 0;
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem), "l"(gmem) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "r"(n) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem), "l"(gmem) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(smem), "l"(gmem), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
@@ -142,29 +151,38 @@ __device__ __forceinline__ void code_operands(uint32_t w, uint32_t (&o)[4])
 
 __device__ __forceinline__ float pow2_int(int e) { return __int_as_float((e + 127) << 23); }   // -126 .. 127
 
-// Shared memory of a CTA of WARPS warps for head size D and NB blocks of 8 query rows.
-template <int D, int NB, int WARPS>
+// Shared memory of a CTA for head size D and NB blocks of 8 query rows.
+template <int D, int NB, bool SPLIT>
 struct Plan {
+    static constexpr int kBlocks = SPLIT ? 1 : kChunkBlocks;   // blocks of a warp
     static constexpr int G = D / kKv4Group;
     static constexpr int R = 8 * NB;                       // query rows
     static constexpr int kPiece = D / 8;                   // bytes of a lane's share of 8 positions (16 or 8)
     static constexpr int kCodes = 8 * 32 * kPiece;         // 64 positions of keys (or values)
     static constexpr int kPar = kBlock * 8 * G;            // their parameters
-    static constexpr int kPrep = kBlock * 8 * G;           // value scales and z / s of the block, fp32
-    static constexpr int kWarp = 2 * kCodes + 2 * kPar + kPrep;   // parameters of two blocks
+    static constexpr int kScale = kBlock * 4 * G;          // value scales of the block, fp32 [position][group]
+    static constexpr int kRatio = kBlock * 4 * G;          // their z / s, two f16 parts [tile][group][part][16 positions]
+    static constexpr int kZero = 16 * 2;                   // zeros for the rows of V^T that are not there
+    static constexpr int kWarp = 2 * kCodes + 2 * kPar + kScale + kRatio + kZero;   // parameters of two blocks
     static constexpr int kQRow = 2 * D + 8;                // bytes of a query row in f16; the 8 spread the banks
-    static constexpr int kO = R * D * 4;                   // a warp's weighted values take the place of its codes
-    static constexpr int kLZ = 32 * 2 * NB * (1 + G) * 4;  // and behind them its lanes' sums (16-warp form)
-    static constexpr int kQ = WARPS * kWarp;
-    static constexpr int kT = kQ + R * kQRow;              // sums of q per row and group
-    static constexpr int kF = kT + R * G * 4;              // factor per row
+    static constexpr int kO = R * D * 4;                   // a result's values; they take the place of the warp's codes
+    static constexpr int kLZ = 32 * 2 * NB * (1 + G) * 4;  // and, in a cluster, its sums lane by lane
+    static constexpr int kResult = kO + (SPLIT ? kLZ : 0);
+    static constexpr int kQ = kChunks * kWarp;
+    static constexpr int kT = kQ + R * kQRow;              // sums of q per row: 8 bf16, three parts a group, then zeros
+    static constexpr int kF = kT + R * 16;                 // factor per row
     static constexpr int kN = kF + R * 4;                  // positions that a row sees
     static constexpr int kM = kN + R * 4;                  // maxima [warp][row]
-    static constexpr int kL = kM + WARPS * R * 4;          // sums [chunk][row]
-    static constexpr int kZ = kL + kChunks * R * 4;        // weighted minima [chunk][row][group] (16-warp form)
-    static constexpr int kFlag = kZ + kChunks * R * G * 4;
+    static constexpr int kL = kM + kChunks * R * 4;        // sums [chunk][row]
+    // in a cluster: the chunks' maxima and weighted minima, weights of the folds [chunk][block][row], chunks' values
+    static constexpr int kC = kL + kChunks * R * 4;
+    static constexpr int kZ = kC + (SPLIT ? kChunks * R * 4 : 0);
+    static constexpr int kFold = kZ + (SPLIT ? kChunks * R * G * 4 : 0);
+    static constexpr int kV = kFold + (SPLIT ? kChunks * kChunkBlocks * R * 8 : 0);
+    static constexpr int kFlag = kV + (SPLIT ? kO / 8 * kChunks : 0);
     static constexpr int kBytes = kFlag + 16;
-    static_assert(kO + kLZ <= kWarp, "a warp's results fit in the place of its codes");
+    static_assert(R * D / 4 / kCluster % (D / 4) == 0, "a CTA of a cluster joins whole rows");
+    static_assert(kResult <= kWarp && kV % 16 == 0 && kFold % 16 == 0, "a warp's results fit in the place of its codes");
 };
 
 template <int BYTES>
@@ -179,13 +197,30 @@ __device__ __forceinline__ void lds_words(const unsigned char *p, uint32_t (&w)[
     }
 }
 
-// D = A(16x16) B(16x8) + D in f16 with fp32 sums; not volatile, so that independent chains may interleave.
+// D = A(16x16) B(16x8) + C in f16 with fp32 sums; not volatile, so that independent chains may interleave.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The first of a chain: C = 0.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// D = A(16x8) B(8x8) in bf16.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
 }
 
 // The rows of a CTA: query rows r0 .. r_last of one kv head, row r = (token r / GH of the sequence, head r % GH).
@@ -204,55 +239,95 @@ __device__ __forceinline__ int row_positions(const AttnKv4Args &a, const Rows &w
 // Query rows to shared memory: f16 elements scaled by a power of two, odd
 // element pairs divided by 16; the sums and the factor that turn products with
 // codes into scores in units of log2.
-template <int D, int NB, int WARPS>
+template <int D, int NB, bool SPLIT>
 __device__ __forceinline__ void stage_queries(const AttnKv4Args &a, unsigned char *smem, const Rows &rows)
 {
-    using P = Plan<D, NB, WARPS>;
-    constexpr int E = D / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int rl = warp; rl < P::R; rl += WARPS) {
-        const int r = rows.r0 + rl, tok = rows.token(min(r, rows.r_last));
-        uint32_t w[E / 2] = {};
-        if (r <= rows.r_last) {
-            const uint16_t *src = a.q + (rows.t0 + tok) * a.ldq + (rows.hk * rows.GH + r - tok * rows.GH) * D + lane * E;
+    using P = Plan<D, NB, SPLIT>;
+    // all rows at once: L lanes a row, E elements a lane
+    constexpr int L = kThreads / P::R, E = D / L;
+    const int rl = threadIdx.x / L, at = threadIdx.x % L * E;
+    const int r = rows.r0 + rl, tok = rows.token(min(r, rows.r_last));
+    uint32_t w[E / 2] = {};
+    if (r <= rows.r_last) {                                // idle rows are zeros
+        const uint16_t *src = a.q + (rows.t0 + tok) * a.ldq + (rows.hk * rows.GH + r - tok * rows.GH) * D + at;
+        if constexpr (E == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(src);
+            w[0] = v.x, w[1] = v.y;
+        } else {
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e) w[e] = *reinterpret_cast<const uint32_t *>(src + 2 * e);
+            for (int e = 0; e < E / 8; ++e) {
+                const uint4 v = reinterpret_cast<const uint4 *>(src)[e];
+                w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+            }
         }
-        float x[E], top = 0.0f;
+    }
+    float x[E], top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            x[e] = e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
-            top = fmaxf(top, fabsf(x[e]));
+    for (int e = 0; e < E; ++e) {
+        x[e] = e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+        top = fmaxf(top, fabsf(x[e]));
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // up = 2^(14 - floor(log2 top)), kept in fp32's range
+    const int ex = max(-100, min(127, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+    const float up = pow2_int(14 - ex);
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        x[e] *= up;
+        sum += x[e];
+    }
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e) {                      // a lane's elements begin with an even pair
+        const __half2 h0 = __floats2half2_rn(x[4 * e], x[4 * e + 1]),
+                      h1 = __floats2half2_rn(x[4 * e + 2] * 0.0625f, x[4 * e + 3] * 0.0625f);
+        *reinterpret_cast<uint2 *>(smem + P::kQ + rl * P::kQRow + (at + 4 * e) * 2) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+    }
+#pragma unroll
+    for (int o = kKv4Group / E / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (at % kKv4Group == 0) {
+        // three parts of 8 bits: all 24 of the sum
+        uint16_t *dst = reinterpret_cast<uint16_t *>(smem + P::kT + rl * 16) + 3 * (at / kKv4Group);
+        float rest = sum * 0x1p-24f;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const uint32_t part = bf16_rne_bits(rest);
+            dst[i] = static_cast<uint16_t>(part);
+            rest -= __uint_as_float(part << 16);
         }
+        if (at == 0) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // up = 2^(14 - floor(log2 top)), kept in fp32's range
-        const int ex = max(-100, min(127, static_cast<int>(__float_as_uint(top) >> 23) - 127));
-        const float up = pow2_int(14 - ex);
-        float sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            x[e] *= up;
-            sum += x[e];
-        }
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-            const float f = (lane * E / 2 + e) % 2 ? 0.0625f : 1.0f;
-            const __half2 h = __floats2half2_rn(x[2 * e] * f, x[2 * e + 1] * f);
-            *reinterpret_cast<__half2 *>(smem + P::kQ + rl * P::kQRow + (lane * E + 2 * e) * 2) = h;
-        }
-#pragma unroll
-        for (int o = 16 / P::G; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane % (32 / P::G) == 0)
-            *reinterpret_cast<float *>(smem + P::kT + (rl * P::G + lane / (32 / P::G)) * 4) = sum * 0x1p-24f;
-        if (lane == 0) {
-            // scores = factor * (products with 2^-24 c and up q); idle rows go with the last
+            for (int i = 3 * P::G; i < 8; ++i) dst[i] = 0;
+            // scores = factor * (products with 2^-24 c and up q)
             *reinterpret_cast<float *>(smem + P::kF + rl * 4) =
                 fmaxf(fminf(a.scale * 1.4426950408889634f * 0x1p10f * pow2_int(ex), 0x1p126f), 0x1p-126f);
             *reinterpret_cast<int *>(smem + P::kN + rl * 4) = min(a.c.max_kv, rows.first + tok + 1);
         }
     }
 }
+
+__device__ __forceinline__ unsigned long long ld_cluster_b64(uint32_t addr)
+{
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// The two halves of a cluster barrier: everything before the arrival is done for those who have waited.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The fold of a block's result into a chunk's: weights of the two sides.
 __device__ __forceinline__ float fold_weights(float m, float mb, float &wa, float &wb)
@@ -272,18 +347,14 @@ __device__ __forceinline__ void write_out(const AttnKv4Args &a, int64_t at, int 
         make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
 }
 
-// A row's spans joined in order, 4 elements at d; part: the row's span results (D + 4 floats each: maximum, sum, values from 4 on).
+// Adds spans first .. end - 1 of a row in order, 4 elements at d, under the
+// row's maximum; part: the row's span results (D + 4 floats each: maximum, sum,
+// values from 4 on).
 template <int D>
-__device__ __forceinline__ void join_spans(const float *part, int n, int d, float4 &v, float &sum)
+__device__ __forceinline__ void add_spans(const float *part, int first, int end, float top, int d, float4 &v, float &sum)
 {
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg(part + static_cast<int64_t>(c) * (D + 4)));
-    sum = 0.0f;
-    v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (top == -INFINITY) return;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
+#pragma unroll 8
+    for (int c = first; c < end; ++c) {
         const float *pc = part + static_cast<int64_t>(c) * (D + 4);
         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pc));
         const float4 x = __ldcg(reinterpret_cast<const float4 *>(pc + 4 + d));
@@ -304,24 +375,26 @@ struct SpanArgs {
     int pdl;
 };
 
-template <int D, int NB, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3 : 4)) attn_kv4_span_kernel(SpanArgs p)
+template <int D, int NB, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_kernel(SpanArgs p)
 {
-    constexpr int WARPS = WIDE ? kChunks * kChunkBlocks : kChunks;
-    constexpr int BLOCKS = WIDE ? 1 : kChunkBlocks;       // a warp's blocks
-    using P = Plan<D, NB, WARPS>;
-    constexpr int G = P::G, W = P::kPiece / 4;
+    using P = Plan<D, NB, SPLIT>;
+    constexpr int G = P::G, W = P::kPiece / 4, BLOCKS = P::kBlocks;
     extern __shared__ __align__(16) unsigned char smem[];
     const AttnKv4Args &a = p.a;
     const Kv4View &c = a.c;
-    const int span = blockIdx.x / p.row_blocks, rb = blockIdx.x - span * p.row_blocks, b = blockIdx.z;
+    const int rank = SPLIT ? blockIdx.x % kCluster : 0, task = SPLIT ? blockIdx.x / kCluster : blockIdx.x;
+    const int span = task / p.row_blocks, rb = task - span * p.row_blocks, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (p.pdl) pdl_wait();
     pdl_launch_dependents();
 
-    // pages of the warp's positions, 16 a lane; the lengths are on their way meanwhile
-    const int p0 = span * kSpan, pw = p0 + warp * (BLOCKS * kBlock);
-    int pages = lane < BLOCKS * 4 ? kv4_page(c, b, pw + 16 * lane) : -1;
+    // the warp's blocks are 4 rank + warp and every fourth after it; lane 4 j + i looks after positions 16 i .. of the
+    // j-th: their page (the lengths are on their way meanwhile)
+    const int p0 = span * kSpan, pw = p0 + (rank * kChunks + warp) * kBlock;
+    constexpr int kStep = kChunks * kBlock;
+    const int my_pos = pw + (lane >> 2) * kStep + 16 * (lane & 3);
+    int page = lane < BLOCKS * 4 ? kv4_page(c, b, my_pos) : -1;
     const int cu0 = __ldg(c.cu_q + b), cu1 = __ldg(c.cu_q + b + 1), len = __ldg(c.kv_len + b);
     Rows rows;
     rows.t0 = max(0, cu0);
@@ -331,9 +404,9 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
     rows.r0 = rb * P::R;
     rows.first = len - (cu1 - cu0);                       // position of the first new token
     const int tokens = min(c.T, cu1) - rows.t0, n_rows = min(tokens, c.max_q) * rows.GH;
-    if (blockIdx.x == 0)                                  // tokens past max_q are left out: zeros
+    if (task == 0 && rank == 0)                           // tokens past max_q are left out: zeros
         for (int64_t i = static_cast<int64_t>(c.max_q) * rows.GH * (D / 4) + threadIdx.x;
-             i < static_cast<int64_t>(tokens) * rows.GH * (D / 4); i += 32 * WARPS) {
+             i < static_cast<int64_t>(tokens) * rows.GH * (D / 4); i += kThreads) {
             const int64_t r = i / (D / 4), tok = r / rows.GH;
             write_out<D>(a, (rows.t0 + tok) * a.Hq + rows.hk * rows.GH + r - tok * rows.GH, static_cast<int>(i % (D / 4)) * 4,
                          make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
@@ -342,45 +415,78 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
     rows.r_last = min(n_rows, rows.r0 + P::R) - 1;
     const int n_most = row_positions(a, rows, rows.r_last), n_least = row_positions(a, rows, rows.r0);
     if (p0 >= n_most && (span > 0 || n_most > 0)) return;
-    if (pw + 16 * lane >= n_most) pages = -1;
+    if (my_pos >= n_most) page = -1;
+    const unsigned pages = __ballot_sync(0xffffffffu, page >= 0);
 
     unsigned char *mine = smem + warp * P::kWarp;
     const uint32_t my = smem_u32(mine);
     const int PS = 1 << c.page_shift;
-    const int64_t head = static_cast<int64_t>(rows.hk) * Kv4Layout::block(PS, D);
-    // copies of a block's keys and parameters, or of its values; pages that are not there are left out
+    // this lane's 16 positions: where their codes begin in the page's block of the kv head, and the page's block
+    const int slot = my_pos & (PS - 1);
+    const unsigned char *block = kv4_block<D>(c, max(page, 0), rows.hk);
+    const unsigned long long codes = reinterpret_cast<unsigned long long>(block + slot * Kv4Layout::k_row(D));
+    const int v_off = Kv4Layout::v_off(PS, D) + t * Kv4Layout::v_pair(D) + g * P::kPiece, k_off = lane * P::kPiece;
+    // parameters begin p_off(PS) - slot (k_row - p_row) after the codes
+    const int par_off = Kv4Layout::p_off(PS, D) - slot * (Kv4Layout::k_row(D) - Kv4Layout::p_row(D));
+    const bool long_pages = PS >= kBlock;                  // then a block lies in one page
+    // copies of a block's keys and parameters, or of its values; zeros for pages that are not there
     auto copy_keys = [&](int blk) {
+        const uint32_t par = my + 2 * P::kCodes + (blk & 1) * P::kPar;
+        if (long_pages) {
+            const bool there = (pages >> (4 * blk)) & 1u;
+            const unsigned char *src = reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk));
+            const int po = __shfl_sync(0xffffffffu, par_off, 4 * blk);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int page = __shfl_sync(0xffffffffu, pages, blk * 4 + i), slot = (pw + blk * kBlock + 16 * i) & (PS - 1);
-            if (page >= 0) {
-                const unsigned char *src = c.pool + page * c.page_stride + head;
-                cp_async<P::kPiece>(my + (64 * i + lane) * P::kPiece, src + slot * Kv4Layout::k_row(D) + lane * P::kPiece);
-                cp_async<P::kPiece>(my + (64 * i + 32 + lane) * P::kPiece,
-                                    src + slot * Kv4Layout::k_row(D) + (32 + lane) * P::kPiece);
-                if (lane < 16)
-                    cp_async<8 * G>(my + 2 * P::kCodes + (blk & 1) * P::kPar + (16 * i + lane) * 8 * G,
-                                    src + Kv4Layout::p_off(PS, D) + (slot + lane) * Kv4Layout::p_row(D));
+            for (int i = 0; i < 8; ++i)
+                cp_async<P::kPiece>(my + (32 * i + lane) * P::kPiece, src + k_off + i * 32 * P::kPiece, there);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                cp_async<8 * G>(par + (32 * i + lane) * 8 * G, src + po + (32 * i + lane) * 8 * G, there);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool there = (pages >> (4 * blk + i)) & 1u;
+                const unsigned char *src =
+                    reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk + i));
+                const int po = __shfl_sync(0xffffffffu, par_off, 4 * blk + i);
+                cp_async<P::kPiece>(my + (64 * i + lane) * P::kPiece, src + k_off, there);
+                cp_async<P::kPiece>(my + (64 * i + 32 + lane) * P::kPiece, src + k_off + 32 * P::kPiece, there);
+                if (lane < 16) cp_async<8 * G>(par + (16 * i + lane) * 8 * G, src + po + lane * 8 * G, there);
             }
         }
         cp_commit();
     };
     auto copy_values = [&](int blk) {
+        if (long_pages) {
+            const bool there = (pages >> (4 * blk)) & 1u;
+            const unsigned char *src = reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int page = __shfl_sync(0xffffffffu, pages, blk * 4 + i), slot = (pw + blk * kBlock + 16 * i) & (PS - 1);
-            if (page >= 0) {
-                const unsigned char *src = c.pool + page * c.page_stride + head + Kv4Layout::v_off(PS, D) +
-                                           (slot / 2 + t) * Kv4Layout::v_pair(D) + g * P::kPiece;
-                cp_async<P::kPiece>(my + P::kCodes + (64 * i + lane) * P::kPiece, src);
-                cp_async<P::kPiece>(my + P::kCodes + (64 * i + 32 + lane) * P::kPiece, src + 4 * Kv4Layout::v_pair(D));
+            for (int i = 0; i < 8; ++i)
+                cp_async<P::kPiece>(my + P::kCodes + (32 * i + lane) * P::kPiece, src + v_off + i * 4 * Kv4Layout::v_pair(D),
+                                    there);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool there = (pages >> (4 * blk + i)) & 1u;
+                const unsigned char *src =
+                    reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk + i));
+                cp_async<P::kPiece>(my + P::kCodes + (64 * i + lane) * P::kPiece, src + v_off, there);
+                cp_async<P::kPiece>(my + P::kCodes + (64 * i + 32 + lane) * P::kPiece,
+                                    src + v_off + 4 * Kv4Layout::v_pair(D), there);
             }
         }
         cp_commit();
     };
     copy_keys(0);
     copy_values(0);
-    stage_queries<D, NB, WARPS>(a, smem, rows);
+    stage_queries<D, NB, SPLIT>(a, smem, rows);
+    unsigned char *scale = mine + 2 * P::kCodes + 2 * P::kPar, *ratio = scale + P::kScale;
+    if (lane < 8) *reinterpret_cast<uint32_t *>(ratio + P::kRatio + 4 * lane) = 0;
+    // this lane's part of z / s as rows of V^T: row 0 the first parts, row 1 the second, no others
+    const unsigned char *my_ratio = g < 2 ? ratio + g * 32 + t * 8 : ratio + P::kRatio + t * 8;
+    const int ratio_step = g < 2 ? 64 : 0;
+    // bytes of two parameter words for the rows of K's minima: parts of group 0 in columns 0-2, of group 1 in 3-5
+    const uint32_t pick = G == 1 ? 0x3232u : t == 0 ? 0x3232u : t == 1 ? 0x7632u : 0x7676u;
     __syncthreads();
 
     // this lane's columns: rows 8 nb + 2 t + i of the row block
@@ -401,31 +507,76 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
 
 #pragma unroll 1
     for (int blk = 0; blk < BLOCKS; ++blk) {
-        const int pb = pw + blk * kBlock;
+        const int pb = pw + blk * kStep;
         if (pb >= n_most) break;
-        const bool more = blk + 1 < BLOCKS && pb + kBlock < n_most;
+        const bool more = blk + 1 < BLOCKS && pb + kStep < n_most;
         // bit i: positions 16 i .. of the block are on a page; full: and every row sees the whole block
-        const unsigned there = (__ballot_sync(0xffffffffu, pages >= 0) >> (4 * blk)) & 15u;
+        const unsigned there = (pages >> (4 * blk)) & 15u;
         const bool full = there == 15u && pb + kBlock <= n_least;
         cp_wait<1>();
         __syncwarp();
         const unsigned char *par = mine + 2 * P::kCodes + (blk & 1) * P::kPar;
 
+        // ---- the values' scales and z / s, two positions a lane; nothing for positions that no row sees
+        uint32_t top_scale = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int y = lane + 32 * i;
+            uint32_t w[2 * G];
+            lds_words<8 * G>(par + y * 8 * G, w);
+            const bool seen = ((there >> (y >> 4)) & 1u) && pb + y < n_most;
+            // position y of tile y / 16 is element 2 t + (i & 1) + 8 (i / 2) of its rows, kept as 4 t + i
+            const int at = (y & 6) * 2 + (y & 1) + (y & 8) / 4;
+            float sv[G];
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                const float zv = bf16_hi(w[G + k]);
+                const float v = w[G + k] & 0x7FFFu ? bf16_lo(w[G + k]) : 0.125f * fabsf(zv);
+                const bool some = seen && v >= kMinScale;
+                sv[k] = some ? v : 0.0f;
+                const float r = some ? __fdividef(zv, v) : 0.0f;
+                const __half hi = __float2half_rn(r), lo = __float2half_rn(r - __half2float(hi));
+                __half *dst = reinterpret_cast<__half *>(ratio + ((y >> 4) * G + k) * 64) + at;
+                dst[0] = hi;
+                dst[16] = lo;
+                top_scale = max(top_scale, __float_as_uint(sv[k]));
+            }
+            if constexpr (G == 2)
+                *reinterpret_cast<float2 *>(scale + y * 8) = make_float2(sv[0], sv[G - 1]);
+            else
+                *reinterpret_cast<float *>(scale + y * 4) = sv[0];
+        }
+
         // ---- scores: the tiles' chains of products side by side
         float s[kTiles][NB][4];
         {
-            uint32_t kw[2 * kTiles][W];
+            uint32_t kw[2 * kTiles][W], kp[kTiles][2][G];    // codes; key parameters of positions g and g + 8 of a tile
 #pragma unroll
             for (int i = 0; i < 2 * kTiles; ++i) lds_words<P::kPiece>(mine + (i * 32 + lane) * P::kPiece, kw[i]);
+            uint32_t tq[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) tq[nb] = *reinterpret_cast<const uint32_t *>(smem + P::kT + (8 * nb + g) * 16 + 4 * t);
+#pragma unroll
+            for (int tile = 0; tile < kTiles; ++tile) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const unsigned char *src = par + (16 * tile + 8 * half + g) * 8 * G;
+                    if constexpr (G == 2) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                        kp[tile][half][0] = v.x;
+                        kp[tile][half][G - 1] = v.y;
+                    } else {
+                        kp[tile][half][0] = *reinterpret_cast<const uint32_t *>(src);
+                    }
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    mma_bf16(s[tile][nb], __byte_perm(kp[tile][0][0], kp[tile][0][G - 1], pick),
+                             __byte_perm(kp[tile][1][0], kp[tile][1][G - 1], pick), tq[nb]);
+            }
 #pragma unroll
             for (int k = 0; k < G; ++k) {
                 float acc[kTiles][NB][4];
-#pragma unroll
-                for (int tile = 0; tile < kTiles; ++tile)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[tile][nb][i] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -441,29 +592,22 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
                             code_operands(kw[2 * tile + 1][2 * k + j], x1);
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb)
-                                mma(acc[tile][nb], x0[2 * h], x1[2 * h], x0[2 * h + 1], x1[2 * h + 1], q[nb][0], q[nb][1]);
+                                if (j == 0 && h == 0)
+                                    mma_first(acc[tile][nb], x0[0], x1[0], x0[1], x1[1], q[nb][0], q[nb][1]);
+                                else
+                                    mma(acc[tile][nb], x0[2 * h], x1[2 * h], x0[2 * h + 1], x1[2 * h + 1], q[nb][0], q[nb][1]);
                         }
                     }
-                f2 tq[NB];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-                    tq[nb] = pk(*reinterpret_cast<const float *>(smem + P::kT + ((8 * nb + 2 * t) * G + k) * 4),
-                                *reinterpret_cast<const float *>(smem + P::kT + ((8 * nb + 2 * t + 1) * G + k) * 4));
 #pragma unroll
                 for (int tile = 0; tile < kTiles; ++tile)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const uint32_t w =
-                            *reinterpret_cast<const uint32_t *>(par + (16 * tile + 8 * half + g) * 8 * G + 4 * k);
-                        const f2 sk = pk(bf16_lo(w), bf16_lo(w)), zk = pk(bf16_hi(w), bf16_hi(w));
+                        const float sk = __uint_as_float(kp[tile][half][k] << 16);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            float *x = &s[tile][nb][2 * half];
-                            const f2 u = fma2(zk, tq[nb], k ? pk(x[0], x[1]) : 0ull);
-                            const float2 r = upk(fma2(sk, pk(acc[tile][nb][2 * half], acc[tile][nb][2 * half + 1]), u));
-                            x[0] = r.x;
-                            x[1] = r.y;
-                        }
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                s[tile][nb][2 * half + i] = __fmaf_rn(sk, acc[tile][nb][2 * half + i], s[tile][nb][2 * half + i]);
                     }
             }
         }
@@ -486,38 +630,12 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
         if (more) copy_keys(blk + 1);
         else cp_commit();
 
-        // ---- the values' scales and z / s, two positions a lane; nothing for positions that no row sees
-        unsigned char *prep = mine + 2 * P::kCodes + 2 * P::kPar;
-        int e_all = kMinExp;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int x = lane + 32 * i;
-            uint32_t w[2 * G];
-            lds_words<8 * G>(par + x * 8 * G, w);
-            const bool seen = ((there >> (x >> 4)) & 1u) && pb + x < n_most;
-            float out[2 * G];
-#pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const float zv = bf16_hi(w[G + k]);
-                float sv = bf16_lo(w[G + k]);
-                sv = sv > 0.0f ? sv : 0.125f * fabsf(zv);
-                const bool some = seen && sv >= kMinScale;
-                out[2 * k] = some ? sv : 0.0f;
-                out[2 * k + 1] = some ? __fdividef(zv, sv) : 0.0f;
-                e_all = max(e_all, static_cast<int>(__float_as_uint(out[2 * k]) >> 23) - 126);   // out < 2^e
-            }
-            if constexpr (G == 2)
-                *reinterpret_cast<float4 *>(prep + x * 16) = make_float4(out[0], out[1], out[2], out[3]);
-            else
-                *reinterpret_cast<float2 *>(prep + x * 8) = make_float2(out[0], out[1]);
-        }
-        __syncwarp();
 
         // ---- the block's maxima of scores and of value scales' exponents, per row
         float mb[NB][2];
         int es[NB][2];
         if (full) {
-            e_all = __reduce_max_sync(0xffffffffu, e_all);
+            const int e_all = max(kMinExp, static_cast<int>(__reduce_max_sync(0xffffffffu, top_scale) >> 23) - 126);   // s < 2^e
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) es[nb][0] = es[nb][1] = e_all;
         } else {
@@ -527,11 +645,8 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
             for (int tile = 0; tile < kTiles; ++tile)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t w[2 * G];
-                    lds_words<8 * G>(prep + (16 * tile + 8 * half + g) * 8 * G, w);
-                    uint32_t top = w[0];
-                    if constexpr (G == 2) top = max(top, w[2]);
-                    const int e = static_cast<int>(top >> 23) - 126;
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(scale + (16 * tile + 8 * half + g) * 4 * G);
+                    const int e = static_cast<int>(max(w[0], w[G - 1]) >> 23) - 126;
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -543,7 +658,7 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) es[nb][i] = max(es[nb][i], __shfl_xor_sync(0xffffffffu, es[nb][i], x));
+                    for (int y = 4; y < 32; y <<= 1) es[nb][i] = max(es[nb][i], __shfl_xor_sync(0xffffffffu, es[nb][i], y));
         }
         f2 ref[NB];                                       // weights are 2^(f s - ref) = 2^(15 - es) e^(score - max)
 #pragma unroll
@@ -554,7 +669,7 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
 #pragma unroll
                 for (int tile = 0; tile < kTiles; ++tile) top = fmaxf(top, fmaxf(s[tile][nb][i], s[tile][nb][2 + i]));
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
                 const float2 ff = upk(f[nb]);
                 mb[nb][i] = top * (i ? ff.y : ff.x);       // in units of log2
             }
@@ -564,51 +679,55 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
 
         // ---- weights, rounded to f16 after the value's scale, as operands
         uint32_t w16[kTiles][G][NB][2];
-        f2 lb[NB], zb[NB][G];
+        f2 lb[NB];
+        float zb[G][NB][4];                               // rows 0 and 1 (lanes g = 0 and 1): the parts of the minima's term
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            lb[nb] = 0;
+        for (int nb = 0; nb < NB; ++nb) lb[nb] = 0;
 #pragma unroll
-            for (int k = 0; k < G; ++k) zb[nb][k] = 0;
-        }
-#pragma unroll
-        for (int tile = 0; tile < kTiles; ++tile)
+        for (int tile = 0; tile < kTiles; ++tile) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                uint32_t pr[2 * G];
-                lds_words<8 * G>(prep + (16 * tile + 8 * half + g) * 8 * G, pr);
+                const float *sv = reinterpret_cast<const float *>(scale + (16 * tile + 8 * half + g) * 4 * G);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    const float2 x = upk(fma2(pk(s[tile][nb][2 * half], s[tile][nb][2 * half + 1]), f[nb], ref[nb]));
-                    const f2 w = pk(ex2(x.x), ex2(x.y));
-                    lb[nb] = add2(lb[nb], w);
+                    const float2 y = upk(fma2(pk(s[tile][nb][2 * half], s[tile][nb][2 * half + 1]), f[nb], ref[nb]));
+                    const float w0 = ex2(y.x), w1 = ex2(y.y);
+                    lb[nb] = add2(lb[nb], pk(w0, w1));
 #pragma unroll
                     for (int k = 0; k < G; ++k) {
-                        const float sv = __uint_as_float(pr[2 * k]), zr = __uint_as_float(pr[2 * k + 1]);
-                        const float2 ws = upk(mul2(w, pk(sv, sv)));
-                        const __half2 h = __floats2half2_rn(ws.x, ws.y);
-                        const float2 back = __half22float2(h);
-                        zb[nb][k] = fma2(pk(back.x, back.y), pk(zr, zr), zb[nb][k]);
+                        const __half2 h = __floats2half2_rn(w0 * sv[k], w1 * sv[k]);
                         w16[tile][k][nb][half] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h));
                     }
                 }
             }
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                const uint2 r = *reinterpret_cast<const uint2 *>(my_ratio + (tile * G + k) * ratio_step);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    if (tile == 0)
+                        mma_first(zb[k][nb], r.x, 0u, r.y, 0u, w16[tile][k][nb][0], w16[tile][k][nb][1]);
+                    else
+                        mma(zb[k][nb], r.x, 0u, r.y, 0u, w16[tile][k][nb][0], w16[tile][k][nb][1]);
+            }
+        }
 
         // ---- weights of the fold: the chunk's side, and the block's with its power of two undone
         f2 wa[NB], wo[NB], wq[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            float x[2], y[2];
+            float u[2], v[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[nb][i] = fold_weights(m[nb][i], mb[nb][i], x[i], y[i]);
-                y[i] *= pow2_int(min(es[nb][i], kMaxExp) - 20);   // 2^(es - 15), its 2^5 left out
+                m[nb][i] = fold_weights(m[nb][i], mb[nb][i], u[i], v[i]);
+                v[i] *= pow2_int(min(es[nb][i], kMaxExp) - 20);   // 2^(es - 15), its 2^5 left out
             }
-            wa[nb] = pk(x[0], x[1]);
-            const f2 wb = pk(y[0], y[1]);
+            wa[nb] = pk(u[0], u[1]);
+            const f2 wb = pk(v[0], v[1]);
             l[nb] = fma2(mul2(lb[nb], pk(32.0f, 32.0f)), wb, mul2(l[nb], wa[nb]));
 #pragma unroll
-            for (int k = 0; k < G; ++k) z[nb][k] = fma2(mul2(zb[nb][k], pk(32.0f, 32.0f)), wb, mul2(z[nb][k], wa[nb]));
+            for (int k = 0; k < G; ++k)
+                z[nb][k] = fma2(mul2(pk(zb[k][nb][0], zb[k][nb][1]), pk(32.0f, 32.0f)), wb, mul2(z[nb][k], wa[nb]));
             wo[nb] = mul2(wb, pk(0x1p29f, 0x1p29f));        // and products carry 2^-24, odd elements 2^-20
             wq[nb] = mul2(wb, pk(0x1p25f, 0x1p25f));
         }
@@ -625,12 +744,6 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
                 for (int j = 0; j < 2; ++j) {
                     float acc[2][NB][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[h][nb][i] = 0.0f;
-#pragma unroll
                     for (int tile = 0; tile < kTiles; ++tile) {
                         uint32_t x0[4], x1[4];
                         code_operands(vw[2 * tile][2 * k + j], x0);
@@ -639,16 +752,20 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb)
-                                mma(acc[h][nb], x0[2 * h], x0[2 * h + 1], x1[2 * h], x1[2 * h + 1], w16[tile][k][nb][0],
-                                    w16[tile][k][nb][1]);
+                                if (tile == 0)
+                                    mma_first(acc[h][nb], x0[2 * h], x0[2 * h + 1], x1[2 * h], x1[2 * h + 1],
+                                              w16[tile][k][nb][0], w16[tile][k][nb][1]);
+                                else
+                                    mma(acc[h][nb], x0[2 * h], x0[2 * h + 1], x1[2 * h], x1[2 * h + 1], w16[tile][k][nb][0],
+                                        w16[tile][k][nb][1]);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
-                            f2 *x = o[k][2 * j + h][nb];   // elements 2 h and 2 h + 1 of the word, two rows each
-                            x[0] = fma2(pk(acc[h][nb][0], acc[h][nb][1]), wo[nb], mul2(x[0], wa[nb]));
-                            x[1] = fma2(pk(acc[h][nb][2], acc[h][nb][3]), wq[nb], mul2(x[1], wa[nb]));
+                            f2 *u = o[k][2 * j + h][nb];   // elements 2 h and 2 h + 1 of the word, two rows each
+                            u[0] = fma2(pk(acc[h][nb][0], acc[h][nb][1]), wo[nb], mul2(u[0], wa[nb]));
+                            u[1] = fma2(pk(acc[h][nb][2], acc[h][nb][3]), wq[nb], mul2(u[1], wa[nb]));
                         }
                 }
         }
@@ -659,40 +776,32 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
     cp_wait<0>();
     __syncwarp();                                          // the warp's codes are read; its results take their place
 
-    float *ow = reinterpret_cast<float *>(mine);
     float *sm = reinterpret_cast<float *>(smem + P::kM), *sl = reinterpret_cast<float *>(smem + P::kL);
-    if (g == 0)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-            *reinterpret_cast<float2 *>(sm + warp * P::R + 8 * nb + 2 * t) = make_float2(m[nb][0], m[nb][1]);
     // sums over the lanes that share a row (after the fold, lane by lane)
-    auto over_lanes = [&](f2 x) {
+    auto over_lanes = [&](f2 v) {
 #pragma unroll
-        for (int i = 4; i < 32; i <<= 1) x = add2(x, __shfl_xor_sync(0xffffffffu, x, i));
-        return x;
+        for (int i = 4; i < 32; i <<= 1) v = add2(v, __shfl_xor_sync(0xffffffffu, v, i));
+        return v;
     };
-    if constexpr (!WIDE) {
+    float *ow = reinterpret_cast<float *>(mine);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+    for (int nb = 0; nb < NB; ++nb) {
+        if (g == 0)
+            *reinterpret_cast<float2 *>(sm + warp * P::R + 8 * nb + 2 * t) = make_float2(m[nb][0], m[nb][1]);
+        if constexpr (SPLIT) {
+            f2 *lz = reinterpret_cast<f2 *>(mine + P::kO) + nb * (1 + G) * 32 + lane;
+            lz[0] = l[nb];
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                lz[32 * (1 + k)] = z[nb][k];
+                z[nb][k] = 0;
+            }
+        } else {
             const f2 sum = over_lanes(l[nb]);
             if (g == 0) *reinterpret_cast<f2 *>(sl + warp * P::R + 8 * nb + 2 * t) = sum;
 #pragma unroll
             for (int k = 0; k < G; ++k) z[nb][k] = over_lanes(z[nb][k]);
         }
-    } else {
-        f2 *lz = reinterpret_cast<f2 *>(mine + P::kO) + lane * (NB * (1 + G));
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            lz[nb * (1 + G)] = l[nb];
-#pragma unroll
-            for (int k = 0; k < G; ++k) {
-                lz[nb * (1 + G) + 1 + k] = z[nb][k];
-                z[nb][k] = 0;
-            }
-        }
-    }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int k = 0; k < G; ++k)
 #pragma unroll
@@ -700,7 +809,7 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
                 const float2 e0 = upk(o[k][2 * j][nb][0]), e1 = upk(o[k][2 * j][nb][1]), e2 = upk(o[k][2 * j + 1][nb][0]),
                              e3 = upk(o[k][2 * j + 1][nb][1]), zz = upk(z[nb][k]);
                 float *dst = ow + (8 * nb + 2 * t) * D + 64 * k + 8 * g + 4 * j;
-                if constexpr (WIDE) {
+                if constexpr (SPLIT) {
                     *reinterpret_cast<float4 *>(dst) = make_float4(e0.x, e1.x, e2.x, e3.x);
                     *reinterpret_cast<float4 *>(dst + D) = make_float4(e0.y, e1.y, e2.y, e3.y);
                 } else {
@@ -708,48 +817,89 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
                     *reinterpret_cast<float4 *>(dst + D) = make_float4(e0.y + zz.y, e1.y + zz.y, e2.y + zz.y, e3.y + zz.y);
                 }
             }
-    __syncthreads();
-    if constexpr (WIDE) {
-        // chunk `warp`: the lanes' sums folded over its blocks as a single warp would, then over the lanes
-        if (warp < kChunks) {
+    }
+    // a CTA's share of the rows' elements, 4 each: all of them, or an eighth
+    constexpr int kItems = P::R * D / 4 / (SPLIT ? kCluster : 1);
+    const float *maxima = sm;
+    if constexpr (SPLIT) {
+        cluster_sync_all();                                // the cluster's results are in its shared memory
+        // chunk `warp`: block j is warp `warp` of CTA j; the lanes' sums folded as a single warp would, then over the
+        // lanes.  A block that no row sees has maxima of -inf, and folding it in changes nothing.
+        float2 *fold = reinterpret_cast<float2 *>(smem + P::kFold) + warp * kChunkBlocks * P::R;
+        float *chunk_max = reinterpret_cast<float *>(smem + P::kC);
+        uint32_t there[kChunkBlocks];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                f2 ll = 0, zz[G];
-                float mm[2] = {-INFINITY, -INFINITY};
+        for (int j = 0; j < kChunkBlocks; ++j) there[j] = cluster_map(smem_u32(smem), j);
 #pragma unroll
-                for (int k = 0; k < G; ++k) zz[k] = 0;
+        for (int nb = 0; nb < NB; ++nb) {
+            f2 mj[kChunkBlocks], lj[kChunkBlocks], zj[kChunkBlocks][G], ll = 0, zz[G];
 #pragma unroll
-                for (int j = 0; j < kChunkBlocks; ++j) {
-                    const int wj = warp * kChunkBlocks + j;
-                    const f2 *lz = reinterpret_cast<const f2 *>(smem + wj * P::kWarp + P::kO) + (lane * NB + nb) * (1 + G);
-                    float x[2], y[2];
+            for (int j = 0; j < kChunkBlocks; ++j) {
+                const uint32_t lz = there[j] + warp * P::kWarp + P::kO + (nb * (1 + G) * 32 + lane) * 8;
+                mj[j] = ld_cluster_b64(there[j] + P::kM + (warp * P::R + 8 * nb + 2 * t) * 4);
+                lj[j] = ld_cluster_b64(lz);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        mm[i] = fold_weights(mm[i], sm[wj * P::R + 8 * nb + 2 * t + i], x[i], y[i]);
-                    const f2 fa = pk(x[0], x[1]), fb = pk(y[0], y[1]);
-                    ll = fma2(lz[0], fb, mul2(ll, fa));
+                for (int k = 0; k < G; ++k) zj[j][k] = ld_cluster_b64(lz + 256 * (1 + k));
+            }
+            float mm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < G; ++k) zz[k] = fma2(lz[1 + k], fb, mul2(zz[k], fa));
-                }
-                const f2 sum = over_lanes(ll);
-                if (g == 0) *reinterpret_cast<f2 *>(sl + warp * P::R + 8 * nb + 2 * t) = sum;
+            for (int k = 0; k < G; ++k) zz[k] = 0;
 #pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    const float2 v = upk(over_lanes(zz[k]));
-                    float *dst = reinterpret_cast<float *>(smem + P::kZ) + (warp * P::R + 8 * nb + 2 * t) * G + k;
-                    if (g == 0) {
-                        dst[0] = v.x;
-                        dst[G] = v.y;
-                    }
+            for (int j = 0; j < kChunkBlocks; ++j) {
+                const float2 x = upk(mj[j]);
+                float u[2], v[2];
+                mm[0] = fold_weights(mm[0], x.x, u[0], v[0]);
+                mm[1] = fold_weights(mm[1], x.y, u[1], v[1]);
+                if (g == 0)
+                    *reinterpret_cast<float4 *>(fold + j * P::R + 8 * nb + 2 * t) = make_float4(u[0], v[0], u[1], v[1]);
+                const f2 fa = pk(u[0], u[1]), fb = pk(v[0], v[1]);
+                ll = fma2(lj[j], fb, mul2(ll, fa));
+#pragma unroll
+                for (int k = 0; k < G; ++k) zz[k] = fma2(zj[j][k], fb, mul2(zz[k], fa));
+            }
+            const f2 sum = over_lanes(ll);
+            if (g == 0) {
+                *reinterpret_cast<f2 *>(sl + warp * P::R + 8 * nb + 2 * t) = sum;
+                *reinterpret_cast<float2 *>(chunk_max + warp * P::R + 8 * nb + 2 * t) = make_float2(mm[0], mm[1]);
+            }
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                const float2 v = upk(over_lanes(zz[k]));
+                float *dst = reinterpret_cast<float *>(smem + P::kZ) + (warp * P::R + 8 * nb + 2 * t) * G + k;
+                if (g == 0) {
+                    dst[0] = v.x;
+                    dst[G] = v.y;
                 }
             }
         }
-        __syncthreads();
+        __syncwarp();
+        // this CTA's items of chunk `warp`
+        for (int i = lane; i < kItems; i += 32) {
+            const int e = rank * kItems + i, rl = e / (D / 4), d = e % (D / 4) * 4;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u[kChunkBlocks];
+#pragma unroll
+            for (int j = 0; j < kChunkBlocks; ++j) u[j] = ld_cluster_f4(there[j] + warp * P::kWarp + (rl * D + d) * 4);
+#pragma unroll
+            for (int j = 0; j < kChunkBlocks; ++j) {
+                const float2 w = fold[j * P::R + rl];
+                v.x = __fmaf_rn(u[j].x, w.y, v.x * w.x);
+                v.y = __fmaf_rn(u[j].y, w.y, v.y * w.x);
+                v.z = __fmaf_rn(u[j].z, w.y, v.z * w.x);
+                v.w = __fmaf_rn(u[j].w, w.y, v.w * w.x);
+            }
+            const float zz = reinterpret_cast<const float *>(smem + P::kZ)[(warp * P::R + rl) * G + d / kKv4Group];
+            reinterpret_cast<float4 *>(smem + P::kV)[warp * kItems + i] =
+                make_float4(v.x + zz, v.y + zz, v.z + zz, v.w + zz);
+        }
+        maxima = chunk_max;
+        __syncwarp();
+        cluster_arrive();                                  // this CTA has read what it needs of the others
     }
+    __syncthreads();
 
     // ---- the span's chunks joined in order
-    for (int i = threadIdx.x; i < P::R * D / 4; i += 32 * WARPS) {
-        const int rl = i / (D / 4), d = i % (D / 4) * 4, r = rows.r0 + rl;
+    for (int i = threadIdx.x; i < kItems; i += kThreads) {
+        const int e = rank * kItems + i, rl = e / (D / 4), d = e % (D / 4) * 4, r = rows.r0 + rl;
         if (r > rows.r_last) break;
         const int tok = rows.token(r), n = min(c.max_kv, rows.first + tok + 1);
         if (p0 >= n && (span > 0 || n > 0)) continue;
@@ -757,39 +907,23 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
         float4 vc[kChunks];
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
-            if constexpr (WIDE) {
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float mm = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < kChunkBlocks; ++j) {
-                    const int wj = ch * kChunkBlocks + j;
-                    float x, y;
-                    mm = fold_weights(mm, sm[wj * P::R + rl], x, y);
-                    const float4 u = *reinterpret_cast<const float4 *>(smem + wj * P::kWarp + (rl * D + d) * 4);
-                    v.x = __fmaf_rn(u.x, y, v.x * x);
-                    v.y = __fmaf_rn(u.y, y, v.y * x);
-                    v.z = __fmaf_rn(u.z, y, v.z * x);
-                    v.w = __fmaf_rn(u.w, y, v.w * x);
-                }
-                const float zz = reinterpret_cast<const float *>(smem + P::kZ)[(ch * P::R + rl) * G + d / kKv4Group];
-                mc[ch] = mm;
-                vc[ch] = make_float4(v.x + zz, v.y + zz, v.z + zz, v.w + zz);
-            } else {
-                mc[ch] = sm[ch * P::R + rl];
+            mc[ch] = maxima[ch * P::R + rl];
+            if constexpr (SPLIT)
+                vc[ch] = reinterpret_cast<const float4 *>(smem + P::kV)[ch * kItems + i];
+            else
                 vc[ch] = *reinterpret_cast<const float4 *>(smem + ch * P::kWarp + (rl * D + d) * 4);
-            }
             top = fmaxf(top, mc[ch]);
         }
         const float base = top == -INFINITY ? 0.0f : top;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
-            const float e = ex2(mc[ch] - base);
-            sum = __fmaf_rn(e, sl[ch * P::R + rl], sum);
-            v.x = __fmaf_rn(e, vc[ch].x, v.x);
-            v.y = __fmaf_rn(e, vc[ch].y, v.y);
-            v.z = __fmaf_rn(e, vc[ch].z, v.z);
-            v.w = __fmaf_rn(e, vc[ch].w, v.w);
+            const float w = ex2(mc[ch] - base);
+            sum = __fmaf_rn(w, sl[ch * P::R + rl], sum);
+            v.x = __fmaf_rn(w, vc[ch].x, v.x);
+            v.y = __fmaf_rn(w, vc[ch].y, v.y);
+            v.z = __fmaf_rn(w, vc[ch].z, v.z);
+            v.w = __fmaf_rn(w, vc[ch].w, v.w);
         }
         const int64_t at = static_cast<int64_t>(rows.t0 + tok) * a.Hq + rows.hk * rows.GH + r - tok * rows.GH;
         if (n <= kSpan) {
@@ -801,81 +935,127 @@ __global__ void __launch_bounds__(WIDE ? 512 : 128, WIDE ? 1 : (D * NB > 128 ? 3
         }
     }
 
-    // ---- the row block's last CTA joins the spans
+    // ---- the last CTA of a row block, or in clusters the last of a rank (which holds whole rows), joins the spans
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_wait();                                    // no CTA leaves while another reads its shared memory
+    }
     if (!p.count || n_most <= kSpan) return;
     int *flag = reinterpret_cast<int *>(smem + P::kFlag);
     __syncthreads();
     if (threadIdx.x == 0) {
-        int *counter = static_cast<int *>(a.ws) + (static_cast<int64_t>(b) * c.Hkv + rows.hk) * p.row_blocks + rb;
+        int *counter = static_cast<int *>(a.ws) +
+                       ((static_cast<int64_t>(b) * c.Hkv + rows.hk) * p.row_blocks + rb) * (SPLIT ? kCluster : 1) + rank;
         const bool last = atom_add_acq_rel_gpu(counter, 1) == (n_most + kSpan - 1) / kSpan - 1;
         if (last) *counter = 0;
         *flag = last;
     }
     __syncthreads();
     if (!*flag) return;
-    for (int i = threadIdx.x; i < P::R * D / 4; i += 32 * WARPS) {
-        const int rl = i / (D / 4), d = i % (D / 4) * 4, r = rows.r0 + rl;
+    for (int i = threadIdx.x; i < kItems; i += kThreads) {
+        const int e = rank * kItems + i, rl = e / (D / 4), d = e % (D / 4) * 4, r = rows.r0 + rl;
         if (r > rows.r_last) break;
         const int tok = rows.token(r), n = min(c.max_kv, rows.first + tok + 1);
         if (n <= kSpan) continue;
         const int64_t at = static_cast<int64_t>(rows.t0 + tok) * a.Hq + rows.hk * rows.GH + r - tok * rows.GH;
-        float4 v;
-        float sum;
-        join_spans<D>(reinterpret_cast<const float *>(static_cast<char *>(a.ws) + kCounterBytes) + at * p.spans * (D + 4),
-                      (n + kSpan - 1) / kSpan, d, v, sum);
+        const float *part =
+            reinterpret_cast<const float *>(static_cast<char *>(a.ws) + kCounterBytes) + at * p.spans * (D + 4);
+        const int C = (n + kSpan - 1) / kSpan;
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll 8
+        for (int x = 0; x < C; ++x) top = fmaxf(top, __ldcg(part + static_cast<int64_t>(x) * (D + 4)));
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (top > -INFINITY) add_spans<D>(part, 0, C, top, d, v, sum);
         write_out<D>(a, at, d, v, sum);
     }
 }
 
-// D / 4 threads per (token, q head): the spans' results in order, where the
-// span kernel does not join them itself.
+// One CTA per (token, q head), where the span kernel does not join a row's
+// spans itself: eight groups of D / 4 threads take runs of kJoinSpans spans in
+// turn, and their sums are added in order.  (Rows of at most one run get the
+// bits of the span kernel's own join: the other groups' sums are zeros.)
 template <int D>
-__global__ void __launch_bounds__(128) attn_kv4_join_kernel(AttnKv4Args a, int spans)
+__global__ void __launch_bounds__(2 * D) attn_kv4_join_kernel(AttnKv4Args a, int spans)
 {
     constexpr int L = D / 4;
-    const int64_t id = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) / L;
-    const int d = threadIdx.x % L * 4;
-    const int t = static_cast<int>(min(id / a.Hq, static_cast<int64_t>(a.c.T - 1)));
+    __shared__ float red[2 * D / 32];
+    __shared__ float4 vs[8][L];
+    __shared__ float ss[8];
+    const int tid = threadIdx.x, group = tid / L, d = tid % L * 4;
+    const int t = blockIdx.x / a.Hq;
     pdl_wait();
     const int b = kv4_sequence(a.c, t);
-    if (b < 0 || id >= static_cast<int64_t>(a.c.T) * a.Hq) return;
+    if (b < 0) return;
     const int begin = __ldg(a.c.cu_q + b), end = __ldg(a.c.cu_q + b + 1);
     const int n = min(a.c.max_kv, __ldg(a.c.kv_len + b) - (end - t) + 1);
     if (t - begin >= a.c.max_q || n <= kSpan) return;
-    float4 v;
-    float sum;
-    join_spans<D>(reinterpret_cast<const float *>(static_cast<char *>(a.ws) + kCounterBytes) + id * spans * (D + 4),
-                  (n + kSpan - 1) / kSpan, d, v, sum);
-    write_out<D>(a, id, d, v, sum);
+    const int C = (n + kSpan - 1) / kSpan;
+    const float *part = reinterpret_cast<const float *>(static_cast<char *>(a.ws) + kCounterBytes) +
+                        static_cast<int64_t>(blockIdx.x) * spans * (D + 4);
+    float top = -INFINITY;
+    for (int c = tid; c < C; c += 2 * D) top = fmaxf(top, __ldcg(part + static_cast<int64_t>(c) * (D + 4)));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (tid % 32 == 0) red[tid / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2 * D / 32; ++w) top = fmaxf(top, red[w]);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+    if (top > -INFINITY)
+        for (int c = group * kJoinSpans; c < C; c += 8 * kJoinSpans)
+            add_spans<D>(part, c, min(C, c + kJoinSpans), top, d, v, sum);
+    vs[group][tid % L] = v;
+    if (d == 0) ss[group] = sum;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+        const float4 u = vs[j][tid];
+        v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        sum += ss[j];
+    }
+    write_out<D>(a, blockIdx.x, d, v, sum);
 }
 
 int spans_of(int max_kv) { return (max_kv + kSpan - 1) / kSpan; }
 
-template <int D, int NB, bool WIDE>
+template <int D, int NB, bool SPLIT>
 cudaError_t launch_span(const SpanArgs &p, cudaStream_t stream)
 {
-    constexpr int WARPS = WIDE ? kChunks * kChunkBlocks : kChunks, bytes = Plan<D, NB, WARPS>::kBytes;
+    constexpr int bytes = Plan<D, NB, SPLIT>::kBytes;
     const cudaError_t e =
-        cudaFuncSetAttribute(attn_kv4_span_kernel<D, NB, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaFuncSetAttribute(attn_kv4_span_kernel<D, NB, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * p.spans), static_cast<unsigned>(p.a.c.Hkv),
+    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * p.spans) * (SPLIT ? kCluster : 1), static_cast<unsigned>(p.a.c.Hkv),
                        static_cast<unsigned>(p.a.c.B));
-    cfg.blockDim = dim3(32 * WARPS);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (SPLIT) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = kCluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (p.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = p.pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_kv4_span_kernel<D, NB, WIDE>, p);
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, attn_kv4_span_kernel<D, NB, SPLIT>, p);
 }
 
 template <int D, int NB>
-cudaError_t launch_span(const SpanArgs &p, bool wide, cudaStream_t stream)
+cudaError_t launch_span(const SpanArgs &p, bool split, cudaStream_t stream)
 {
-    return wide ? launch_span<D, NB, true>(p, stream) : launch_span<D, NB, false>(p, stream);
+    return split ? launch_span<D, NB, true>(p, stream) : launch_span<D, NB, false>(p, stream);
 }
 
 }  // namespace
@@ -888,24 +1068,28 @@ size_t attention_kv4_workspace(int Hq, int D, int T, int max_kv)
 
 cudaError_t launch_attention_kv4(const AttnKv4Args &a, int D, bool pdl, cudaStream_t stream)
 {
-    const int GH = a.Hq / a.c.Hkv, rows = a.c.max_q * GH, NB = rows <= 8 ? 1 : 2;
+    const int GH = a.Hq / a.c.Hkv, rows = a.c.max_q * GH;
     SpanArgs p;
     p.a = a;
     p.magic = (1ull << 32) / GH + 1;
-    p.row_blocks = (rows + 8 * NB - 1) / (8 * NB);
     p.spans = spans_of(a.c.max_kv);
     p.pdl = pdl ? 1 : 0;
+    // 16 rows a CTA where there are as many; a span a cluster while the spans alone leave SMs idle
+    const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv;
+    const bool two = rows > 8;
+    p.row_blocks = two ? (rows + 15) / 16 : (rows + 7) / 8;
+    const bool split = heads * p.row_blocks * p.spans <= a.sms;
     if (static_cast<int64_t>(p.row_blocks) * p.spans > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    const int64_t groups = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
-    p.count = groups <= kCounters && p.spans <= kJoinSpans;
-    // 16 warps a CTA where every CTA has a SM to itself
-    const bool wide = groups * p.spans <= a.sms;
-    cudaError_t e = D == 64 ? (NB == 1 ? launch_span<64, 1>(p, wide, stream) : launch_span<64, 2>(p, wide, stream))
-                            : (NB == 1 ? launch_span<128, 1>(p, wide, stream) : launch_span<128, 2>(p, wide, stream));
+    p.count = heads * p.row_blocks * (split ? kCluster : 1) <= kCounters && p.spans <= kJoinSpans;
+    cudaError_t e;
+    if (D == 64)
+        e = two ? launch_span<64, 2>(p, split, stream) : launch_span<64, 1>(p, split, stream);
+    else
+        e = two ? launch_span<128, 2>(p, split, stream) : launch_span<128, 1>(p, split, stream);
     if (e != cudaSuccess || p.count || p.spans == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.c.T) * a.Hq * (D / 4) + 127) / 128));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.c.T) * a.Hq);
+    cfg.blockDim = dim3(2 * D);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
