@@ -69,7 +69,8 @@ constexpr int kMaxExp = 118;                        // largest that is undone ag
 constexpr float kMinScale = 0x1p-110f;              // groups of smaller scale count as zeros
 constexpr int kCounters = 16384;                    // row blocks whose spans are counted in the workspace
 constexpr int kJoinSpans = 16;                      // spans that a CTA joins itself at most, and a run of the second launch
-constexpr size_t kCounterBytes = kCounters * sizeof(int);
+constexpr size_t kStatusBytes = 256;                // the status word, then the counters, then the spans' results
+constexpr size_t kCounterBytes = kStatusBytes + kCounters * sizeof(int);
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -78,21 +79,13 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// BYTES bytes to shared memory, or zeros where `there` is false (the address is not read then).
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t smem, const void *gmem, bool there)
+// `bytes` (a multiple of 16) from global to shared memory by the copy engine, counted on `bar`.
+__device__ __forceinline__ void bulk_copy(uint32_t smem, unsigned long long gmem, uint32_t bytes, uint64_t *bar)
 {
-    const int n = there ? BYTES : 0;
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(smem), "l"(gmem), "r"(n) : "memory");
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem),
+                 "l"(gmem), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
-
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
 {
@@ -163,10 +156,10 @@ struct Plan {
     static constexpr int kScale = kBlock * 4 * G;          // value scales of the block, fp32 [position][group]
     static constexpr int kRatio = kBlock * 4 * G;          // their z / s, two f16 parts [tile][group][part][16 positions]
     static constexpr int kZero = 16 * 2;                   // zeros for the rows of V^T that are not there
-    static constexpr int kWarp = 2 * kCodes + 2 * kPar + kScale + kRatio + kZero;   // parameters of two blocks
+    static constexpr int kWarp = 2 * kCodes + kPar + kScale + kRatio + kZero;
     static constexpr int kQRow = 2 * D + 8;                // bytes of a query row in f16; the 8 spread the banks
     static constexpr int kO = R * D * 4;                   // a result's values; they take the place of the warp's codes
-    static constexpr int kLZ = 32 * 2 * NB * (1 + G) * 4;  // and, in a cluster, its sums lane by lane
+    static constexpr int kLZ = (32 + 8 * G) * NB * 8;      // and, in a cluster, its sums lane by lane
     static constexpr int kResult = kO + (SPLIT ? kLZ : 0);
     static constexpr int kQ = kChunks * kWarp;
     static constexpr int kT = kQ + R * kQRow;              // sums of q per row: 8 bf16, three parts a group, then zeros
@@ -174,15 +167,14 @@ struct Plan {
     static constexpr int kN = kF + R * 4;                  // positions that a row sees
     static constexpr int kM = kN + R * 4;                  // maxima [warp][row]
     static constexpr int kL = kM + kChunks * R * 4;        // sums [chunk][row]
-    // in a cluster: the chunks' maxima and weighted minima, weights of the folds [chunk][block][row], chunks' values
+    // in a cluster: the chunks' maxima [chunk][row] and values of the CTA's rows [chunk][item]
     static constexpr int kC = kL + kChunks * R * 4;
-    static constexpr int kZ = kC + (SPLIT ? kChunks * R * 4 : 0);
-    static constexpr int kFold = kZ + (SPLIT ? kChunks * R * G * 4 : 0);
-    static constexpr int kV = kFold + (SPLIT ? kChunks * kChunkBlocks * R * 8 : 0);
+    static constexpr int kV = kC + (SPLIT ? kChunks * R * 4 : 0);
     static constexpr int kFlag = kV + (SPLIT ? kO / 8 * kChunks : 0);
-    static constexpr int kBytes = kFlag + 16;
+    static constexpr int kBar = kFlag + 16;                // two barriers a warp: keys and parameters, values
+    static constexpr int kBytes = kBar + kChunks * 16;
     static_assert(R * D / 4 / kCluster % (D / 4) == 0, "a CTA of a cluster joins whole rows");
-    static_assert(kResult <= kWarp && kV % 16 == 0 && kFold % 16 == 0, "a warp's results fit in the place of its codes");
+    static_assert(kResult <= kWarp && kV % 16 == 0, "a warp's results fit in the place of its codes");
 };
 
 template <int BYTES>
@@ -347,24 +339,15 @@ __device__ __forceinline__ void write_out(const AttnKv4Args &a, int64_t at, int 
         make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
 }
 
-// Adds spans first .. end - 1 of a row in order, 4 elements at d, under the
-// row's maximum; part: the row's span results (D + 4 floats each: maximum, sum,
-// values from 4 on).
-template <int D>
-__device__ __forceinline__ void add_spans(const float *part, int first, int end, float top, int d, float4 &v, float &sum)
+// Adds one span's result, maximum and sum ml and 4 values x, under the row's maximum.
+__device__ __forceinline__ void add_span(const float2 &ml, const float4 &x, float top, float4 &v, float &sum)
 {
-#pragma unroll 8
-    for (int c = first; c < end; ++c) {
-        const float *pc = part + static_cast<int64_t>(c) * (D + 4);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pc));
-        const float4 x = __ldcg(reinterpret_cast<const float4 *>(pc + 4 + d));
-        const float w = ex2(ml.x - top);
-        sum = __fmaf_rn(w, ml.y, sum);
-        v.x = __fmaf_rn(w, x.x, v.x);
-        v.y = __fmaf_rn(w, x.y, v.y);
-        v.z = __fmaf_rn(w, x.z, v.z);
-        v.w = __fmaf_rn(w, x.w, v.w);
-    }
+    const float w = ex2(ml.x - top);
+    sum = __fmaf_rn(w, ml.y, sum);
+    v.x = __fmaf_rn(w, x.x, v.x);
+    v.y = __fmaf_rn(w, x.y, v.y);
+    v.z = __fmaf_rn(w, x.z, v.z);
+    v.w = __fmaf_rn(w, x.w, v.w);
 }
 
 struct SpanArgs {
@@ -376,15 +359,16 @@ struct SpanArgs {
 };
 
 template <int D, int NB, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_kernel(SpanArgs p)
+__global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : D * NB > 64 || SPLIT ? 4 : 5) attn_kv4_span_kernel(SpanArgs p)
 {
     using P = Plan<D, NB, SPLIT>;
     constexpr int G = P::G, W = P::kPiece / 4, BLOCKS = P::kBlocks;
     extern __shared__ __align__(16) unsigned char smem[];
     const AttnKv4Args &a = p.a;
     const Kv4View &c = a.c;
+    // the spans are the slowest axis: the short last spans of a batch come last
     const int rank = SPLIT ? blockIdx.x % kCluster : 0, task = SPLIT ? blockIdx.x / kCluster : blockIdx.x;
-    const int span = task / p.row_blocks, rb = task - span * p.row_blocks, b = blockIdx.z;
+    const int hk = task / p.row_blocks, rb = task - hk * p.row_blocks, b = blockIdx.y, span = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (p.pdl) pdl_wait();
     pdl_launch_dependents();
@@ -399,12 +383,12 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
     Rows rows;
     rows.t0 = max(0, cu0);
     rows.GH = a.Hq / c.Hkv;
-    rows.hk = blockIdx.y;
+    rows.hk = hk;
     rows.magic = p.magic;
     rows.r0 = rb * P::R;
     rows.first = len - (cu1 - cu0);                       // position of the first new token
     const int tokens = min(c.T, cu1) - rows.t0, n_rows = min(tokens, c.max_q) * rows.GH;
-    if (task == 0 && rank == 0)                           // tokens past max_q are left out: zeros
+    if (rb == 0 && span == 0 && rank == 0)                // tokens past max_q are left out: zeros
         for (int64_t i = static_cast<int64_t>(c.max_q) * rows.GH * (D / 4) + threadIdx.x;
              i < static_cast<int64_t>(tokens) * rows.GH * (D / 4); i += kThreads) {
             const int64_t r = i / (D / 4), tok = r / rows.GH;
@@ -425,62 +409,51 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
     const int slot = my_pos & (PS - 1);
     const unsigned char *block = kv4_block<D>(c, max(page, 0), rows.hk);
     const unsigned long long codes = reinterpret_cast<unsigned long long>(block + slot * Kv4Layout::k_row(D));
-    const int v_off = Kv4Layout::v_off(PS, D) + t * Kv4Layout::v_pair(D) + g * P::kPiece, k_off = lane * P::kPiece;
     // parameters begin p_off(PS) - slot (k_row - p_row) after the codes
     const int par_off = Kv4Layout::p_off(PS, D) - slot * (Kv4Layout::k_row(D) - Kv4Layout::p_row(D));
-    const bool long_pages = PS >= kBlock;                  // then a block lies in one page
-    // copies of a block's keys and parameters, or of its values; zeros for pages that are not there
+    // Copies of a block's keys with parameters, or of its values: 16 positions a lane, or one lane for all where a page
+    // holds the whole block.  Pages that are not there are left out (what stands in their place is not used).
+    const bool whole = PS >= kBlock;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + P::kBar) + 2 * warp;
+    if (lane == 0) {
+        mbar_init(bars, 1);
+        mbar_init(bars + 1, 1);
+        fence_mbarrier_init();
+    }
+    __syncwarp();
+    const int sub = whole ? 0 : lane & 3, count = whole ? kBlock : 16;
+    const bool copies = page >= 0 && (!whole || (lane & 3) == 0);
+    const unsigned copy_mask = __ballot_sync(0xffffffffu, copies);
     auto copy_keys = [&](int blk) {
-        const uint32_t par = my + 2 * P::kCodes + (blk & 1) * P::kPar;
-        if (long_pages) {
-            const bool there = (pages >> (4 * blk)) & 1u;
-            const unsigned char *src = reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk));
-            const int po = __shfl_sync(0xffffffffu, par_off, 4 * blk);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                cp_async<P::kPiece>(my + (32 * i + lane) * P::kPiece, src + k_off + i * 32 * P::kPiece, there);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                cp_async<8 * G>(par + (32 * i + lane) * 8 * G, src + po + (32 * i + lane) * 8 * G, there);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool there = (pages >> (4 * blk + i)) & 1u;
-                const unsigned char *src =
-                    reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk + i));
-                const int po = __shfl_sync(0xffffffffu, par_off, 4 * blk + i);
-                cp_async<P::kPiece>(my + (64 * i + lane) * P::kPiece, src + k_off, there);
-                cp_async<P::kPiece>(my + (64 * i + 32 + lane) * P::kPiece, src + k_off + 32 * P::kPiece, there);
-                if (lane < 16) cp_async<8 * G>(par + (16 * i + lane) * 8 * G, src + po + lane * 8 * G, there);
+        if ((lane >> 2) == blk) {
+            if ((lane & 3) == 0)
+                mbar_arrive_expect_tx(bars, __popc((copy_mask >> (4 * blk)) & 15u) * count *
+                                                (Kv4Layout::k_row(D) + Kv4Layout::p_row(D)));
+            if (copies) {
+                bulk_copy(my + sub * 16 * Kv4Layout::k_row(D), codes, count * Kv4Layout::k_row(D), bars);
+                bulk_copy(my + 2 * P::kCodes + sub * 16 * Kv4Layout::p_row(D), codes + par_off, count * Kv4Layout::p_row(D),
+                          bars);
             }
         }
-        cp_commit();
     };
     auto copy_values = [&](int blk) {
-        if (long_pages) {
-            const bool there = (pages >> (4 * blk)) & 1u;
-            const unsigned char *src = reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk));
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                cp_async<P::kPiece>(my + P::kCodes + (32 * i + lane) * P::kPiece, src + v_off + i * 4 * Kv4Layout::v_pair(D),
-                                    there);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool there = (pages >> (4 * blk + i)) & 1u;
-                const unsigned char *src =
-                    reinterpret_cast<const unsigned char *>(__shfl_sync(0xffffffffu, codes, 4 * blk + i));
-                cp_async<P::kPiece>(my + P::kCodes + (64 * i + lane) * P::kPiece, src + v_off, there);
-                cp_async<P::kPiece>(my + P::kCodes + (64 * i + 32 + lane) * P::kPiece,
-                                    src + v_off + 4 * Kv4Layout::v_pair(D), there);
-            }
+        if ((lane >> 2) == blk) {
+            if ((lane & 3) == 0)
+                mbar_arrive_expect_tx(bars + 1, __popc((copy_mask >> (4 * blk)) & 15u) * count * Kv4Layout::k_row(D));
+            if (copies)
+                bulk_copy(my + P::kCodes + sub * 16 * Kv4Layout::k_row(D), codes + Kv4Layout::v_off(PS, D),
+                          count * Kv4Layout::k_row(D), bars + 1);
         }
-        cp_commit();
+    };
+    int *status = static_cast<int *>(a.ws);
+    auto wait = [&](int which, int blk) {
+        if (!mbar_wait_bounded(bars + which, blk & 1, status)) *status = DEV_TIMEOUT;
+        __syncwarp();
     };
     copy_keys(0);
     copy_values(0);
     stage_queries<D, NB, SPLIT>(a, smem, rows);
-    unsigned char *scale = mine + 2 * P::kCodes + 2 * P::kPar, *ratio = scale + P::kScale;
+    unsigned char *scale = mine + 2 * P::kCodes + P::kPar, *ratio = scale + P::kScale;
     if (lane < 8) *reinterpret_cast<uint32_t *>(ratio + P::kRatio + 4 * lane) = 0;
     // this lane's part of z / s as rows of V^T: row 0 the first parts, row 1 the second, no others
     const unsigned char *my_ratio = g < 2 ? ratio + g * 32 + t * 8 : ratio + P::kRatio + t * 8;
@@ -513,9 +486,8 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
         // bit i: positions 16 i .. of the block are on a page; full: and every row sees the whole block
         const unsigned there = (pages >> (4 * blk)) & 15u;
         const bool full = there == 15u && pb + kBlock <= n_least;
-        cp_wait<1>();
-        __syncwarp();
-        const unsigned char *par = mine + 2 * P::kCodes + (blk & 1) * P::kPar;
+        wait(0, blk);
+        const unsigned char *par = mine + 2 * P::kCodes;
 
         // ---- the values' scales and z / s, two positions a lane; nothing for positions that no row sees
         uint32_t top_scale = 0;
@@ -625,10 +597,9 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
                             if (!((there >> tile) & 1u) || 16 * tile + 8 * half >= n) s[tile][nb][2 * half + i] = -INFINITY;
                 }
         }
-        // the keys are read: the next block's may come (parameters are double-buffered)
+        // keys and parameters are read: the next block's may come
         __syncwarp();
         if (more) copy_keys(blk + 1);
-        else cp_commit();
 
 
         // ---- the block's maxima of scores and of value scales' exponents, per row
@@ -733,11 +704,11 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
         }
 
         // ---- weighted values
-        cp_wait<1>();
+        wait(1, blk);
         {
             uint32_t vw[2 * kTiles][W];
 #pragma unroll
-            for (int i = 0; i < 2 * kTiles; ++i) lds_words<P::kPiece>(mine + P::kCodes + (i * 32 + lane) * P::kPiece, vw[i]);
+            for (int i = 0; i < 2 * kTiles; ++i) lds_words<P::kPiece>(mine + P::kCodes + (i * 4 + t) * Kv4Layout::v_pair(D) + g * P::kPiece, vw[i]);
 #pragma unroll
             for (int k = 0; k < G; ++k)
 #pragma unroll
@@ -771,9 +742,7 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
         }
         __syncwarp();
         if (more) copy_values(blk + 1);
-        else cp_commit();
     }
-    cp_wait<0>();
     __syncwarp();                                          // the warp's codes are read; its results take their place
 
     float *sm = reinterpret_cast<float *>(smem + P::kM), *sl = reinterpret_cast<float *>(smem + P::kL);
@@ -789,11 +758,12 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
         if (g == 0)
             *reinterpret_cast<float2 *>(sm + warp * P::R + 8 * nb + 2 * t) = make_float2(m[nb][0], m[nb][1]);
         if constexpr (SPLIT) {
-            f2 *lz = reinterpret_cast<f2 *>(mine + P::kO) + nb * (1 + G) * 32 + lane;
-            lz[0] = l[nb];
+            // l of every lane, [nb][lane]; z of the lanes that have some (g < 2), [nb][group][lane]
+            f2 *lz = reinterpret_cast<f2 *>(mine + P::kO);
+            lz[nb * 32 + lane] = l[nb];
 #pragma unroll
             for (int k = 0; k < G; ++k) {
-                lz[32 * (1 + k)] = z[nb][k];
+                if (g < 2) lz[(32 + 8 * k) * NB + nb * 8 + lane] = z[nb][k];
                 z[nb][k] = 0;
             }
         } else {
@@ -823,73 +793,66 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
     const float *maxima = sm;
     if constexpr (SPLIT) {
         cluster_sync_all();                                // the cluster's results are in its shared memory
-        // chunk `warp`: block j is warp `warp` of CTA j; the lanes' sums folded as a single warp would, then over the
-        // lanes.  A block that no row sees has maxima of -inf, and folding it in changes nothing.
-        float2 *fold = reinterpret_cast<float2 *>(smem + P::kFold) + warp * kChunkBlocks * P::R;
+        // The CTA ends with NB whole rows: 8 nb + 2 tr + i, i below.  Chunk `warp`: block j is warp `warp` of CTA j.  Sums
+        // are folded lane by lane as a single warp would, then added over the lanes.  A block that no row sees has
+        // maxima of -inf, and folding it in changes nothing.
+        const int nbr = NB == 2 ? rank / 4 : 0, tr = NB == 2 ? rank % 4 : rank / 2;
         float *chunk_max = reinterpret_cast<float *>(smem + P::kC);
-        uint32_t there[kChunkBlocks];
+        uint32_t cta[kCluster];
+        f2 mj[kChunkBlocks], lj[kChunkBlocks], zj[kChunkBlocks][G], ll = 0, zz[G];
 #pragma unroll
-        for (int j = 0; j < kChunkBlocks; ++j) there[j] = cluster_map(smem_u32(smem), j);
+        for (int j = 0; j < kChunkBlocks; ++j) {
+            cta[j] = cluster_map(smem_u32(smem), j);
+            const uint32_t lz = cta[j] + warp * P::kWarp + P::kO;
+            mj[j] = ld_cluster_b64(cta[j] + P::kM + (warp * P::R + 8 * nbr + 2 * tr) * 4);
+            lj[j] = ld_cluster_b64(lz + (nbr * 32 + 4 * g + tr) * 8);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            f2 mj[kChunkBlocks], lj[kChunkBlocks], zj[kChunkBlocks][G], ll = 0, zz[G];
-#pragma unroll
-            for (int j = 0; j < kChunkBlocks; ++j) {
-                const uint32_t lz = there[j] + warp * P::kWarp + P::kO + (nb * (1 + G) * 32 + lane) * 8;
-                mj[j] = ld_cluster_b64(there[j] + P::kM + (warp * P::R + 8 * nb + 2 * t) * 4);
-                lj[j] = ld_cluster_b64(lz);
-#pragma unroll
-                for (int k = 0; k < G; ++k) zj[j][k] = ld_cluster_b64(lz + 256 * (1 + k));
-            }
-            float mm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int k = 0; k < G; ++k) zz[k] = 0;
-#pragma unroll
-            for (int j = 0; j < kChunkBlocks; ++j) {
-                const float2 x = upk(mj[j]);
-                float u[2], v[2];
-                mm[0] = fold_weights(mm[0], x.x, u[0], v[0]);
-                mm[1] = fold_weights(mm[1], x.y, u[1], v[1]);
-                if (g == 0)
-                    *reinterpret_cast<float4 *>(fold + j * P::R + 8 * nb + 2 * t) = make_float4(u[0], v[0], u[1], v[1]);
-                const f2 fa = pk(u[0], u[1]), fb = pk(v[0], v[1]);
-                ll = fma2(lj[j], fb, mul2(ll, fa));
-#pragma unroll
-                for (int k = 0; k < G; ++k) zz[k] = fma2(zj[j][k], fb, mul2(zz[k], fa));
-            }
-            const f2 sum = over_lanes(ll);
-            if (g == 0) {
-                *reinterpret_cast<f2 *>(sl + warp * P::R + 8 * nb + 2 * t) = sum;
-                *reinterpret_cast<float2 *>(chunk_max + warp * P::R + 8 * nb + 2 * t) = make_float2(mm[0], mm[1]);
-            }
-#pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const float2 v = upk(over_lanes(zz[k]));
-                float *dst = reinterpret_cast<float *>(smem + P::kZ) + (warp * P::R + 8 * nb + 2 * t) * G + k;
-                if (g == 0) {
-                    dst[0] = v.x;
-                    dst[G] = v.y;
-                }
-            }
+            for (int k = 0; k < G; ++k)
+                zj[j][k] = ld_cluster_b64(lz + ((32 + 8 * k) * NB + nbr * 8 + 4 * (g & 1) + tr) * 8);
         }
-        __syncwarp();
-        // this CTA's items of chunk `warp`
+        f2 fa[kChunkBlocks], fb[kChunkBlocks];
+        float mm[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < G; ++k) zz[k] = 0;
+#pragma unroll
+        for (int j = 0; j < kChunkBlocks; ++j) {
+            const float2 x = upk(mj[j]);
+            float u[2], v[2];
+            mm[0] = fold_weights(mm[0], x.x, u[0], v[0]);
+            mm[1] = fold_weights(mm[1], x.y, u[1], v[1]);
+            fa[j] = pk(u[0], u[1]);
+            fb[j] = pk(v[0], v[1]);
+            ll = fma2(lj[j], fb[j], mul2(ll, fa[j]));
+#pragma unroll
+            for (int k = 0; k < G; ++k) zz[k] = fma2(zj[j][k], fb[j], mul2(zz[k], fa[j]));
+        }
+        const f2 sum = over_lanes(ll);
+        if (lane == 0) {
+            *reinterpret_cast<f2 *>(sl + warp * P::R + 8 * nbr + 2 * tr) = sum;
+            *reinterpret_cast<float2 *>(chunk_max + warp * P::R + 8 * nbr + 2 * tr) = make_float2(mm[0], mm[1]);
+        }
+        float2 zr[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) zr[k] = upk(over_lanes(g < 2 ? zz[k] : 0ull));
+        // the rows' elements of the chunk, 4 a lane
         for (int i = lane; i < kItems; i += 32) {
             const int e = rank * kItems + i, rl = e / (D / 4), d = e % (D / 4) * 4;
+            const bool odd = rl & 1;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u[kChunkBlocks];
 #pragma unroll
-            for (int j = 0; j < kChunkBlocks; ++j) u[j] = ld_cluster_f4(there[j] + warp * P::kWarp + (rl * D + d) * 4);
+            for (int j = 0; j < kChunkBlocks; ++j) u[j] = ld_cluster_f4(cta[j] + warp * P::kWarp + (rl * D + d) * 4);
 #pragma unroll
             for (int j = 0; j < kChunkBlocks; ++j) {
-                const float2 w = fold[j * P::R + rl];
-                v.x = __fmaf_rn(u[j].x, w.y, v.x * w.x);
-                v.y = __fmaf_rn(u[j].y, w.y, v.y * w.x);
-                v.z = __fmaf_rn(u[j].z, w.y, v.z * w.x);
-                v.w = __fmaf_rn(u[j].w, w.y, v.w * w.x);
+                const float2 a2 = upk(fa[j]), b2 = upk(fb[j]);
+                const float wx = odd ? a2.y : a2.x, wy = odd ? b2.y : b2.x;
+                v.x = __fmaf_rn(u[j].x, wy, v.x * wx);
+                v.y = __fmaf_rn(u[j].y, wy, v.y * wx);
+                v.z = __fmaf_rn(u[j].z, wy, v.z * wx);
+                v.w = __fmaf_rn(u[j].w, wy, v.w * wx);
             }
-            const float zz = reinterpret_cast<const float *>(smem + P::kZ)[(warp * P::R + rl) * G + d / kKv4Group];
-            reinterpret_cast<float4 *>(smem + P::kV)[warp * kItems + i] =
-                make_float4(v.x + zz, v.y + zz, v.z + zz, v.w + zz);
+            const float2 zk = G == 2 && d >= kKv4Group ? zr[G - 1] : zr[0];
+            const float z1 = odd ? zk.y : zk.x;
+            reinterpret_cast<float4 *>(smem + P::kV)[warp * kItems + i] = make_float4(v.x + z1, v.y + z1, v.z + z1, v.w + z1);
         }
         maxima = chunk_max;
         __syncwarp();
@@ -944,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
     int *flag = reinterpret_cast<int *>(smem + P::kFlag);
     __syncthreads();
     if (threadIdx.x == 0) {
-        int *counter = static_cast<int *>(a.ws) +
+        int *counter = reinterpret_cast<int *>(static_cast<char *>(a.ws) + kStatusBytes) +
                        ((static_cast<int64_t>(b) * c.Hkv + rows.hk) * p.row_blocks + rb) * (SPLIT ? kCluster : 1) + rank;
         const bool last = atom_add_acq_rel_gpu(counter, 1) == (n_most + kSpan - 1) / kSpan - 1;
         if (last) *counter = 0;
@@ -961,11 +924,28 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : 4) attn_kv4_span_
         const float *part =
             reinterpret_cast<const float *>(static_cast<char *>(a.ws) + kCounterBytes) + at * p.spans * (D + 4);
         const int C = (n + kSpan - 1) / kSpan;
+        // at most kJoinSpans: their maxima and sums, and the values of eight, are on their way at once
+        float2 ml[kJoinSpans];
+        float4 x[8], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-        for (int x = 0; x < C; ++x) top = fmaxf(top, __ldcg(part + static_cast<int64_t>(x) * (D + 4)));
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (top > -INFINITY) add_spans<D>(part, 0, C, top, d, v, sum);
+#pragma unroll
+        for (int j = 0; j < kJoinSpans; ++j) {
+            ml[j] = make_float2(-INFINITY, 0.0f);
+            if (j < C) ml[j] = __ldcg(reinterpret_cast<const float2 *>(part + static_cast<int64_t>(j) * (D + 4)));
+            if (j < 8 && j < C) x[j] = __ldcg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(j) * (D + 4) + 4 + d));
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinSpans; ++j) top = fmaxf(top, ml[j].x);
+        if (top > -INFINITY) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < C) add_span(ml[j], x[j], top, v, sum);
+#pragma unroll
+            for (int j = 8; j < kJoinSpans; ++j)
+                if (j < C)
+                    add_span(ml[j], __ldcg(reinterpret_cast<const float4 *>(part + static_cast<int64_t>(j) * (D + 4) + 4 + d)),
+                             top, v, sum);
+        }
         write_out<D>(a, at, d, v, sum);
     }
 }
@@ -1004,7 +984,12 @@ __global__ void __launch_bounds__(2 * D) attn_kv4_join_kernel(AttnKv4Args a, int
     float sum = 0.0f;
     if (top > -INFINITY)
         for (int c = group * kJoinSpans; c < C; c += 8 * kJoinSpans)
-            add_spans<D>(part, c, min(C, c + kJoinSpans), top, d, v, sum);
+#pragma unroll 8
+            for (int j = c; j < min(C, c + kJoinSpans); ++j) {
+                const float *from = part + static_cast<int64_t>(j) * (D + 4);
+                add_span(__ldcg(reinterpret_cast<const float2 *>(from)), __ldcg(reinterpret_cast<const float4 *>(from + 4 + d)),
+                         top, v, sum);
+            }
     vs[group][tid % L] = v;
     if (d == 0) ss[group] = sum;
     __syncthreads();
@@ -1028,8 +1013,8 @@ cudaError_t launch_span(const SpanArgs &p, cudaStream_t stream)
         cudaFuncSetAttribute(attn_kv4_span_kernel<D, NB, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * p.spans) * (SPLIT ? kCluster : 1), static_cast<unsigned>(p.a.c.Hkv),
-                       static_cast<unsigned>(p.a.c.B));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.a.c.Hkv * p.row_blocks) * (SPLIT ? kCluster : 1),
+                       static_cast<unsigned>(p.a.c.B), static_cast<unsigned>(p.spans));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
@@ -1078,8 +1063,7 @@ cudaError_t launch_attention_kv4(const AttnKv4Args &a, int D, bool pdl, cudaStre
     const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv;
     const bool two = rows > 8;
     p.row_blocks = two ? (rows + 15) / 16 : (rows + 7) / 8;
-    const bool split = heads * p.row_blocks * p.spans <= a.sms;
-    if (static_cast<int64_t>(p.row_blocks) * p.spans > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const bool split = 3 * heads * p.row_blocks * p.spans <= 2 * a.sms;
     p.count = heads * p.row_blocks * (split ? kCluster : 1) <= kCounters && p.spans <= kJoinSpans;
     cudaError_t e;
     if (D == 64)
