@@ -452,7 +452,8 @@ BI_API bi_status bi_rope_table(const double *inv_freq, int n_freq, float amp, in
  *   q  bf16, row t and head h at q + t ldq + h D, Hq heads (read only)
  *   k, v  bf16, rows of Hkv heads with strides ldk, ldv
  *        (the three may be parts of one packed projection output)
- *   rope  fp32 [n_pos, rot / 2, 2];  rot a multiple of 4, 0 .. D
+ *   rope  fp32 [n_pos, rot / 2, 2];  rot 0 .. D, a multiple of 8 (of 4 with
+ *        BI_ROPE_INTERLEAVED)
  *   q_norm, k_norm  bf16 [D] or NULL;  eps >= 0
  *   q_out bf16 [T, Hq, D], must not overlap the inputs
  * 16-byte aligned pointers; strides multiples of 8 elements.  Hq, Hkv <= 1024.

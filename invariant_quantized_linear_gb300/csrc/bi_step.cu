@@ -157,7 +157,7 @@ bi_status bi_rope_append_kv4(const uint16_t *q, int64_t ldq, int Hq, const uint1
     if (st != BI_OK) return st;
     const int64_t D = cache->D, T = batch->T, wq = Hq * D, wk = cache->Hkv * D;
     if (!q || !k || !v || !q_out || !rope || Hq < 1 || Hq > kMaxHeads || ldq < wq || ldk < wk || ldv < wk || n_pos < 1 ||
-        rot < 0 || rot > D || (rot % 4) != 0 || (layout != BI_ROPE_HALF && layout != BI_ROPE_INTERLEAVED) ||
+        rot < 0 || rot > D || (rot % (layout == BI_ROPE_HALF ? 8 : 4)) != 0 || (layout != BI_ROPE_HALF && layout != BI_ROPE_INTERLEAVED) ||
         !finite_at_least(eps, 0.0f))
         return BI_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope) ||
@@ -168,7 +168,8 @@ bi_status bi_rope_append_kv4(const uint16_t *q, int64_t ldq, int Hq, const uint1
     if (overlaps(q_out, ob, q, rows_bytes(T, ldq, wq, 2)) || overlaps(q_out, ob, k, rows_bytes(T, ldk, wk, 2)) ||
         overlaps(q_out, ob, v, rows_bytes(T, ldv, wk, 2)))
         return BI_ERR_INVALID_ARG;
-    st = device_info(nullptr);
+    int sms = 0;
+    st = device_info(&sms);
     if (st != BI_OK) return st;
     bi::RopeAppendArgs a;
     a.c = view(cache, batch);
@@ -186,8 +187,8 @@ bi_status bi_rope_append_kv4(const uint16_t *q, int64_t ldq, int Hq, const uint1
     a.n_pos = n_pos;
     a.rot = rot;
     a.q_out = q_out;
-    return from_cuda(bi::launch_rope_append_kv4(a, cache->D, layout == BI_ROPE_INTERLEAVED, (flags & BI_FLAG_PDL) != 0,
-                                                stream));
+    return from_cuda(bi::launch_rope_append_kv4(a, cache->D, layout == BI_ROPE_INTERLEAVED, sms,
+                                                (flags & BI_FLAG_PDL) != 0, stream));
 }
 
 bi_status bi_kv4_gather(const bi_kv4_cache *cache, const bi_kv4_batch *batch, uint16_t *k_out, uint16_t *v_out,
@@ -201,9 +202,10 @@ bi_status bi_kv4_gather(const bi_kv4_cache *cache, const bi_kv4_batch *batch, ui
     if (!aligned16(k_out) || !aligned16(v_out)) return BI_ERR_ALIGNMENT;
     const size_t nb = static_cast<size_t>(batch->T) * cache->Hkv * cache->D * 2;
     if (overlaps(k_out, nb, v_out, nb)) return BI_ERR_INVALID_ARG;
-    st = device_info(nullptr);
+    int sms = 0;
+    st = device_info(&sms);
     if (st != BI_OK) return st;
-    return from_cuda(bi::launch_kv4_gather(view(cache, batch), cache->D, k_out, v_out, stream));
+    return from_cuda(bi::launch_kv4_gather(view(cache, batch), cache->D, k_out, v_out, sms, stream));
 }
 
 size_t bi_attention_kv4_workspace_size(int Hq, const bi_kv4_cache *cache, const bi_kv4_batch *batch)
@@ -263,7 +265,8 @@ bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, int V, c
         return BI_ERR_ALIGNMENT;
     if (out && overlaps(out, rows_bytes(M, ldo, V, 4), logits, rows_bytes(M, ldl, V, 2))) return BI_ERR_INVALID_ARG;
     if (!ws || ws_bytes < bi::logits_workspace(M) || !aligned16(ws)) return BI_ERR_WORKSPACE;
-    const bi_status st = device_info(nullptr);
+    int sms = 0;
+    const bi_status st = device_info(&sms);
     if (st != BI_OK) return st;
     bi::LogitsArgs a;
     a.r = r;
@@ -276,7 +279,7 @@ bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, int V, c
     a.out = out;
     a.argmax = argmax;
     a.ws = ws;
-    return from_cuda(bi::launch_logits_process(a, (flags & BI_FLAG_PDL) != 0, stream));
+    return from_cuda(bi::launch_logits_process(a, sms, (flags & BI_FLAG_PDL) != 0, stream));
 }
 
 }  // extern "C"

@@ -2,12 +2,17 @@
 //
 // One CTA per (vocabulary slice, row).  The CTA counts the row's history ids
 // that fall into its slice in shared memory (integer adds, so the order of the
-// threads does not matter), then streams the slice once.  The slices' largest
-// values meet in a 64-bit key per row, (ordered value, ~index), by atomicMax;
-// the last CTA of a row writes the argmax and restores the row's words to zero.
+// threads does not matter), then streams the slice once; its logits are on
+// their way meanwhile.  Few elements are in a history, so four at a time are
+// looked up and only those with a count or a bias leave the straight path.  The
+// slices' largest values meet in a 64-bit key per row, (ordered value, ~index),
+// by atomicMax; the last CTA of a row writes the argmax and restores the row's
+// words to zero.
 //
 // Bound: HBM; 2 bytes read, 4 written and 1/8 of mask per logit.  A history is
-// read once per slice, from L2 after the first.
+// read once per slice, from L2 after the first.  Rows of an odd vocabulary start
+// anywhere: slices are cut so that a thread's four results are one aligned
+// store, and its four logits come out of two aligned loads.
 #include "ptx.cuh"
 #include "row_ops.cuh"
 #include "step.cuh"
@@ -16,7 +21,6 @@ namespace bi {
 
 namespace {
 
-constexpr int kSlice = 4096;
 constexpr int kLogitsThreads = 256;
 
 struct RowKey {
@@ -25,36 +29,66 @@ struct RowKey {
     int pad;
 };
 
-// Monotone map of a float that is not NaN to an unsigned integer above 0 (-inf: 0x007FFFFF + 1 > 0).
+// Monotone map of a float that is not NaN to an unsigned integer (above 0 for all but the lowest).
 __device__ __forceinline__ uint32_t ordered(float x)
 {
     const uint32_t b = __float_as_uint(x);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// N elements a thread, four at a time; the slice is 256 N elements.
+template <int N>
 __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, int pdl)
 {
-    __shared__ uint32_t held[kSlice];    // bit 31: in the history; the rest: times generated
-    __shared__ uint32_t biased[kSlice];  // 1 + index of the last bias for the element
+    constexpr int kSlice = kLogitsThreads * N, kSteps = N / 4;
+    extern __shared__ __align__(16) uint32_t smem[];
+    uint32_t *held = smem;               // bit 31: in the history; the rest: times generated
+    uint32_t *biased = smem + kSlice;    // 1 + index of the last bias for the element
     __shared__ unsigned long long best;
     if (pdl) {
         pdl_launch_dependents();
         pdl_wait();
     }
-    const int row = blockIdx.y, v0 = blockIdx.x * kSlice, tid = threadIdx.x;
-    const int n = min(kSlice, a.V - v0);
-    const bool hist = a.r.ids != nullptr, bias = a.r.bias_ids != nullptr && a.r.n_bias > 0;
+    const int row = blockIdx.y, tid = threadIdx.x;
+    const uint16_t *x = a.logits + row * a.ldl;
+    float *out = a.out ? a.out + row * a.ldo : nullptr;
+    // element v is number v + shift of the row's slices: numbers that are multiples of 4 are aligned for the store, or,
+    // without one, for the load
+    const int shift = out ? static_cast<int>((reinterpret_cast<uintptr_t>(out) >> 2) & 3u)
+                          : static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 1) & 3u);
+    const int v0 = static_cast<int>(blockIdx.x) * kSlice - shift;
+    // the four logits begin `off` elements into an aligned group of four
+    const int off = static_cast<int>(((reinterpret_cast<uintptr_t>(x) >> 1) + 4 - shift) & 3u);
+    uint2 lo[kSteps], hi[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int v = v0 + 4 * (tid + i * kLogitsThreads) - off;
+        const bool inner = v >= 0 && v + (off ? 8 : 4) <= a.V;
+        lo[i] = hi[i] = make_uint2(0u, 0u);
+        if (inner) {
+            lo[i] = __ldcs(reinterpret_cast<const uint2 *>(x + v));
+            if (off) hi[i] = __ldcs(reinterpret_cast<const uint2 *>(x + v + 4));
+        }
+    }
+    const bool hist = a.r.ids != nullptr, bias = a.r.bias_ids != nullptr;
+    const int end = hist ? a.r.end[row] : 0, mid = hist ? a.r.mid[row] : 0, begin = hist ? a.r.begin[row] : 0;
+    const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
+    const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
+    const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
     if (tid == 0) best = 0;
-    if (hist)
-        for (int i = tid; i < kSlice; i += kLogitsThreads) held[i] = 0;
-    if (bias)
-        for (int i = tid; i < kSlice; i += kLogitsThreads) biased[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        if (hist) reinterpret_cast<uint4 *>(held)[tid + i * kLogitsThreads] = make_uint4(0u, 0u, 0u, 0u);
+        if (bias) reinterpret_cast<uint4 *>(biased)[tid + i * kLogitsThreads] = make_uint4(0u, 0u, 0u, 0u);
+    }
     __syncthreads();
+    // ids of the slice: v0 <= id < v0 + kSlice, and 0 <= id < V
+    const int first = max(v0, 0), past = min(v0 + kSlice, a.V);
     if (hist) {
-        const int mid = a.r.mid[row], end = a.r.end[row];
-        for (int i = a.r.begin[row] + tid; i < end; i += kLogitsThreads) {
-            const int id = a.r.ids[i];
-            if (id >= v0 && id - v0 < n) {
+#pragma unroll 4
+        for (int i = begin + tid; i < end; i += kLogitsThreads) {
+            const int id = __ldg(a.r.ids + i);
+            if (id >= first && id < past) {
                 atomicOr(&held[id - v0], 0x80000000u);
                 if (i >= mid) atomicAdd(&held[id - v0], 1u);
             }
@@ -62,33 +96,79 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, in
     }
     if (bias)
         for (int i = tid; i < a.r.n_bias; i += kLogitsThreads) {
-            const int id = a.r.bias_ids[static_cast<int64_t>(row) * a.r.n_bias + i];
-            if (id >= v0 && id - v0 < n) atomicMax(&biased[id - v0], static_cast<uint32_t>(i + 1));
+            const int id = __ldg(a.r.bias_ids + static_cast<int64_t>(row) * a.r.n_bias + i);
+            if (id >= first && id < past) atomicMax(&biased[id - v0], static_cast<uint32_t>(i + 1));
         }
     __syncthreads();
-    const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
-    const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
-    const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
-    unsigned long long key = 0;
-    for (int i = tid; i < n; i += kLogitsThreads) {
-        const int v = v0 + i;
-        float x = __uint_as_float(static_cast<uint32_t>(a.logits[row * a.ldl + v]) << 16);
-        if (hist && held[i]) {
-            x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-            const uint32_t c = held[i] & 0x7FFFFFFFu;
-            if (c) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, static_cast<float>(c))), pres);
+
+    const uint32_t *mask = a.r.mask ? a.r.mask + row * a.r.ld_mask : nullptr;
+    float top = -INFINITY;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int k = tid + i * kLogitsThreads, v = v0 + 4 * k;
+        if (v + 4 <= 0 || v >= a.V) continue;
+        float y[4];
+        if (v - off >= 0 && v - off + (off ? 8 : 4) <= a.V) {
+            // elements off .. off + 3 of the eight
+            const uint32_t w[4] = {lo[i].x, lo[i].y, hi[i].x, hi[i].y};
+            const uint32_t p = off & 2 ? w[1] : w[0], q = off & 2 ? w[2] : w[1], r = off & 2 ? w[3] : w[2];
+            const uint32_t z0 = off & 1 ? __byte_perm(p, q, 0x5432) : p, z1 = off & 1 ? __byte_perm(q, r, 0x5432) : q;
+            y[0] = bf16_lo(z0), y[1] = bf16_hi(z0), y[2] = bf16_lo(z1), y[3] = bf16_hi(z1);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[e] = v + e >= 0 && v + e < a.V ? __uint_as_float(static_cast<uint32_t>(x[v + e]) << 16) : -INFINITY;
         }
-        if (bias && biased[i]) x = __fadd_rn(x, a.r.bias[static_cast<int64_t>(row) * a.r.n_bias + biased[i] - 1]);
-        if (a.r.mask && !((a.r.mask[row * a.r.ld_mask + (v >> 5)] >> (v & 31)) & 1u)) x = -INFINITY;
-        if (a.out) a.out[row * a.ldo + v] = x;
-        if (x > -INFINITY) {
-            if (x == 0.0f) x = 0.0f;                 // -0 and +0 tie
-            const unsigned long long k =
-                (static_cast<unsigned long long>(ordered(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(v));
-            key = k > key ? k : key;
+        if (hist) {
+            const uint4 c4 = reinterpret_cast<const uint4 *>(held)[k];
+            const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+            if (c[0] | c[1] | c[2] | c[3]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c[e]) {
+                        y[e] = y[e] > 0.0f ? __fdiv_rn(y[e], rep) : __fmul_rn(y[e], rep);
+                        const uint32_t n = c[e] & 0x7FFFFFFFu;
+                        if (n) y[e] = __fsub_rn(__fsub_rn(y[e], __fmul_rn(freq, static_cast<float>(n))), pres);
+                    }
+            }
+        }
+        if (bias) {
+            const uint4 b4 = reinterpret_cast<const uint4 *>(biased)[k];
+            const uint32_t b[4] = {b4.x, b4.y, b4.z, b4.w};
+            if (b[0] | b[1] | b[2] | b[3]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (b[e]) y[e] = __fadd_rn(y[e], __ldg(a.r.bias + static_cast<int64_t>(row) * a.r.n_bias + b[e] - 1));
+            }
+        }
+        if (mask) {
+            const int m = max(v, 0);                       // a row's first group may begin before it
+            const uint32_t bits = __funnelshift_r(__ldg(mask + (m >> 5)), __ldg(mask + (min(m + 3, a.V - 1) >> 5)), m & 31)
+                                  << (m - v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = (bits >> e) & 1u ? y[e] : -INFINITY;
+        }
+        if (out) {
+            if (v >= 0 && v + 4 <= a.V) {
+                __stcs(reinterpret_cast<float4 *>(out + v), make_float4(y[0], y[1], y[2], y[3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (v + e >= 0 && v + e < a.V) out[v + e] = y[e];
+            }
+        }
+        const float most = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+        if (most > top) {                                  // rare after a few; the lowest element of the largest value
+            top = most;
+            at = v + (y[0] == most ? 0 : y[1] == most ? 1 : y[2] == most ? 2 : 3);
         }
     }
     if (!a.argmax) return;
+    unsigned long long key = 0;
+    if (top > -INFINITY)                                   // + 0: -0 and +0 tie
+        key = (static_cast<unsigned long long>(ordered(top + 0.0f)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(at));
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
         key = k > key ? k : key;
@@ -106,22 +186,38 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, in
     }
 }
 
-}  // namespace
-
-size_t logits_workspace(int M) { return sizeof(RowKey) * static_cast<size_t>(M); }
-
-cudaError_t launch_logits_process(const LogitsArgs &a, bool pdl, cudaStream_t stream)
+template <int N>
+cudaError_t launch(const LogitsArgs &a, bool pdl, cudaStream_t stream)
 {
+    constexpr int slice = kLogitsThreads * N;
+    // room for the history's counts and the biases, as far as there are such
+    const int bytes = a.r.bias_ids ? 8 * slice : a.r.ids ? 4 * slice : 0;
+    if (8 * slice > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * slice);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.V + kSlice - 1) / kSlice), static_cast<unsigned>(a.M));
+    // up to 3 elements of shift
+    cfg.gridDim = dim3(static_cast<unsigned>((a.V + 3 + slice - 1) / slice), static_cast<unsigned>(a.M));
     cfg.blockDim = dim3(kLogitsThreads);
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, logits_kernel, a, pdl ? 1 : 0);
+    return cudaLaunchKernelEx(&cfg, logits_kernel<N>, a, pdl ? 1 : 0);
+}
+
+}  // namespace
+
+size_t logits_workspace(int M) { return sizeof(RowKey) * static_cast<size_t>(M); }
+
+cudaError_t launch_logits_process(const LogitsArgs &a, int sms, bool pdl, cudaStream_t stream)
+{
+    // short slices while the long ones would leave SMs idle: each slice reads the row's history again
+    return static_cast<int64_t>(a.M) * ((a.V + 8191) / 8192) < 2 * sms ? launch<8>(a, pdl, stream) : launch<32>(a, pdl, stream);
 }
 
 }  // namespace bi

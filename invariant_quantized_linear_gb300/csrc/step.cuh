@@ -61,8 +61,9 @@ struct RopeAppendArgs {
 cudaError_t launch_rope_table(const double *inv_freq, int n_freq, float amp, int n_pos, float2 *rope,
                               cudaStream_t stream);
 // D is 64 or 128
-cudaError_t launch_rope_append_kv4(const RopeAppendArgs &a, int D, bool interleaved, bool pdl, cudaStream_t stream);
-cudaError_t launch_kv4_gather(const Kv4View &c, int D, uint16_t *k_out, uint16_t *v_out, cudaStream_t stream);
+cudaError_t launch_rope_append_kv4(const RopeAppendArgs &a, int D, bool interleaved, int sms, bool pdl,
+                                   cudaStream_t stream);
+cudaError_t launch_kv4_gather(const Kv4View &c, int D, uint16_t *k_out, uint16_t *v_out, int sms, cudaStream_t stream);
 
 struct AttnKv4Args {
     Kv4View c;
@@ -89,7 +90,7 @@ struct LogitsArgs {
 };
 
 size_t logits_workspace(int M);
-cudaError_t launch_logits_process(const LogitsArgs &a, bool pdl, cudaStream_t stream);
+cudaError_t launch_logits_process(const LogitsArgs &a, int sms, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------------------ device helpers
 
