@@ -521,7 +521,7 @@ typedef struct {
     const float *frequency;    /* [M] or NULL: 0 */
     const int32_t *bias_ids;   /* [M, n_bias] or NULL; of equal ids in a row the last applies */
     const float *bias;         /* [M, n_bias], given with bias_ids */
-    int n_bias;                /* 0 .. 65536 */
+    int n_bias;                /* 0 .. 65535 */
     const uint32_t *mask;      /* [M, ld_mask] words, bit v % 32 of word v / 32 set = allowed; or NULL: all */
     int64_t ld_mask;           /* >= ceil(V / 32) */
 } bi_logits_rules;

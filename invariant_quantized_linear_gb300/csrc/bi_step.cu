@@ -256,7 +256,7 @@ bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, int V, c
         (out && ldo < V))
         return BI_ERR_INVALID_ARG;
     const bi_logits_rules &r = *rules;
-    if ((r.ids && (!r.begin || !r.mid || !r.end)) || r.n_bias < 0 || r.n_bias > 65536 ||
+    if ((r.ids && (!r.begin || !r.mid || !r.end)) || r.n_bias < 0 || r.n_bias > 65535 ||
         (r.n_bias > 0 && (!r.bias_ids || !r.bias)) || (r.mask && r.ld_mask < (V + 31) / 32))
         return BI_ERR_INVALID_ARG;
     if (!aligned(logits, 2) || !aligned4(out) || !aligned4(argmax) || !aligned4(r.ids) || !aligned4(r.begin) ||

@@ -18,7 +18,8 @@ namespace bi {
 namespace {
 
 constexpr int kAppendWarps = 4;                      // warps of a CTA
-constexpr int kBatch = 4;                            // heads (of a lane) in flight
+constexpr int kAppendCtas = 5;                       // CTAs a SM that the registers are to allow
+constexpr int kBatch = 3;                            // heads (of a lane) in flight
 constexpr int kTargetWarps = 16;                     // warps a SM that a call is cut into, if it has the heads
 
 __global__ void __launch_bounds__(256) rope_table_kernel(const double *inv_freq, int n_freq, float amp, int n_pos,
@@ -96,7 +97,7 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t &par
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float u = __fadd_rn(quotient_rn(__fsub_rn(x[e], lo), s, r), 12582912.0f);   // rne, as in code_byte
-            codes |= static_cast<uint32_t>(min(15, __float_as_int(u) - 0x4B400000)) << (4 * e);
+            codes |= (__float_as_uint(u) & 15u) << (4 * e);    // (max - z) / s < 15.5: s is off by 2^-9 at most
         }
     } else if (s > 0.0f) {
 #pragma unroll
@@ -134,156 +135,193 @@ struct Places {
     }
 };
 
-// Warps parts t .. of token t, a run of heads each: q heads 0 .. Hq - 1, then the kv heads' k, then their v.
+// Two fp32 to bf16, rounded to nearest even, in one conversion.
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The lane's 8 elements of a q or k head, normed and rotated, as bf16 pairs.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(32 * kAppendWarps) rope_append_kernel(RopeAppendArgs a, int parts, int pdl)
+struct Rotation {
+    static constexpr int L = D / 8;
+    float co[8], si[8];                                    // out = x co + partner si, si with its sign
+    int rot, swap, from[4], lane, d;
+    bool full;
+
+    __device__ __forceinline__ Rotation(const float2 *cs, int rot_, int lane_) : rot(rot_), lane(lane_)
+    {
+        const int l = lane % L, half = rot / 2;
+        d = 8 * l;
+        full = rot == D;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            co[e] = 1.0f;
+            si[e] = 0.0f;
+            if (d + e < rot) {
+                const bool second = INTERLEAVED ? e % 2 : d + e >= half;
+                const float2 f = __ldg(cs + (INTERLEAVED ? (d + e) / 2 : second ? d + e - half : d + e));
+                co[e] = f.x;
+                si[e] = second ? f.y : -f.y;
+            }
+        }
+        // partner words of the half layout: word j's comes from word j ^ swap of lane from[j]; a whole head's are the
+        // words D / 2 further (or back)
+        swap = half / 2 % 4;                               // 0 or 2: half is a multiple of 4
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int w = 4 * l + j + (d + 2 * j >= half ? -half / 2 : half / 2);
+            from[j] = (lane - l) + min(max(w, 0) / 4, L - 1);
+        }
+    }
+
+    // pn: the words D / 2 further
+    __device__ __forceinline__ void partner(const uint32_t (&w)[4], const uint32_t (&pn)[4], uint32_t (&p)[4]) const
+    {
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = (w[j] >> 16) | (w[j] << 16);
+        } else if (full) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = pn[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = __shfl_sync(0xffffffffu, swap ? w[j ^ 2] : w[j], from[j]);
+        }
+    }
+
+    // wn, wp: the norm's weights and the partners'
+    __device__ __forceinline__ void apply(uint32_t (&w)[4], bool norm, const uint32_t (&wn)[4], const uint32_t (&wp)[4],
+                                          float eps) const
+    {
+        uint32_t p[4], pn[4];
+        if (norm || (!INTERLEAVED && full)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pn[j] = __shfl_xor_sync(0xffffffffu, w[j], L / 2);
+        }
+        partner(w, pn, p);
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = elem(w, e);
+            y[e] = elem(p, e);
+        }
+        if (norm) {
+            const float sum = square_sum<D>(w, pn);
+            const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(sum / D, eps)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = __fmul_rn(__fmul_rn(x[e], r), elem(wn, e));
+                y[e] = __fmul_rn(__fmul_rn(y[e], r), elem(wp, e));
+            }
+        }
+        if (full) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(__fmul_rn(x[e], co[e]), __fmul_rn(y[e], si[e]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (d + e < rot) x[e] = __fadd_rn(__fmul_rn(x[e], co[e]), __fmul_rn(y[e], si[e]));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = to_bf16x2(x[2 * j], x[2 * j + 1]);
+    }
+};
+
+// `parts` warps a token, a run of steps each; a step is HEADS heads of one
+// kind: first the steps of the q heads, then of k, then of v.
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_kernel(RopeAppendArgs a, int parts, int pdl)
 {
     constexpr int L = D / 8, HEADS = 32 / L, G = D / kKv4Group;
     if (pdl) {
         pdl_launch_dependents();
         pdl_wait();
     }
-    const int lane = threadIdx.x & 31, l = lane % L, d = 8 * l;
+    const int lane = threadIdx.x & 31, d = lane % L * 8, hl = lane / L;
     const int64_t id = (static_cast<int64_t>(blockIdx.x) * (32 * kAppendWarps) + threadIdx.x) >> 5;
     const int t = static_cast<int>(id / parts), part = static_cast<int>(id - static_cast<int64_t>(t) * parts);
     if (t >= a.c.T) return;
-    const int heads = a.Hq + 2 * a.c.Hkv, steps = (heads + HEADS - 1) / HEADS;
-    const int per = (steps + parts - 1) / parts, first = part * per, last = min(steps, first + per);
-
-    // head h of the token: what it is and where it stands
-    auto source = [&](int h) {
-        return h < a.Hq ? a.q + t * a.ldq + h * D
-                        : h < a.Hq + a.c.Hkv ? a.k + t * a.ldk + (h - a.Hq) * D
-                                             : a.v + t * a.ldv + (h - a.Hq - a.c.Hkv) * D;
-    };
-    uint4 raw[kBatch];
-    auto load = [&](int step) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int h = (step + i) * HEADS + lane / L;
-            raw[i] = step + i < last && h < heads ? *reinterpret_cast<const uint4 *>(source(h) + d) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    load(first);
+    const int q_steps = (a.Hq + HEADS - 1) / HEADS, kv_steps = (a.c.Hkv + HEADS - 1) / HEADS;
+    const int steps = q_steps + 2 * kv_steps, per = (steps + parts - 1) / parts;
+    const int first = part * per, last = min(steps, first + per);
     const Kv4Token tok = kv4_token(a.c, t);
     if (tok.b < 0) return;
+    uint16_t *const qo = a.q_out + (static_cast<int64_t>(t) * a.Hq + hl) * D + d;
     if (tok.pos < 0 || tok.pos >= a.n_pos) {
-        for (int step = first; step < last; ++step) {
-            const int h = step * HEADS + lane / L;
-            if (h < a.Hq)
-                *reinterpret_cast<uint4 *>(a.q_out + (static_cast<int64_t>(t) * a.Hq + h) * D + d) = make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int step = first; step < min(last, q_steps); ++step)
+            if (step * HEADS + hl < a.Hq) *reinterpret_cast<uint4 *>(qo + step * (HEADS * D)) = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
+    const Rotation<D, INTERLEAVED> turn(a.rope + static_cast<int64_t>(tok.pos) * (a.rot / 2), a.rot, lane);
+    // The steps of one kind that are this warp's, kBatch loads ahead: body(step of the kind, whether the lane has a head,
+    // the lane's words).
+    auto each = [&](const uint16_t *base, int64_t ld, int heads, int begin, int n, auto body) {
+        const int s0 = max(first - begin, 0), s1 = min(last - begin, n);
+        if (s0 >= s1) return;
+        const uint16_t *src = base + t * ld + hl * D + d;
+        auto load = [&](int s) {
+            return s < s1 && s * HEADS + hl < heads ? __ldcs(reinterpret_cast<const uint4 *>(src + s * (HEADS * D)))
+                                                    : make_uint4(0u, 0u, 0u, 0u);
+        };
+        uint4 ahead[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) ahead[i] = load(s0 + i);
+#pragma unroll 1
+        for (int s = s0; s < s1; ++s) {
+            uint32_t w[4] = {ahead[0].x, ahead[0].y, ahead[0].z, ahead[0].w};
+#pragma unroll
+            for (int i = 0; i + 1 < kBatch; ++i) ahead[i] = ahead[i + 1];
+            ahead[kBatch - 1] = load(s + kBatch);
+            body(s, s * HEADS + hl < heads, w);
+        }
+    };
+    auto weights = [&](const uint16_t *norm, uint32_t (&wn)[4], uint32_t (&wp)[4]) {
+        uint32_t pn[4];
+        const uint4 v = norm ? __ldg(reinterpret_cast<const uint4 *>(norm + d)) : make_uint4(0u, 0u, 0u, 0u);
+        wn[0] = v.x, wn[1] = v.y, wn[2] = v.z, wn[3] = v.w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pn[j] = __shfl_xor_sync(0xffffffffu, wn[j], L / 2);
+        turn.partner(wn, pn, wp);
+    };
+    uint32_t wn[4], wp[4];
+    if (first < q_steps) {
+        weights(a.q_norm, wn, wp);
+        each(a.q, a.ldq, a.Hq, 0, q_steps, [&](int s, bool there, uint32_t (&w)[4]) {
+            turn.apply(w, a.q_norm != nullptr, wn, wp, a.eps);
+            if (there) *reinterpret_cast<uint4 *>(qo + s * (HEADS * D)) = make_uint4(w[0], w[1], w[2], w[3]);
+        });
+    }
+    if (last <= q_steps) return;
     const int P = 1 << a.c.page_shift;
     const Places<D> at(d, tok.pos & (P - 1), P);
-
-    // the lane's rotations: out = x co + partner si, si with its sign
-    const int half = a.rot / 2;
-    float co[8], si[8];
-    const float2 *cs = a.rope + static_cast<int64_t>(tok.pos) * half;
+    unsigned char *const block = kv4_block<D>(a.c, max(tok.page, 0), hl);
+    auto quantise = [&](int s, bool there, const uint32_t (&w)[4], bool key) {
+        float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        co[e] = 1.0f;
-        si[e] = 0.0f;
-        if (d + e < a.rot) {
-            const bool second = INTERLEAVED ? e % 2 : d + e >= half;
-            const float2 f = __ldg(cs + (INTERLEAVED ? (d + e) / 2 : second ? d + e - half : d + e));
-            co[e] = f.x;
-            si[e] = second ? f.y : -f.y;
+        for (int e = 0; e < 8; ++e) x[e] = elem(w, e);
+        uint32_t param;
+        const uint32_t codes = quantise8(x, param);
+        if (!there || tok.page < 0) return;
+        unsigned char *to = block + s * (HEADS * Kv4Layout::block(P, D));
+        if (key) {
+            *reinterpret_cast<uint32_t *>(to + at.key) = key_word(codes);
+        } else {
+            *reinterpret_cast<uint16_t *>(to + at.value) = static_cast<uint16_t>(codes);
+            *reinterpret_cast<uint16_t *>(to + at.value + 4) = static_cast<uint16_t>(codes >> 16);
         }
-    }
-    // the partner words of the half layout: word j's comes from word j ^ swap of lane from[j]
-    const int swap = half / 2 % 4;                    // 0 or 2: half is a multiple of 4
-    int from[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int w = 4 * l + j + (d + 2 * j >= half ? -half / 2 : half / 2);
-        from[j] = (lane - l) + min(max(w, 0) / 4, L - 1);
-    }
-    uint32_t wq[4] = {}, wk[4] = {}, wqp[4], wkp[4];
-    if (a.q_norm) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.q_norm + d));
-        wq[0] = v.x, wq[1] = v.y, wq[2] = v.z, wq[3] = v.w;
-    }
-    if (a.k_norm) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.k_norm + d));
-        wk[0] = v.x, wk[1] = v.y, wk[2] = v.z, wk[3] = v.w;
-    }
-    auto partner = [&](const uint32_t (&w)[4], uint32_t (&p)[4]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = __shfl_sync(0xffffffffu, swap ? w[j ^ 2] : w[j], from[j]);
+        if (d % kKv4Group == 0) *reinterpret_cast<uint32_t *>(to + at.par + (key ? 0 : 4 * G)) = param;
     };
-    if constexpr (!INTERLEAVED) {
-        partner(wq, wqp);
-        partner(wk, wkp);
+    if (first < q_steps + kv_steps) {
+        weights(a.k_norm, wn, wp);
+        each(a.k, a.ldk, a.c.Hkv, q_steps, kv_steps, [&](int s, bool there, uint32_t (&w)[4]) {
+            turn.apply(w, a.k_norm != nullptr, wn, wp, a.eps);
+            quantise(s, there, w, true);
+        });
     }
-
-    for (int step0 = first; step0 < last; step0 += kBatch) {
-        uint4 now[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) now[i] = raw[i];
-        if (step0 + kBatch < last) load(step0 + kBatch);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (step0 + i >= last) break;
-            const int h = (step0 + i) * HEADS + lane / L;
-            const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.c.Hkv, is_v = !is_q && !is_k;
-            const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = elem(w, e);
-            if ((step0 + i) * HEADS < a.Hq + a.c.Hkv) {   // some q or k in the warp
-                uint32_t p[4];
-                if constexpr (!INTERLEAVED) partner(w, p);
-                const bool norm = is_q ? a.q_norm != nullptr : is_k && a.k_norm != nullptr;
-                float y[8];                                // partners
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = INTERLEAVED ? elem(w, e ^ 1) : elem(p, e);
-                if (a.q_norm || a.k_norm) {
-                    uint32_t pn[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) pn[j] = __shfl_xor_sync(0xffffffffu, w[j], L / 2);
-                    const float sum = square_sum<D>(w, pn);
-                    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(sum / D, a.eps)));
-                    if (norm) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float u = is_q ? elem(wq, e) : elem(wk, e);
-                            const float v = INTERLEAVED ? (is_q ? elem(wq, e ^ 1) : elem(wk, e ^ 1))
-                                                        : (is_q ? elem(wqp, e) : elem(wkp, e));
-                            x[e] = __fmul_rn(__fmul_rn(x[e], r), u);
-                            y[e] = __fmul_rn(__fmul_rn(y[e], r), v);
-                        }
-                    }
-                }
-                if (!is_v) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (d + e < a.rot) x[e] = __fadd_rn(__fmul_rn(x[e], co[e]), __fmul_rn(y[e], si[e]));
-                }
-            }
-            const uint32_t o[4] = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                   pack_bf16x2(x[6], x[7])};
-            if (is_q)
-                *reinterpret_cast<uint4 *>(a.q_out + (static_cast<int64_t>(t) * a.Hq + h) * D + d) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-            if ((step0 + i + 1) * HEADS <= a.Hq) continue;     // q heads only
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = elem(o, e);
-            uint32_t param;
-            const uint32_t codes = quantise8(x, param);
-            if (is_q || h >= heads || tok.page < 0) continue;
-            unsigned char *block = kv4_block<D>(a.c, tok.page, is_k ? h - a.Hq : h - a.Hq - a.c.Hkv);
-            if (is_k) {
-                *reinterpret_cast<uint32_t *>(block + at.key) = key_word(codes);
-            } else {
-                *reinterpret_cast<uint16_t *>(block + at.value) = static_cast<uint16_t>(codes);
-                *reinterpret_cast<uint16_t *>(block + at.value + 4) = static_cast<uint16_t>(codes >> 16);
-            }
-            if (d % kKv4Group == 0) *reinterpret_cast<uint32_t *>(block + at.par + (is_k ? 0 : 4 * G)) = param;
-        }
-    }
+    each(a.v, a.ldv, a.c.Hkv, q_steps + kv_steps, kv_steps,
+         [&](int s, bool there, uint32_t (&w)[4]) { quantise(s, there, w, false); });
 }
 
 // A lane holds 8 elements of a (token, kv head), the key's and the value's.
@@ -321,8 +359,8 @@ __global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4View c, uint16_t *k_
                     y[i] = __fmaf_rn(bf16_lo(kp), static_cast<float>((kc >> sh) & 15u), bf16_hi(kp));
                     y[2 + i] = __fmaf_rn(bf16_lo(vp), static_cast<float>((vc >> sh) & 15u), bf16_hi(vp));
                 }
-                ko[e] = pack_bf16x2(y[0], y[1]);
-                vo[e] = pack_bf16x2(y[2], y[3]);
+                ko[e] = to_bf16x2(y[0], y[1]);
+                vo[e] = to_bf16x2(y[2], y[3]);
             }
             k = make_uint4(ko[0], ko[1], ko[2], ko[3]);
             v = make_uint4(vo[0], vo[1], vo[2], vo[3]);
@@ -346,7 +384,7 @@ template <int D, bool INTERLEAVED>
 cudaError_t launch_append(const RopeAppendArgs &a, int sms, bool pdl, cudaStream_t stream)
 {
     constexpr int HEADS = 32 / (D / 8);
-    const int parts = parts_of(a.c.T, (a.Hq + 2 * a.c.Hkv + HEADS - 1) / HEADS, sms);
+    const int parts = parts_of(a.c.T, (a.Hq + HEADS - 1) / HEADS + 2 * ((a.c.Hkv + HEADS - 1) / HEADS), sms);
     const int64_t warps = static_cast<int64_t>(a.c.T) * parts;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((warps + kAppendWarps - 1) / kAppendWarps));

@@ -2,12 +2,14 @@
 //
 // One CTA per (vocabulary slice, row).  The CTA counts the row's history ids
 // that fall into its slice in shared memory (integer adds, so the order of the
-// threads does not matter), then streams the slice once; its logits are on
-// their way meanwhile.  Few elements are in a history, so four at a time are
-// looked up and only those with a count or a bias leave the straight path.  The
-// slices' largest values meet in a 64-bit key per row, (ordered value, ~index),
-// by atomicMax; the last CTA of a row writes the argmax and restores the row's
-// words to zero.
+// threads does not matter) and lists the elements that it meets; their logits
+// are on their way meanwhile.  The slice is then streamed once, four elements a
+// thread, leaving the listed ones out of the maximum, and these are done
+// afterwards, one a thread: a text's few hundred tokens touch nearly every
+// group of 128 elements, and penalties in the stream would cost it twice its
+// time.  The slices' largest values meet in a 64-bit key per row, (ordered
+// value, ~index), by atomicMax; the last CTA of a row writes the argmax and
+// restores the row's words to zero.
 //
 // Bound: HBM; 2 bytes read, 4 written and 1/8 of mask per logit.  A history is
 // read once per slice, from L2 after the first.  Rows of an odd vocabulary start
@@ -36,15 +38,38 @@ __device__ __forceinline__ uint32_t ordered(float x)
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// A row's candidate: larger for a larger value, then for a lower index; 0 for -inf and NaN.
+__device__ __forceinline__ unsigned long long key_of(float x, int v)
+{
+    // + 0: -0 and +0 tie
+    return x > -INFINITY ? (static_cast<unsigned long long>(ordered(x + 0.0f)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(v))
+                         : 0ull;
+}
+
+// x[i] = max(x[i], v) for a 16-bit element, by exchanges of the word that holds it.
+__device__ __forceinline__ void max_u16(uint16_t *x, int i, uint32_t v)
+{
+    uint32_t *word = reinterpret_cast<uint32_t *>(x) + i / 2;
+    const int sh = 16 * (i & 1);
+    uint32_t old = *word;
+    while (((old >> sh) & 0xFFFFu) < v) {                  // each failed exchange means that another lane's went through
+        const uint32_t seen = atomicCAS(word, old, (old & ~(0xFFFFu << sh)) | (v << sh));
+        if (seen == old) break;
+        old = seen;
+    }
+}
+
 // N elements a thread, four at a time; the slice is 256 N elements.
 template <int N>
 __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, int pdl)
 {
     constexpr int kSlice = kLogitsThreads * N, kSteps = N / 4;
     extern __shared__ __align__(16) uint32_t smem[];
-    uint32_t *held = smem;               // bit 31: in the history; the rest: times generated
-    uint32_t *biased = smem + kSlice;    // 1 + index of the last bias for the element
+    uint32_t *held = smem;               // bit 31: in the history, bit 30: has a bias; the rest: times generated
+    uint16_t *listed = reinterpret_cast<uint16_t *>(smem + kSlice);   // the elements with any of these
+    uint16_t *biased = listed + kSlice;  // 1 + index of the last bias for the element
     __shared__ unsigned long long best;
+    __shared__ int n_listed;
     if (pdl) {
         pdl_launch_dependents();
         pdl_wait();
@@ -70,16 +95,31 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, in
             if (off) hi[i] = __ldcs(reinterpret_cast<const uint2 *>(x + v + 4));
         }
     }
-    const bool hist = a.r.ids != nullptr, bias = a.r.bias_ids != nullptr;
+    // and the mask's words; a row's first group of four may begin before it
+    const uint32_t *mask = a.r.mask ? a.r.mask + row * a.r.ld_mask : nullptr;
+    uint32_t m_lo[kSteps], m_hi[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int v = v0 + 4 * (tid + i * kLogitsThreads), m = max(v, 0);
+        m_lo[i] = m_hi[i] = ~0u;
+        if (mask && m < a.V) {
+            m_lo[i] = __ldg(mask + (m >> 5));
+            m_hi[i] = (m & 31) > 28 ? __ldg(mask + (min(m + 3, a.V - 1) >> 5)) : 0u;
+        }
+    }
+    const bool hist = a.r.ids != nullptr, bias = a.r.bias_ids != nullptr, some = hist || bias;
     const int end = hist ? a.r.end[row] : 0, mid = hist ? a.r.mid[row] : 0, begin = hist ? a.r.begin[row] : 0;
     const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
     const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
-    if (tid == 0) best = 0;
+    if (tid == 0) {
+        best = 0;
+        n_listed = 0;
+    }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        if (hist) reinterpret_cast<uint4 *>(held)[tid + i * kLogitsThreads] = make_uint4(0u, 0u, 0u, 0u);
-        if (bias) reinterpret_cast<uint4 *>(biased)[tid + i * kLogitsThreads] = make_uint4(0u, 0u, 0u, 0u);
+        if (some) reinterpret_cast<uint4 *>(held)[tid + i * kLogitsThreads] = make_uint4(0u, 0u, 0u, 0u);
+        if (bias) reinterpret_cast<uint2 *>(biased)[tid + i * kLogitsThreads] = make_uint2(0u, 0u);
     }
     __syncthreads();
     // ids of the slice: v0 <= id < v0 + kSlice, and 0 <= id < V
@@ -89,19 +129,23 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, in
         for (int i = begin + tid; i < end; i += kLogitsThreads) {
             const int id = __ldg(a.r.ids + i);
             if (id >= first && id < past) {
-                atomicOr(&held[id - v0], 0x80000000u);
+                if (atomicOr(&held[id - v0], 0x80000000u) == 0u) listed[atomicAdd(&n_listed, 1)] = static_cast<uint16_t>(id - v0);
                 if (i >= mid) atomicAdd(&held[id - v0], 1u);
             }
         }
     }
-    if (bias)
+    if (bias) {
+        __syncthreads();                                   // an element is listed by whoever finds its word zero
         for (int i = tid; i < a.r.n_bias; i += kLogitsThreads) {
             const int id = __ldg(a.r.bias_ids + static_cast<int64_t>(row) * a.r.n_bias + i);
-            if (id >= first && id < past) atomicMax(&biased[id - v0], static_cast<uint32_t>(i + 1));
+            if (id >= first && id < past) {
+                if (atomicOr(&held[id - v0], 0x40000000u) == 0u) listed[atomicAdd(&n_listed, 1)] = static_cast<uint16_t>(id - v0);
+                max_u16(biased, id - v0, static_cast<uint32_t>(i + 1));
+            }
         }
+    }
     __syncthreads();
 
-    const uint32_t *mask = a.r.mask ? a.r.mask + row * a.r.ld_mask : nullptr;
     float top = -INFINITY;
     int at = 0;
 #pragma unroll
@@ -120,32 +164,9 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, in
             for (int e = 0; e < 4; ++e)
                 y[e] = v + e >= 0 && v + e < a.V ? __uint_as_float(static_cast<uint32_t>(x[v + e]) << 16) : -INFINITY;
         }
-        if (hist) {
-            const uint4 c4 = reinterpret_cast<const uint4 *>(held)[k];
-            const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-            if (c[0] | c[1] | c[2] | c[3]) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c[e]) {
-                        y[e] = y[e] > 0.0f ? __fdiv_rn(y[e], rep) : __fmul_rn(y[e], rep);
-                        const uint32_t n = c[e] & 0x7FFFFFFFu;
-                        if (n) y[e] = __fsub_rn(__fsub_rn(y[e], __fmul_rn(freq, static_cast<float>(n))), pres);
-                    }
-            }
-        }
-        if (bias) {
-            const uint4 b4 = reinterpret_cast<const uint4 *>(biased)[k];
-            const uint32_t b[4] = {b4.x, b4.y, b4.z, b4.w};
-            if (b[0] | b[1] | b[2] | b[3]) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (b[e]) y[e] = __fadd_rn(y[e], __ldg(a.r.bias + static_cast<int64_t>(row) * a.r.n_bias + b[e] - 1));
-            }
-        }
         if (mask) {
-            const int m = max(v, 0);                       // a row's first group may begin before it
-            const uint32_t bits = __funnelshift_r(__ldg(mask + (m >> 5)), __ldg(mask + (min(m + 3, a.V - 1) >> 5)), m & 31)
-                                  << (m - v);
+            const int m = max(v, 0);
+            const uint32_t bits = __funnelshift_r(m_lo[i], m_hi[i], m & 31) << (m - v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = (bits >> e) & 1u ? y[e] : -INFINITY;
         }
@@ -158,16 +179,38 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, in
                     if (v + e >= 0 && v + e < a.V) out[v + e] = y[e];
             }
         }
+        if (some) {
+            const uint4 c = reinterpret_cast<const uint4 *>(held)[k];
+            if (c.x | c.y | c.z | c.w) {
+                y[0] = c.x ? -INFINITY : y[0];
+                y[1] = c.y ? -INFINITY : y[1];
+                y[2] = c.z ? -INFINITY : y[2];
+                y[3] = c.w ? -INFINITY : y[3];
+            }
+        }
         const float most = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
         if (most > top) {                                  // rare after a few; the lowest element of the largest value
             top = most;
             at = v + (y[0] == most ? 0 : y[1] == most ? 1 : y[2] == most ? 2 : 3);
         }
     }
+    unsigned long long key = key_of(top, at);
+    if (some) {
+        __syncthreads();                                   // the stream's stores come before these
+        for (int i = tid; i < n_listed; i += kLogitsThreads) {
+            const int k = listed[i], v = v0 + k;
+            const uint32_t c = held[k], n = c & 0x3FFFFFFFu;
+            float z = __uint_as_float(static_cast<uint32_t>(x[v]) << 16);
+            if (c & 0x80000000u) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+            if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, static_cast<float>(n))), pres);
+            if (c & 0x40000000u) z = __fadd_rn(z, __ldg(a.r.bias + static_cast<int64_t>(row) * a.r.n_bias + biased[k] - 1));
+            if (mask && !((__ldg(mask + (v >> 5)) >> (v & 31)) & 1u)) z = -INFINITY;
+            if (out) out[v] = z;
+            const unsigned long long kz = key_of(z, v);
+            key = kz > key ? kz : key;
+        }
+    }
     if (!a.argmax) return;
-    unsigned long long key = 0;
-    if (top > -INFINITY)                                   // + 0: -0 and +0 tie
-        key = (static_cast<unsigned long long>(ordered(top + 0.0f)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(at));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
@@ -191,8 +234,8 @@ cudaError_t launch(const LogitsArgs &a, bool pdl, cudaStream_t stream)
 {
     constexpr int slice = kLogitsThreads * N;
     // room for the history's counts and the biases, as far as there are such
-    const int bytes = a.r.bias_ids ? 8 * slice : a.r.ids ? 4 * slice : 0;
-    if (8 * slice > 48 * 1024) {
+    const int bytes = a.r.bias_ids ? 8 * slice : a.r.ids ? 6 * slice : 0;
+    if (bytes + 1024 > 48 * 1024) {                        // with the kernel's own, more than any launch may have
         const cudaError_t e = cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * slice);
         if (e != cudaSuccess) return e;
     }

@@ -53,12 +53,47 @@ __device__ __forceinline__ void norm8(const uint4 &h, const uint4 &w, float (&t)
     }
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&t)[8], float st)
+// bf16_rne(h + y) elementwise (one fp32 add each).
+__device__ __forceinline__ uint4 sum8(const uint4 &h, const uint4 &y)
+{
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w};
+    const uint32_t b[4] = {y.x, y.y, y.z, y.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 v =
+            __floats2bfloat162_rn(__fadd_rn(bf16_lo(a[e]), bf16_lo(b[e])), __fadd_rn(bf16_hi(a[e]), bf16_hi(b[e])));
+        o[e] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ uint2 codes8_div(const float (&t)[8], float st)
 {
     uint32_t o[2] = {0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e >> 2] |= code_byte(__fdiv_rn(t[e], st)) << (8 * (e & 3));
     return make_uint2(o[0], o[1]);
+}
+
+// The codes of 8 elements, r = RN(1 / st), 2^-64 <= st <= 2^64.  A quotient q by
+// quotient_rn is t / st but for an error far below an ulp, so rne(q) is the code
+// unless q lies within two ulps (2^-16 below 128) of the middle of two codes;
+// then (one element in 30,000) all 8 are divided.  |t| / st is at most 127 and a
+// rounding, so no code needs a clamp.
+__device__ __forceinline__ uint2 codes8(const float (&t)[8], float st, float r)
+{
+    uint32_t u[8];
+    float far = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float q = quotient_rn(t[e], st, r), c = __fadd_rn(q, 12582912.0f);   // rne, as in code_byte
+        u[e] = __float_as_uint(c);
+        far = fmaxf(far, fabsf(__fsub_rn(q, __fsub_rn(c, 12582912.0f))));
+    }
+    if (far >= 0.5f - 0x1p-16f) return codes8_div(t, st);
+    return make_uint2(__byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
 }
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
@@ -80,7 +115,7 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(NormArgs a,
     float t[C > 0 ? C : 1][8];
     auto load = [&](int k) {
         uint4 h = ldg16(hr + k);
-        return yr ? residual8(h, ldg16(yr + k)) : h;
+        return yr ? sum8(h, ldg16(yr + k)) : h;
     };
     if constexpr (C > 0) {
 #pragma unroll
@@ -97,19 +132,22 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(NormArgs a,
     }
     const float2 r = block_sum_max(s, m, red);
     const float st = r.y == 0.0f ? 1.0f : __fdiv_rn(r.y, 127.0f);
+    const bool plain = st >= kQuotientMinScale && st <= 0x1p64f;
+    const float inv = __fdiv_rn(1.0f, st);
+    auto codes = [&](const float (&x)[8]) { return plain ? codes8(x, st, inv) : codes8_div(x, st); };
     int8_t *qr = a.q + row * K;
     if constexpr (C > 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int k = (c * kNormThreads + threadIdx.x) * 8;
-            if (k < K) *reinterpret_cast<uint2 *>(qr + k) = codes8(t[c], st);
+            if (k < K) *reinterpret_cast<uint2 *>(qr + k) = codes(t[c]);
         }
     } else {
         for (int k = threadIdx.x * 8; k < K; k += kNormThreads * 8) {
             const uint4 h = load(k);                  // h_out may be h: it is written after its last read
             if (yr) *reinterpret_cast<uint4 *>(a.h_out + row * a.ldo + k) = h;
             norm8(h, ldg16(a.w + k), t[0], s, m);
-            *reinterpret_cast<uint2 *>(qr + k) = codes8(t[0], st);
+            *reinterpret_cast<uint2 *>(qr + k) = codes(t[0]);
         }
     }
     if (threadIdx.x == 0) {

@@ -505,6 +505,30 @@ def test_logits(bi, M, V, ldl, ldo, kind):
     assert not ws.any()
 
 
+def test_logits_many_rows(bi):
+    """Enough rows for the long slices: a few random rows of them against the reference, all of them against the same rows
+    a few at a time (short slices)."""
+    rng = np.random.default_rng(21)
+    M, V = 170, 16389                                           # three slices of 8192
+    x = bits(rng, (M, V + 2), 3.0)
+    r = rules_case(rng, M, V, "hist pen bias mask")
+    d = {k: dev(v) for k, v in r.items()}
+    dx = dev(x)[:, :V]
+    ws = bi.new_logits_workspace(M)
+    out, am = torch.empty((M, V), device=DEV), torch.empty(M, dtype=torch.int32, device=DEV)
+    bi.bi_logits_process(dx, bi.logits_rules(**d), out, am, ws)
+    for a in range(0, M, 17):
+        part = {k: v if k == "ids" else v[a:a + 17] for k, v in r.items()}
+        if a % 51 == 0:
+            want, best = ref.logits_process(x[a:a + 17], V, **part)
+            same(host(out)[a:a + 17], want, "logits")
+            same(host(am)[a:a + 17], best, "argmax")
+        o2, a2 = torch.empty((17, V), device=DEV), torch.empty(17, dtype=torch.int32, device=DEV)
+        bi.bi_logits_process(dx[a:a + 17], bi.logits_rules(**{k: dev(v) for k, v in part.items()}), o2, a2, ws)
+        assert torch.equal(o2, out[a:a + 17]) and torch.equal(a2, am[a:a + 17])
+    assert not ws.any()
+
+
 def test_attention_leaves_out_tokens_past_the_bound(bi):
     """Tokens past max_q have zeros, those before it their result, also where T does not show that there are any."""
     rng = np.random.default_rng(12)
