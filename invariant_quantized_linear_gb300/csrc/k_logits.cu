@@ -1,15 +1,16 @@
 // Penalties, biases and grammar masks on logits, with the argmax.
 //
-// One CTA per (vocabulary slice, row).  The CTA counts the row's history ids
-// that fall into its slice in shared memory (integer adds, so the order of the
-// threads does not matter) and lists the elements that it meets; their logits
-// are on their way meanwhile.  The slice is then streamed once, four elements a
-// thread, leaving the listed ones out of the maximum, and these are done
-// afterwards, one a thread: a text's few hundred tokens touch nearly every
-// group of 128 elements, and penalties in the stream would cost it twice its
-// time.  The slices' largest values meet in a 64-bit key per row, (ordered
-// value, ~index), by atomicMax; the last CTA of a row writes the argmax and
-// restores the row's words to zero.
+// One CTA per (vocabulary slice, row).  It marks the row's history ids and biases
+// that fall into the slice in a bit map, ranks the marks, and counts the ids at
+// their ranks (integer adds, so the order of the threads does not matter), all
+// in shared memory; the slice's first logits are on their way meanwhile.  The
+// slice is then streamed, four elements a thread; marked elements go with the
+// forbidden ones there, so that they do not enter the maximum, and are done
+// afterwards, one a thread, their logits asked for before the stream: a text's
+// few hundred tokens touch nearly every group of 128 elements, and penalties in
+// the stream would cost it twice its time.  The largest values meet in a 64-bit
+// key per row, (ordered value, ~index), by atomicMax; the last CTA of a row
+// writes the argmax and restores the row's words to zero.
 //
 // Bound: HBM; 2 bytes read, 4 written and 1/8 of mask per logit.  A history is
 // read once per slice, from L2 after the first.  Rows of an odd vocabulary start
@@ -19,11 +20,15 @@
 #include "row_ops.cuh"
 #include "step.cuh"
 
+#include <type_traits>
+
 namespace bi {
 
 namespace {
 
 constexpr int kLogitsThreads = 256;
+constexpr int kLogitsCtas = 4;           // CTAs a SM that the registers are to allow
+constexpr int kIds = 3;                  // groups of four history ids of a thread in flight
 
 struct RowKey {
     unsigned long long key;
@@ -59,155 +64,285 @@ __device__ __forceinline__ void max_u16(uint16_t *x, int i, uint32_t v)
     }
 }
 
-// N elements a thread, four at a time; the slice is 256 N elements.
-template <int N>
-__global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, int pdl)
+// A row as the kernel sees it.  Element v is number v + shift of the row's
+// slices: numbers that are multiples of 4 are aligned for the store, or, without
+// one, for the load.
+struct Row {
+    const uint16_t *x;
+    float *out;
+    const uint32_t *mask;
+    int V, off;                          // the four logits of a group begin `off` elements into an aligned four
+
+    __device__ __forceinline__ bool inner(int v) const { return v >= off && v - off + (off ? 8 : 4) <= V; }
+};
+
+// Four logits from v on, EDGE: as far as there are such (-inf else).
+template <bool EDGE>
+__device__ __forceinline__ void four(const Row &r, int v, const uint2 &lo, const uint2 &hi, float (&y)[4])
 {
-    constexpr int kSlice = kLogitsThreads * N, kSteps = N / 4;
-    extern __shared__ __align__(16) uint32_t smem[];
-    uint32_t *held = smem;               // bit 31: in the history, bit 30: has a bias; the rest: times generated
-    uint16_t *listed = reinterpret_cast<uint16_t *>(smem + kSlice);   // the elements with any of these
-    uint16_t *biased = listed + kSlice;  // 1 + index of the last bias for the element
+    if (EDGE && !r.inner(v)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[e] = v + e >= 0 && v + e < r.V ? __uint_as_float(static_cast<uint32_t>(r.x[v + e]) << 16) : -INFINITY;
+        return;
+    }
+    const bool up = r.off & 2;
+    const uint32_t p = up ? lo.y : lo.x, q = up ? hi.x : lo.y, s = up ? hi.y : hi.x;
+    const int sh = 16 * (r.off & 1);
+    const uint32_t z0 = __funnelshift_r(p, q, sh), z1 = __funnelshift_r(q, s, sh);
+    y[0] = bf16_lo(z0), y[1] = bf16_hi(z0), y[2] = bf16_lo(z1), y[3] = bf16_hi(z1);
+}
+
+// Bit e of the mask words that hold elements v .. v + 3 (a row's first group may begin before it).
+__device__ __forceinline__ uint32_t mask_bits(uint32_t lo, uint32_t hi, int v)
+{
+    const int m = max(v, 0);
+    return __funnelshift_r(lo, hi, m & 31) << (m - v);
+}
+
+constexpr int kMarks = 4096;             // marked elements of a slice done at once
+
+// Shared memory for a slice of `slice` elements.
+struct LogitsPlan {
+    int rank, held, listed, biased, bytes;
+    __host__ __device__ constexpr LogitsPlan(int slice)
+        : rank(slice / 8), held(rank + slice / 16), listed(held + 4 * kMarks), biased(listed + 2 * kMarks),
+          bytes(biased + 2 * kMarks)
+    {
+    }
+};
+
+// STEPS groups of four elements a thread, BATCH of them in flight; the slice is 1024 STEPS elements.
+template <int STEPS, int BATCH>
+__global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(LogitsArgs a, int pdl)
+{
+    constexpr int kSlice = 4 * kLogitsThreads * STEPS, kWords = kSlice / 32;
+    constexpr LogitsPlan P(kSlice);
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint32_t *marked = reinterpret_cast<uint32_t *>(smem);            // a bit an element
+    uint16_t *rank = reinterpret_cast<uint16_t *>(smem + P.rank);     // marks before each word
+    // of the marked elements, by rank: times generated, bit 31: in the prompt, bit 30: has a bias; which; its last bias + 1
+    uint32_t *held = reinterpret_cast<uint32_t *>(smem + P.held);
+    uint16_t *listed = reinterpret_cast<uint16_t *>(smem + P.listed), *biased = reinterpret_cast<uint16_t *>(smem + P.biased);
     __shared__ unsigned long long best;
-    __shared__ int n_listed;
+    __shared__ int warp_marks[kLogitsThreads / 32];
     if (pdl) {
         pdl_launch_dependents();
         pdl_wait();
     }
-    const int row = blockIdx.y, tid = threadIdx.x;
-    const uint16_t *x = a.logits + row * a.ldl;
-    float *out = a.out ? a.out + row * a.ldo : nullptr;
-    // element v is number v + shift of the row's slices: numbers that are multiples of 4 are aligned for the store, or,
-    // without one, for the load
-    const int shift = out ? static_cast<int>((reinterpret_cast<uintptr_t>(out) >> 2) & 3u)
-                          : static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 1) & 3u);
-    const int v0 = static_cast<int>(blockIdx.x) * kSlice - shift;
-    // the four logits begin `off` elements into an aligned group of four
-    const int off = static_cast<int>(((reinterpret_cast<uintptr_t>(x) >> 1) + 4 - shift) & 3u);
-    uint2 lo[kSteps], hi[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int v = v0 + 4 * (tid + i * kLogitsThreads) - off;
-        const bool inner = v >= 0 && v + (off ? 8 : 4) <= a.V;
-        lo[i] = hi[i] = make_uint2(0u, 0u);
-        if (inner) {
-            lo[i] = __ldcs(reinterpret_cast<const uint2 *>(x + v));
-            if (off) hi[i] = __ldcs(reinterpret_cast<const uint2 *>(x + v + 4));
-        }
-    }
-    // and the mask's words; a row's first group of four may begin before it
-    const uint32_t *mask = a.r.mask ? a.r.mask + row * a.r.ld_mask : nullptr;
-    uint32_t m_lo[kSteps], m_hi[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int v = v0 + 4 * (tid + i * kLogitsThreads), m = max(v, 0);
-        m_lo[i] = m_hi[i] = ~0u;
-        if (mask && m < a.V) {
-            m_lo[i] = __ldg(mask + (m >> 5));
-            m_hi[i] = (m & 31) > 28 ? __ldg(mask + (min(m + 3, a.V - 1) >> 5)) : 0u;
-        }
-    }
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const bool hist = a.r.ids != nullptr, bias = a.r.bias_ids != nullptr, some = hist || bias;
     const int end = hist ? a.r.end[row] : 0, mid = hist ? a.r.mid[row] : 0, begin = hist ? a.r.begin[row] : 0;
+    Row r;
+    r.x = a.logits + row * a.ldl;
+    r.out = a.out ? a.out + row * a.ldo : nullptr;
+    r.mask = a.r.mask ? a.r.mask + row * a.r.ld_mask : nullptr;
+    r.V = a.V;
+    const int shift = r.out ? static_cast<int>((reinterpret_cast<uintptr_t>(r.out) >> 2) & 3u)
+                            : static_cast<int>((reinterpret_cast<uintptr_t>(r.x) >> 1) & 3u);
+    r.off = static_cast<int>(((reinterpret_cast<uintptr_t>(r.x) >> 1) + 4 - shift) & 3u);
+    const int v0 = static_cast<int>(blockIdx.x) * kSlice - shift;
+    const bool edge = v0 < 4 || v0 + kSlice + 8 > a.V;                // some group of the slice is not whole
+
+    // a batch of the slice's logits and mask words
+    uint2 lo[BATCH], hi[BATCH];
+    uint32_t m_lo[BATCH], m_hi[BATCH];
+    auto load = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int v = v0 + 4 * (tid + (step + i) * kLogitsThreads);
+            lo[i] = hi[i] = make_uint2(0u, 0u);
+            m_lo[i] = m_hi[i] = ~0u;
+            if (!edge || r.inner(v)) {
+                lo[i] = __ldcs(reinterpret_cast<const uint2 *>(r.x + v - r.off));
+                if (r.off) hi[i] = __ldcs(reinterpret_cast<const uint2 *>(r.x + v - r.off + 4));
+            }
+            if (r.mask && (!edge || v < a.V)) {
+                m_lo[i] = __ldg(r.mask + (max(v, 0) >> 5));
+                if (v0 & 3) m_hi[i] = __ldg(r.mask + (min(max(v, 0) + 3, a.V - 1) >> 5));   // it may lie in two words
+            }
+        }
+    };
+    load(0);
     const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
     const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
-    if (tid == 0) {
-        best = 0;
-        n_listed = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        if (some) reinterpret_cast<uint4 *>(held)[tid + i * kLogitsThreads] = make_uint4(0u, 0u, 0u, 0u);
-        if (bias) reinterpret_cast<uint2 *>(biased)[tid + i * kLogitsThreads] = make_uint2(0u, 0u);
-    }
-    __syncthreads();
-    // ids of the slice: v0 <= id < v0 + kSlice, and 0 <= id < V
+    if (tid == 0) best = 0;
+
+    // the slice's ids: v0 <= id < v0 + kSlice, and 0 <= id < V
     const int first = max(v0, 0), past = min(v0 + kSlice, a.V);
-    if (hist) {
-#pragma unroll 4
-        for (int i = begin + tid; i < end; i += kLogitsThreads) {
-            const int id = __ldg(a.r.ids + i);
-            if (id >= first && id < past) {
-                if (atomicOr(&held[id - v0], 0x80000000u) == 0u) listed[atomicAdd(&n_listed, 1)] = static_cast<uint16_t>(id - v0);
-                if (i >= mid) atomicAdd(&held[id - v0], 1u);
+    const unsigned n_ids = past > first ? past - first : 0;
+    // f(i, element of the slice) for the history's: aligned fours from vb to ve, at most three ids before and after them
+    const int head = hist ? static_cast<int>((0u - static_cast<unsigned>(reinterpret_cast<uintptr_t>(a.r.ids + begin) >> 2)) & 3u) : 0;
+    const int vb = min(begin + head, max(begin, end)), ve = vb + (max(end - vb, 0) & ~3);
+    auto history = [&](auto f) {
+        auto one = [&](int i, int id) {
+            if (static_cast<unsigned>(id) - first < n_ids && id >= 0) f(i, id - v0);
+        };
+        if (tid < vb - begin) one(begin + tid, __ldg(a.r.ids + begin + tid));
+        if (tid < end - ve) one(ve + tid, __ldg(a.r.ids + ve + tid));
+        for (int i0 = vb + 4 * tid; i0 < ve; i0 += 4 * kIds * kLogitsThreads) {
+            int4 id[kIds];                                 // loads first: a mark in between would hold up the next
+#pragma unroll
+            for (int j = 0; j < kIds; ++j) {
+                const int i = i0 + 4 * j * kLogitsThreads;
+                id[j] = i < ve ? __ldg(reinterpret_cast<const int4 *>(a.r.ids + i)) : make_int4(-1, -1, -1, -1);
+            }
+#pragma unroll
+            for (int j = 0; j < kIds; ++j) {
+                const int i = i0 + 4 * j * kLogitsThreads;
+                one(i, id[j].x);
+                one(i + 1, id[j].y);
+                one(i + 2, id[j].z);
+                one(i + 3, id[j].w);
             }
         }
-    }
-    if (bias) {
-        __syncthreads();                                   // an element is listed by whoever finds its word zero
+    };
+    auto biases = [&](auto f) {
         for (int i = tid; i < a.r.n_bias; i += kLogitsThreads) {
             const int id = __ldg(a.r.bias_ids + static_cast<int64_t>(row) * a.r.n_bias + i);
-            if (id >= first && id < past) {
-                if (atomicOr(&held[id - v0], 0x40000000u) == 0u) listed[atomicAdd(&n_listed, 1)] = static_cast<uint16_t>(id - v0);
-                max_u16(biased, id - v0, static_cast<uint32_t>(i + 1));
-            }
+            if (id >= first && id < past) f(i, id - v0);
         }
+    };
+    int n = 0;                                             // marked elements
+    if (some) {
+        for (int i = tid; i < kWords / 4; i += kLogitsThreads)
+            reinterpret_cast<uint4 *>(marked)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        auto mark = [&](int, int k) { atomicOr(&marked[k >> 5], 1u << (k & 31)); };
+        if (hist) history(mark);
+        if (bias) biases(mark);
+        __syncthreads();
+        // ranks: a run of words a thread, over the warp, over the warps
+        constexpr int kRun = (kWords + kLogitsThreads - 1) / kLogitsThreads;
+        int c = 0;
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+            if (tid * kRun + j < kWords) c += __popc(marked[tid * kRun + j]);
+        int sum = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (lane == 31) warp_marks[tid >> 5] = sum;
+        __syncthreads();
+        int at = sum - c;
+#pragma unroll
+        for (int w = 0; w < kLogitsThreads / 32; ++w) {
+            if (w < tid >> 5) at += warp_marks[w];
+            n += warp_marks[w];
+        }
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+            if (tid * kRun + j < kWords) {
+                rank[tid * kRun + j] = static_cast<uint16_t>(at);
+                at += __popc(marked[tid * kRun + j]);
+            }
     }
-    __syncthreads();
+    // counts, list and biases of the marked elements of ranks from .. from + kMarks - 1
+    auto collect = [&](int from) {
+        const int here = min(n - from, kMarks);
+        for (int i = tid; i < here; i += kLogitsThreads) {
+            held[i] = 0u;
+            biased[i] = 0;
+        }
+        __syncthreads();
+        auto slot = [&](int k) {
+            const uint32_t w = marked[k >> 5];
+            return rank[k >> 5] + __popc(w & ((1u << (k & 31)) - 1u)) - from;
+        };
+        if (hist)
+            history([&](int i, int k) {
+                const int s = slot(k);
+                if (s < 0 || s >= kMarks) return;
+                if (i >= mid) atomicAdd(&held[s], 1u);
+                else atomicOr(&held[s], 0x80000000u);
+                listed[s] = static_cast<uint16_t>(k);
+            });
+        if (bias)
+            biases([&](int i, int k) {
+                const int s = slot(k);
+                if (s < 0 || s >= kMarks) return;
+                atomicOr(&held[s], 0x40000000u);
+                max_u16(biased, s, static_cast<uint32_t>(i + 1));
+                listed[s] = static_cast<uint16_t>(k);
+            });
+        __syncthreads();
+        return here;
+    };
+    int here = 0, k_own = 0;
+    uint32_t x_own = 0, m_own = ~0u;
+    auto own = [&](int i) {
+        k_own = listed[i];
+        x_own = r.x[v0 + k_own];
+        if (r.mask) m_own = __ldg(r.mask + ((v0 + k_own) >> 5));
+    };
+    if (n > 0) {
+        here = collect(0);
+        if (tid < here) own(tid);                          // the thread's first, on its way during the stream
+    }
 
     float top = -INFINITY;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int k = tid + i * kLogitsThreads, v = v0 + 4 * k;
-        if (v + 4 <= 0 || v >= a.V) continue;
+    int top_at = 0;
+    // one step; EDGE: of a slice with groups that are not whole
+    auto one_step = [&](int i, int number, auto is_edge) {
+        constexpr bool EDGE = decltype(is_edge)::value;
+        const int k = tid + number * kLogitsThreads, v = v0 + 4 * k;
+        if (EDGE && (v + 4 <= 0 || v >= a.V)) return;
         float y[4];
-        if (v - off >= 0 && v - off + (off ? 8 : 4) <= a.V) {
-            // elements off .. off + 3 of the eight
-            const uint32_t w[4] = {lo[i].x, lo[i].y, hi[i].x, hi[i].y};
-            const uint32_t p = off & 2 ? w[1] : w[0], q = off & 2 ? w[2] : w[1], r = off & 2 ? w[3] : w[2];
-            const uint32_t z0 = off & 1 ? __byte_perm(p, q, 0x5432) : p, z1 = off & 1 ? __byte_perm(q, r, 0x5432) : q;
-            y[0] = bf16_lo(z0), y[1] = bf16_hi(z0), y[2] = bf16_lo(z1), y[3] = bf16_hi(z1);
-        } else {
+        four<EDGE>(r, v, lo[i], hi[i], y);
+        uint32_t bits = mask_bits(m_lo[i], m_hi[i], v);
+        if (some) bits &= ~(marked[k >> 3] >> (4 * (k & 7)));
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[e] = v + e >= 0 && v + e < a.V ? __uint_as_float(static_cast<uint32_t>(x[v + e]) << 16) : -INFINITY;
-        }
-        if (mask) {
-            const int m = max(v, 0);
-            const uint32_t bits = __funnelshift_r(m_lo[i], m_hi[i], m & 31) << (m - v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = (bits >> e) & 1u ? y[e] : -INFINITY;
-        }
-        if (out) {
-            if (v >= 0 && v + 4 <= a.V) {
-                __stcs(reinterpret_cast<float4 *>(out + v), make_float4(y[0], y[1], y[2], y[3]));
+        for (int e = 0; e < 4; ++e) y[e] = bits & (1u << e) ? y[e] : -INFINITY;
+        if (r.out) {
+            if (!EDGE || (v >= 0 && v + 4 <= a.V)) {
+                __stcs(reinterpret_cast<float4 *>(r.out + v), make_float4(y[0], y[1], y[2], y[3]));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (v + e >= 0 && v + e < a.V) out[v + e] = y[e];
-            }
-        }
-        if (some) {
-            const uint4 c = reinterpret_cast<const uint4 *>(held)[k];
-            if (c.x | c.y | c.z | c.w) {
-                y[0] = c.x ? -INFINITY : y[0];
-                y[1] = c.y ? -INFINITY : y[1];
-                y[2] = c.z ? -INFINITY : y[2];
-                y[3] = c.w ? -INFINITY : y[3];
+                    if (v + e >= 0 && v + e < a.V) r.out[v + e] = y[e];
             }
         }
         const float most = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-        if (most > top) {                                  // rare after a few; the lowest element of the largest value
-            top = most;
-            at = v + (y[0] == most ? 0 : y[1] == most ? 1 : y[2] == most ? 2 : 3);
+        const int at = v + (y[0] == most ? 0 : y[1] == most ? 1 : y[2] == most ? 2 : 3);
+        top_at = most > top ? at : top_at;
+        top = fmaxf(top, most);
+    };
+#pragma unroll 1
+    for (int s = 0; s < STEPS; s += BATCH) {
+        if (edge) {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) one_step(i, s + i, std::true_type());
+        } else {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) one_step(i, s + i, std::false_type());
         }
+        if (s + BATCH < STEPS) load(s + BATCH);
     }
-    unsigned long long key = key_of(top, at);
-    if (some) {
+    unsigned long long key = key_of(top, top_at);
+    if (n > 0) {
         __syncthreads();                                   // the stream's stores come before these
-        for (int i = tid; i < n_listed; i += kLogitsThreads) {
-            const int k = listed[i], v = v0 + k;
-            const uint32_t c = held[k], n = c & 0x3FFFFFFFu;
-            float z = __uint_as_float(static_cast<uint32_t>(x[v]) << 16);
-            if (c & 0x80000000u) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-            if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, static_cast<float>(n))), pres);
-            if (c & 0x40000000u) z = __fadd_rn(z, __ldg(a.r.bias + static_cast<int64_t>(row) * a.r.n_bias + biased[k] - 1));
-            if (mask && !((__ldg(mask + (v >> 5)) >> (v & 31)) & 1u)) z = -INFINITY;
-            if (out) out[v] = z;
-            const unsigned long long kz = key_of(z, v);
-            key = kz > key ? kz : key;
+        for (int from = 0;;) {
+            for (int i = tid; i < here; i += kLogitsThreads) {
+                if (i != tid || from > 0) own(i);
+                const int v = v0 + k_own;
+                const uint32_t c = held[i], times = c & 0x3FFFFFFFu;
+                float z = __uint_as_float(x_own << 16);
+                if ((c & 0x80000000u) || times) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+                if (times) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, static_cast<float>(times))), pres);
+                if (c & 0x40000000u)
+                    z = __fadd_rn(z, __ldg(a.r.bias + static_cast<int64_t>(row) * a.r.n_bias + biased[i] - 1));
+                if (!((m_own >> (v & 31)) & 1u)) z = -INFINITY;
+                if (r.out) r.out[v] = z;
+                const unsigned long long kz = key_of(z, v);
+                key = kz > key ? kz : key;
+            }
+            from += kMarks;
+            if (from >= n) break;
+            __syncthreads();
+            here = collect(from);
         }
     }
     if (!a.argmax) return;
@@ -216,41 +351,38 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(LogitsArgs a, in
         const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
         key = k > key ? k : key;
     }
-    if ((tid & 31) == 0) atomicMax(&best, key);
+    __syncthreads();                                       // best is zero
+    if (lane == 0) atomicMax(&best, key);
     __syncthreads();
     if (tid == 0) {
-        RowKey *r = static_cast<RowKey *>(a.ws) + row;
-        if (best) atomicMax(&r->key, best);
-        if (atom_add_acq_rel_gpu(&r->done, 1) == static_cast<int>(gridDim.x) - 1) {
-            const unsigned long long k = atomicExch(&r->key, 0ull);
+        RowKey *rk = static_cast<RowKey *>(a.ws) + row;
+        if (best) atomicMax(&rk->key, best);
+        if (atom_add_acq_rel_gpu(&rk->done, 1) == static_cast<int>(gridDim.x) - 1) {
+            const unsigned long long k = atomicExch(&rk->key, 0ull);
             a.argmax[row] = k ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k)) : -1;
-            r->done = 0;
+            rk->done = 0;
         }
     }
 }
 
-template <int N>
+template <int STEPS, int BATCH>
 cudaError_t launch(const LogitsArgs &a, bool pdl, cudaStream_t stream)
 {
-    constexpr int slice = kLogitsThreads * N;
-    // room for the history's counts and the biases, as far as there are such
-    const int bytes = a.r.bias_ids ? 8 * slice : a.r.ids ? 6 * slice : 0;
-    if (bytes + 1024 > 48 * 1024) {                        // with the kernel's own, more than any launch may have
-        const cudaError_t e = cudaFuncSetAttribute(logits_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * slice);
-        if (e != cudaSuccess) return e;
-    }
+    constexpr int slice = 4 * kLogitsThreads * STEPS;
+    constexpr LogitsPlan plan(slice);
+    static_assert(slice <= 65536 && plan.bytes + 1024 <= 48 * 1024, "16-bit places, and no more than any launch may have");
     cudaLaunchConfig_t cfg = {};
     // up to 3 elements of shift
     cfg.gridDim = dim3(static_cast<unsigned>((a.V + 3 + slice - 1) / slice), static_cast<unsigned>(a.M));
     cfg.blockDim = dim3(kLogitsThreads);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.dynamicSmemBytes = a.r.ids || a.r.bias_ids ? plan.bytes : 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, logits_kernel<N>, a, pdl ? 1 : 0);
+    return cudaLaunchKernelEx(&cfg, logits_kernel<STEPS, BATCH>, a, pdl ? 1 : 0);
 }
 
 }  // namespace
@@ -260,7 +392,8 @@ size_t logits_workspace(int M) { return sizeof(RowKey) * static_cast<size_t>(M);
 cudaError_t launch_logits_process(const LogitsArgs &a, int sms, bool pdl, cudaStream_t stream)
 {
     // short slices while the long ones would leave SMs idle: each slice reads the row's history again
-    return static_cast<int64_t>(a.M) * ((a.V + 8191) / 8192) < 2 * sms ? launch<8>(a, pdl, stream) : launch<32>(a, pdl, stream);
+    const int64_t slices = static_cast<int64_t>(a.M) * ((a.V + 16383) / 16384);
+    return slices < 4 * sms ? launch<2, 2>(a, pdl, stream) : launch<16, 4>(a, pdl, stream);
 }
 
 }  // namespace bi

@@ -529,6 +529,28 @@ def test_logits_many_rows(bi):
     assert not ws.any()
 
 
+def test_logits_more_marked_elements_than_are_done_at_once(bi):
+    """A history that meets nearly every element of its row, in rows of long and of short slices."""
+    rng = np.random.default_rng(22)
+    V = 16500
+    for M in (1, 320):
+        x = bits(rng, (M, V), 3.0)
+        n = 40000
+        ids = rng.integers(0, V, n).astype(np.int32)
+        begin = np.full(M, 3, np.int32)
+        r = dict(ids=ids, begin=begin, mid=begin + 12345, end=np.full(M, n - 1, np.int32),
+                 repetition=np.full(M, 1.25, np.float32), presence=rng.normal(size=M).astype(np.float32),
+                 frequency=rng.normal(size=M).astype(np.float32), bias_ids=rng.integers(0, V, (M, 300)).astype(np.int32),
+                 bias=rng.normal(size=(M, 300)).astype(np.float32))
+        out, am = torch.empty((M, V), device=DEV), torch.empty(M, dtype=torch.int32, device=DEV)
+        ws = bi.new_logits_workspace(M)
+        bi.bi_logits_process(dev(x), bi.logits_rules(**{k: dev(v) for k, v in r.items()}), out, am, ws)
+        some = slice(0, 2)
+        want, best = ref.logits_process(x[some], V, **{k: v if k == "ids" else v[some] for k, v in r.items()})
+        same(host(out)[some], want, "logits")
+        same(host(am)[some], best, "argmax")
+
+
 def test_attention_leaves_out_tokens_past_the_bound(bi):
     """Tokens past max_q have zeros, those before it their result, also where T does not show that there are any."""
     rng = np.random.default_rng(12)
