@@ -358,36 +358,34 @@ struct SpanArgs {
     int pdl;
 };
 
+// What a CTA finds before it knows how many rows it has.
+struct Task {
+    int rank, hk, rb, b, span;
+    int my_pos, page;                            // the lane's 16 positions and their page
+    int cu0, cu1, len;
+};
+
+// One span (SPLIT: the CTA's eighth of it) for rows block_rows rb .. of a kv head, at most 8 NB.
 template <int D, int NB, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : D * NB > 64 || SPLIT ? 4 : 5) attn_kv4_span_kernel(SpanArgs p)
+__device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, int block_rows, unsigned char *smem)
 {
     using P = Plan<D, NB, SPLIT>;
     constexpr int G = P::G, W = P::kPiece / 4, BLOCKS = P::kBlocks;
-    extern __shared__ __align__(16) unsigned char smem[];
     const AttnKv4Args &a = p.a;
     const Kv4View &c = a.c;
-    // the spans are the slowest axis: the short last spans of a batch come last
-    const int rank = SPLIT ? blockIdx.x % kCluster : 0, task = SPLIT ? blockIdx.x / kCluster : blockIdx.x;
-    const int hk = task / p.row_blocks, rb = task - hk * p.row_blocks, b = blockIdx.y, span = blockIdx.z;
+    const int rank = task.rank, rb = task.rb, b = task.b, span = task.span, my_pos = task.my_pos;
+    int page = task.page;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if (p.pdl) pdl_wait();
-    pdl_launch_dependents();
-
-    // the warp's blocks are 4 rank + warp and every fourth after it; lane 4 j + i looks after positions 16 i .. of the
-    // j-th: their page (the lengths are on their way meanwhile)
     const int p0 = span * kSpan, pw = p0 + (rank * kChunks + warp) * kBlock;
     constexpr int kStep = kChunks * kBlock;
-    const int my_pos = pw + (lane >> 2) * kStep + 16 * (lane & 3);
-    int page = lane < BLOCKS * 4 ? kv4_page(c, b, my_pos) : -1;
-    const int cu0 = __ldg(c.cu_q + b), cu1 = __ldg(c.cu_q + b + 1), len = __ldg(c.kv_len + b);
     Rows rows;
-    rows.t0 = max(0, cu0);
+    rows.t0 = max(0, task.cu0);
     rows.GH = a.Hq / c.Hkv;
-    rows.hk = hk;
+    rows.hk = task.hk;
     rows.magic = p.magic;
-    rows.r0 = rb * P::R;
-    rows.first = len - (cu1 - cu0);                       // position of the first new token
-    const int tokens = min(c.T, cu1) - rows.t0, n_rows = min(tokens, c.max_q) * rows.GH;
+    rows.r0 = rb * block_rows;
+    rows.first = task.len - (task.cu1 - task.cu0);                       // position of the first new token
+    const int tokens = min(c.T, max(0, task.cu1)) - rows.t0, n_rows = min(tokens, c.max_q) * rows.GH;
     if (rb == 0 && span == 0 && rank == 0)                // tokens past max_q are left out: zeros
         for (int64_t i = static_cast<int64_t>(c.max_q) * rows.GH * (D / 4) + threadIdx.x;
              i < static_cast<int64_t>(tokens) * rows.GH * (D / 4); i += kThreads) {
@@ -948,6 +946,45 @@ __global__ void __launch_bounds__(kThreads, D * NB > 128 ? 3 : D * NB > 64 || SP
         }
         write_out<D>(a, at, d, v, sum);
     }
+}
+
+// CTAs a SM: the registers decide.  16 rows of head size 128 spill 300 bytes at three (b 64, q 8, 4096 positions:
+// 148 us, at two 140); 8 rows of it, or 16 of head size 64, wait less for one another's copies at three than at four
+// (b 96, 8191: 128 and 131 us; head size 64, b 6, q 5, 40000: 50 and 53); head size 64 wants five (b 64, 8192: 33 us, at
+// four 37).
+template <int D, int NB, bool SPLIT>
+constexpr int kCtasPerSm = D * NB > 128 && !SPLIT ? 2 : D * NB > 64 ? 3 : SPLIT ? 4 : 5;
+
+template <int D, int NB, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NB, SPLIT>) attn_kv4_span_kernel(SpanArgs p)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    const Kv4View &c = p.a.c;
+    // the spans are the slowest axis: the short last spans of a batch come last
+    Task task;
+    task.rank = SPLIT ? blockIdx.x % kCluster : 0;
+    const int x = SPLIT ? blockIdx.x / kCluster : blockIdx.x;
+    task.hk = x / p.row_blocks;
+    task.rb = x - task.hk * p.row_blocks;
+    task.b = blockIdx.y;
+    task.span = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (p.pdl) pdl_wait();
+    pdl_launch_dependents();
+
+    // the warp's blocks are 4 rank + warp and every fourth after it; lane 4 j + i looks after positions 16 i .. of the
+    // j-th: their page (the lengths are on their way meanwhile)
+    task.my_pos = task.span * kSpan + ((task.rank + (lane >> 2)) * kChunks + warp) * kBlock + 16 * (lane & 3);
+    task.page = lane < Plan<D, NB, SPLIT>::kBlocks * 4 ? kv4_page(c, task.b, task.my_pos) : -1;
+    task.cu0 = __ldg(c.cu_q + task.b);
+    task.cu1 = __ldg(c.cu_q + task.b + 1);
+    task.len = __ldg(c.kv_len + task.b);
+    if constexpr (NB == 2) {
+        // a last block of at most 8 rows does not pay for 16
+        const int n_rows = min(min(c.T, max(0, task.cu1)) - max(0, task.cu0), c.max_q) * (p.a.Hq / c.Hkv);
+        if (n_rows - task.rb * 16 <= 8) return span_task<D, 1, SPLIT>(p, task, 16, smem);
+    }
+    span_task<D, NB, SPLIT>(p, task, 8 * NB, smem);
 }
 
 // One CTA per (token, q head), where the span kernel does not join a row's
