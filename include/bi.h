@@ -212,6 +212,7 @@ BI_API bi_status bi_lmhead_argmax(const int8_t *q, const float *s_a, int M, int 
  * that kernels set when a bounded wait gives up, clears it, and returns BI_OK
  * or BI_ERR_TIMEOUT (or BI_ERR_CUDA if the stream itself reports an error).
  * After BI_ERR_TIMEOUT the workspace must be zero-filled again before reuse.
+ * For workspaces of linear calls, programs and bi_attention_kv4.
  */
 BI_API bi_status bi_workspace_status(void *ws, size_t ws_bytes, bi_stream_t stream);
 
@@ -487,7 +488,8 @@ BI_API bi_status bi_kv4_gather(const bi_kv4_cache *cache, const bi_kv4_batch *ba
  *       16-byte aligned, zero-filled before its first use; every call that
  *       completes leaves it ready for the next.  Its layout depends on no
  *       argument, so one workspace of the largest size serves calls of any
- *       shape on one stream.
+ *       shape on one stream.  A copy that does not arrive within the wait limit
+ *       is reported by bi_workspace_status as BI_ERR_TIMEOUT.
  * Scores, softmax sums and outputs are fp32; the products run on the tensor
  * cores with the codes exact and q exact but for elements 2^-24 below its
  * head's largest, and the weights in f16 with 11 bits.  A query's result

@@ -319,13 +319,19 @@ def new_kv4_pool(num_pages: int, Hkv: int, page_size: int, D: int, device="cuda"
 
 def kv4_batch(cu_q: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, T: int, max_q: int,
               max_kv: int) -> bi_kv4_batch:
-    """cu_q int32 [B + 1], kv_len int32 [B], pages int32 [B, n] (row stride pages.stride(0)); T, max_q, max_kv: bounds
+    """cu_q int32 [B + 1], kv_len int32 [B], pages int32 [B, n]; T, max_q, max_kv: bounds
     known to the host.  The caller keeps the tensors alive."""
     B = kv_len.shape[0]
     assert cu_q.dtype == kv_len.dtype == pages.dtype == torch.int32
     assert cu_q.shape[0] == B + 1 and cu_q.is_contiguous() and kv_len.is_contiguous()
     assert pages.shape[0] == B and pages.is_contiguous()
     return bi_kv4_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, T, max_q, max_kv)
+
+
+def _is_heads(t: torch.Tensor, D: int) -> bool:
+    """16-bit elements [T, H, D], the heads of a row side by side."""
+    return (t.element_size() == 2 and t.dim() == 3 and t.shape[2] == D and t.stride(2) == 1 and
+            (t.stride(1) == D or t.shape[1] == 1))
 
 
 def bi_rope_table(inv_freq: torch.Tensor, rope: torch.Tensor, amp: float = 1.0, stream=None) -> None:
@@ -341,6 +347,11 @@ def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: 
                        k_norm: torch.Tensor | None = None, eps: float = 0.0, flags: int = 0, stream=None) -> None:
     """q: bf16 [T, Hq, D], k, v: bf16 [T, Hkv, D] (row strides stride(0); parts of one packed tensor will do);
     rope: fp32 [positions, rot / 2, 2]; q_norm, k_norm: bf16 [D] or None; q_out: bf16 [T, Hq, D]."""
+    T, D = batch.T, cache.D
+    assert _is_heads(q, D) and _is_heads(k, D) and _is_heads(v, D) and min(q.shape[0], k.shape[0], v.shape[0]) >= T
+    assert k.shape[1] == v.shape[1] == cache.Hkv
+    assert _is_heads(q_out, D) and q_out.shape[1] == q.shape[1] and q_out.shape[0] >= T and q_out.is_contiguous()
+    assert rope.dtype == torch.float32 and rope.is_contiguous()
     _check(lib.bi_rope_append_kv4(q.data_ptr(), q.stride(0), q.shape[1], k.data_ptr(), k.stride(0), v.data_ptr(),
                                   v.stride(0), _ptr(q_norm), _ptr(k_norm), eps, rope.data_ptr(), rope.shape[0], rot,
                                   layout, q_out.data_ptr(), cache, batch, flags, _stream(stream)), "bi_rope_append_kv4")
@@ -349,6 +360,9 @@ def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: 
 def bi_kv4_gather(cache: bi_kv4_cache, batch: bi_kv4_batch, k_out: torch.Tensor, v_out: torch.Tensor,
                   stream=None) -> None:
     """k_out, v_out: bf16 [T, Hkv, D], the cached values of the batch's token rows."""
+    for t in (k_out, v_out):
+        assert t.element_size() == 2 and t.is_contiguous()
+        assert t.shape[1:] == (cache.Hkv, cache.D) and t.shape[0] >= batch.T
     _check(lib.bi_kv4_gather(cache, batch, k_out.data_ptr(), v_out.data_ptr(), _stream(stream)), "bi_kv4_gather")
 
 
@@ -364,6 +378,8 @@ def new_attention_kv4_workspace(Hq: int, cache: bi_kv4_cache, batch: bi_kv4_batc
 def bi_attention_kv4(q: torch.Tensor, cache: bi_kv4_cache, batch: bi_kv4_batch, scale: float, o: torch.Tensor,
                      ws: torch.Tensor, flags: int = 0, stream=None) -> None:
     """q: bf16 [T, Hq, D] (row stride q.stride(0)); o: bf16 [T, Hq, D] out; ws: from new_attention_kv4_workspace."""
+    assert _is_heads(q, cache.D) and _is_heads(o, cache.D) and o.shape == q.shape and q.shape[0] >= batch.T
+    assert o.stride(0) == q.shape[1] * cache.D or q.shape[0] == 1
     _check(lib.bi_attention_kv4(q.data_ptr(), q.stride(0), q.shape[1], cache, batch, scale, o.data_ptr(), ws.data_ptr(),
                                 ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_attention_kv4")
 
@@ -381,10 +397,11 @@ def logits_rules(ids: torch.Tensor | None = None, begin: torch.Tensor | None = N
         assert t is None or t.dtype == torch.float32
     for t in (ids, begin, mid, end, repetition, presence, frequency, bias_ids, bias):
         assert t is None or t.is_contiguous()
+    assert mask is None or mask.stride(1) == 1 or mask.shape[1] == 1
     n = 0 if bias_ids is None else bias_ids.shape[1]
     return bi_logits_rules(_ptr(ids), _ptr(begin), _ptr(mid), _ptr(end), _ptr(repetition), _ptr(presence),
                            _ptr(frequency), _ptr(bias_ids), _ptr(bias), n, _ptr(mask),
-                           0 if mask is None else max(mask.stride(0), mask.shape[1]))
+                           0 if mask is None else mask.stride(0) if mask.shape[0] > 1 else mask.shape[1])
 
 
 def bi_logits_workspace_size(M: int) -> int:
@@ -400,6 +417,8 @@ def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.T
                       argmax: torch.Tensor | None, ws: torch.Tensor, flags: int = 0, stream=None) -> None:
     """logits: bf16 [M, V] (row stride logits.stride(0)); out: fp32 [M, V] or None; argmax: int32 [M] or None."""
     M, V = logits.shape
+    assert logits.element_size() == 2 and logits.stride(1) == 1
+    assert out is None or (out.dtype == torch.float32 and out.stride(1) == 1)
     _check(lib.bi_logits_process(logits.data_ptr(), logits.stride(0), M, V, rules, _ptr(out),
                                  0 if out is None else out.stride(0), _ptr(argmax), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_logits_process")

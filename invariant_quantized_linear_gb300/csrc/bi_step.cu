@@ -2,8 +2,10 @@
 // Declarations and the contract of every entry point are in include/bi.h.
 #include "bi.h"
 #include "host_common.h"
+#include "kernels.cuh"
 #include "step.cuh"
 
+#include <algorithm>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -214,7 +216,8 @@ size_t bi_attention_kv4_workspace_size(int Hq, const bi_kv4_cache *cache, const 
         !head_size_ok(cache->D) || batch->B < 1 || batch->B > 65535 || batch->T < 1 || batch->T > kMaxTokens ||
         batch->max_q < 1 || batch->max_q > 65535 || batch->max_kv < 1 || batch->max_kv > kMaxPositions)
         return 0;
-    return bi::attention_kv4_workspace(Hq, cache->D, batch->T, batch->max_kv);
+    // at least what bi_workspace_status asks for
+    return std::max(bi::kWsBytes, bi::attention_kv4_workspace(Hq, cache->D, batch->T, batch->max_kv));
 }
 
 bi_status bi_attention_kv4(const uint16_t *q, int64_t ldq, int Hq, const bi_kv4_cache *cache, const bi_kv4_batch *batch,

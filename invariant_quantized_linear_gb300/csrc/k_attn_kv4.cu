@@ -445,7 +445,11 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
     };
     int *status = static_cast<int *>(a.ws);
     auto wait = [&](int which, int blk) {
-        if (!mbar_wait_bounded(bars + which, blk & 1, status)) *status = DEV_TIMEOUT;
+        if (!mbar_wait_bounded(bars + which, blk & 1, status)) {
+            *status = DEV_TIMEOUT;
+            volatile int never = 0;                        // the copies may not land after the CTA has gone
+            mbar_wait_bounded(bars + which, blk & 1, &never);
+        }
         __syncwarp();
     };
     copy_keys(0);

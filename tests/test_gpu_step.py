@@ -566,3 +566,19 @@ def test_attention_leaves_out_tokens_past_the_bound(bi):
     b.batch = bi.kv4_batch(*b.d, 5, 6, b.max_kv)              # rows from T on are not touched
     o = attend(bi, b, q, 0.1)
     assert torch.equal(o[:5], whole[:5]) and (o[5:] == 7).all()
+
+
+def test_attention_status(bi):
+    """A call leaves the status at BI_OK; what a timeout would leave (set here) is reported once."""
+    rng = np.random.default_rng(13)
+    seqs = [(1, 70)]
+    b = Batch(bi, seqs, 1, 64, 16)
+    b.fill(0, *kv(rng, seqs, 1, 64))
+    b.to_device()
+    ws = bi.new_attention_kv4_workspace(2, b.cache, b.batch)
+    o = torch.empty((1, 2, 64), dtype=torch.int16, device=DEV)
+    bi.bi_attention_kv4(dev(bits(rng, (1, 2, 64))), b.cache, b.batch, 0.1, o, ws)
+    assert bi.bi_workspace_status(ws) == bi.BI_OK
+    ws.view(torch.int32)[0] = 1
+    assert bi.bi_workspace_status(ws) == bi.BI_ERR_TIMEOUT
+    assert bi.bi_workspace_status(ws) == bi.BI_OK

@@ -5,6 +5,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from tests import step_ref as ref
 
@@ -193,6 +194,45 @@ def test_reference_layout_round_trip(P, D):
         s = ref.f32(ref.quantise(want)[1]).astype(np.float64).repeat(ref.GROUP, -1)
         # half a step; the top code may fall short by the rounding of s (2^-8 of 15 steps)
         assert (np.abs(got - want) <= s * (0.5 + 15 * 2.0 ** -8 + 2.0 ** -16)).all()
+
+
+def test_half_rotation_is_in_steps_of_eight(bi):
+    f = calls(bi)["append"]
+    for rot in (4, 12, 124):
+        assert f(cache(bi), batch(bi), rot=rot, layout=bi.BI_ROPE_HALF) == bi.BI_ERR_INVALID_ARG, rot
+    for rot in (2, 6, 14):
+        assert f(cache(bi), batch(bi), rot=rot, layout=bi.BI_ROPE_INTERLEAVED) == bi.BI_ERR_INVALID_ARG, rot
+
+
+def test_attention_workspace_has_a_status(bi):
+    """Small calls' workspaces too are large enough for bi_workspace_status."""
+    need = bi.bi_linear_workspace_size(1, 1, 16)
+    assert bi.bi_attention_kv4_workspace_size(1, cache(bi, Hkv=1, D=64), batch(bi, B=1, T=1, max_q=1, max_kv=1)) >= need
+    assert bi.bi_attention_kv4_workspace_size(8, cache(bi), batch(bi)) >= need
+
+
+def test_mask_of_one_row_for_all_is_refused(bi):
+    """A mask whose rows are one and the same (stride 0) is not read past its end."""
+    words = torch.zeros((1, 32), dtype=torch.int32)
+    assert bi.logits_rules(mask=words).ld_mask == 32
+    r = bi.logits_rules(mask=words.expand(4, 32))
+    assert bi.lib.bi_logits_process(FAKE, 1000, 4, 1000, r, FAR, 1000, 2 * FAR, 3 * FAR, 1 << 20, 0,
+                                    None) == bi.BI_ERR_INVALID_ARG
+
+
+def test_bindings_refuse_heads_that_are_not_side_by_side(bi):
+    c, b = cache(bi), batch(bi)
+    q = torch.zeros((6, 8, 128), dtype=torch.bfloat16)
+    for bad in (q.transpose(0, 1).contiguous().transpose(0, 1), q.float(), q[:5], q[..., :64]):
+        with pytest.raises(AssertionError):
+            bi.bi_attention_kv4(bad, c, b, 1.0, torch.zeros_like(q), torch.zeros(1), stream=0)
+    k = torch.zeros((6, 4, 128), dtype=torch.bfloat16)
+    rope = torch.zeros((10, 64, 2))
+    for qq, kk, vv in ((q, k[:, :3], k[:, :3]), (q, k[:5], k), (q, k, k.float())):
+        with pytest.raises(AssertionError):
+            bi.bi_rope_append_kv4(qq, kk, vv, rope, 128, 0, torch.zeros_like(q), c, b, stream=0)
+    with pytest.raises(AssertionError):
+        bi.bi_kv4_gather(c, b, k, k[:, :2], stream=0)
 
 
 def test_ctypes_structs_match_the_header(bi):
