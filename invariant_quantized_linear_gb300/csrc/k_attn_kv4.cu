@@ -578,10 +578,12 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
                     for (int half = 0; half < 2; ++half) {
                         const float sk = __uint_as_float(kp[tile][half][k] << 16);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                s[tile][nb][2 * half + i] = __fmaf_rn(sk, acc[tile][nb][2 * half + i], s[tile][nb][2 * half + i]);
+                        for (int nb = 0; nb < NB; ++nb) {
+                            float *u = s[tile][nb] + 2 * half;
+                            const float2 v = upk(fma2(pk(sk, sk), pk(acc[tile][nb][2 * half], acc[tile][nb][2 * half + 1]), pk(u[0], u[1])));
+                            u[0] = v.x;
+                            u[1] = v.y;
+                        }
                     }
             }
         }
@@ -668,7 +670,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
                     lb[nb] = add2(lb[nb], pk(w0, w1));
 #pragma unroll
                     for (int k = 0; k < G; ++k) {
-                        const __half2 h = __floats2half2_rn(w0 * sv[k], w1 * sv[k]);
+                        const float2 ws = upk(mul2(pk(w0, w1), pk(sv[k], sv[k])));
+                        const __half2 h = __floats2half2_rn(ws.x, ws.y);
                         w16[tile][k][nb][half] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h));
                     }
                 }
