@@ -101,13 +101,14 @@ __device__ __forceinline__ uint32_t mask_bits(uint32_t lo, uint32_t hi, int v)
 }
 
 constexpr int kMarks = 4096;             // marked elements of a slice done at once
+constexpr int kMet = 2048;               // history ids of a slice that are kept between the two passes over them
 
 // Shared memory for a slice of `slice` elements.
 struct LogitsPlan {
-    int rank, held, listed, biased, bytes;
+    int rank, held, listed, biased, met, bytes;
     __host__ __device__ constexpr LogitsPlan(int slice)
         : rank(slice / 8), held(rank + slice / 16), listed(held + 4 * kMarks), biased(listed + 2 * kMarks),
-          bytes(biased + 2 * kMarks)
+          met(biased + 2 * kMarks), bytes(met + 2 * kMet)
     {
     }
 };
@@ -116,7 +117,7 @@ struct LogitsPlan {
 template <int STEPS, int BATCH>
 __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(LogitsArgs a, int pdl)
 {
-    constexpr int kSlice = 4 * kLogitsThreads * STEPS, kWords = kSlice / 32;
+    constexpr int kStep = 4 * kLogitsThreads, kSlice = kStep * STEPS, kWords = kSlice / 32;
     constexpr LogitsPlan P(kSlice);
     extern __shared__ __align__(16) unsigned char smem[];
     uint32_t *marked = reinterpret_cast<uint32_t *>(smem);            // a bit an element
@@ -124,6 +125,9 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
     // of the marked elements, by rank: times generated, bit 31: in the prompt, bit 30: has a bias; which; its last bias + 1
     uint32_t *held = reinterpret_cast<uint32_t *>(smem + P.held);
     uint16_t *listed = reinterpret_cast<uint16_t *>(smem + P.listed), *biased = reinterpret_cast<uint16_t *>(smem + P.biased);
+    // the history's ids in the slice, in any order: element, bit 15: generated; as many as there is room for
+    uint16_t *met = reinterpret_cast<uint16_t *>(smem + P.met);
+    __shared__ int n_met;
     __shared__ unsigned long long best;
     __shared__ int warp_marks[kLogitsThreads / 32];
     if (pdl) {
@@ -142,24 +146,42 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
                             : static_cast<int>((reinterpret_cast<uintptr_t>(r.x) >> 1) & 3u);
     r.off = static_cast<int>(((reinterpret_cast<uintptr_t>(r.x) >> 1) + 4 - shift) & 3u);
     const int v0 = static_cast<int>(blockIdx.x) * kSlice - shift;
-    const bool edge = v0 < 4 || v0 + kSlice + 8 > a.V;                // some group of the slice is not whole
-
+    // whether some group of a batch is not whole: at a row's ends
+    auto edge = [&](int step) {
+        const int v = v0 + step * kStep;
+        return v < 4 || v + BATCH * kStep + 8 > a.V;
+    };
     // a batch of the slice's logits and mask words
+    const int own0 = v0 + 4 * tid;                         // the thread's groups begin here and every kStep elements
+    const uint16_t *const px = r.x + (own0 - r.off);
+    const uint32_t *const pm = r.mask ? r.mask + (own0 >> 5) : nullptr;
+    const int next = ((own0 + 3) >> 5) - (own0 >> 5);      // a group may lie in two words
     uint2 lo[BATCH], hi[BATCH];
     uint32_t m_lo[BATCH], m_hi[BATCH];
     auto load = [&](int step) {
+        const bool whole = !edge(step);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-            const int v = v0 + 4 * (tid + (step + i) * kLogitsThreads);
-            lo[i] = hi[i] = make_uint2(0u, 0u);
+            const int at = (step + i) * kStep, v = own0 + at;
+            hi[i] = make_uint2(0u, 0u);
             m_lo[i] = m_hi[i] = ~0u;
-            if (!edge || r.inner(v)) {
-                lo[i] = __ldcs(reinterpret_cast<const uint2 *>(r.x + v - r.off));
-                if (r.off) hi[i] = __ldcs(reinterpret_cast<const uint2 *>(r.x + v - r.off + 4));
-            }
-            if (r.mask && (!edge || v < a.V)) {
-                m_lo[i] = __ldg(r.mask + (max(v, 0) >> 5));
-                if (v0 & 3) m_hi[i] = __ldg(r.mask + (min(max(v, 0) + 3, a.V - 1) >> 5));   // it may lie in two words
+            if (whole) {
+                lo[i] = __ldcs(reinterpret_cast<const uint2 *>(px + at));
+                if (r.off) hi[i] = __ldcs(reinterpret_cast<const uint2 *>(px + at + 4));
+                if (pm) {
+                    m_lo[i] = __ldg(pm + at / 32);
+                    if (v0 & 3) m_hi[i] = __ldg(pm + at / 32 + next);
+                }
+            } else {
+                lo[i] = make_uint2(0u, 0u);
+                if (r.inner(v)) {
+                    lo[i] = __ldcs(reinterpret_cast<const uint2 *>(px + at));
+                    if (r.off) hi[i] = __ldcs(reinterpret_cast<const uint2 *>(px + at + 4));
+                }
+                if (pm && v < a.V) {
+                    m_lo[i] = __ldg(r.mask + (max(v, 0) >> 5));
+                    m_hi[i] = __ldg(r.mask + (min(max(v, 0) + 3, a.V - 1) >> 5));
+                }
             }
         }
     };
@@ -167,7 +189,7 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
     const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
     const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
-    if (tid == 0) best = 0;
+    if (tid == 0) best = 0, n_met = 0;
 
     // the slice's ids: v0 <= id < v0 + kSlice, and 0 <= id < V
     const int first = max(v0, 0), past = min(v0 + kSlice, a.V);
@@ -210,7 +232,12 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
             reinterpret_cast<uint4 *>(marked)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
         auto mark = [&](int, int k) { atomicOr(&marked[k >> 5], 1u << (k & 31)); };
-        if (hist) history(mark);
+        if (hist)
+            history([&](int i, int k) {
+                atomicOr(&marked[k >> 5], 1u << (k & 31));
+                const int at = atomicAdd(&n_met, 1);
+                if (at < kMet) met[at] = static_cast<uint16_t>(k | (i >= mid ? 0x8000 : 0));
+            });
         if (bias) biases(mark);
         __syncthreads();
         // ranks: a run of words a thread, over the warp, over the warps
@@ -252,14 +279,21 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
             const uint32_t w = marked[k >> 5];
             return rank[k >> 5] + __popc(w & ((1u << (k & 31)) - 1u)) - from;
         };
-        if (hist)
-            history([&](int i, int k) {
+        if (hist) {
+            auto count = [&](bool generated, int k) {
                 const int s = slot(k);
                 if (s < 0 || s >= kMarks) return;
-                if (i >= mid) atomicAdd(&held[s], 1u);
+                if (generated) atomicAdd(&held[s], 1u);
                 else atomicOr(&held[s], 0x80000000u);
                 listed[s] = static_cast<uint16_t>(k);
-            });
+            };
+            const int m = n_met;
+            if (m <= kMet) {
+                for (int i = tid; i < m; i += kLogitsThreads) count(met[i] & 0x8000u, met[i] & 0x7FFF);
+            } else {
+                history([&](int i, int k) { count(i >= mid, k); });
+            }
+        }
         if (bias)
             biases([&](int i, int k) {
                 const int s = slot(k);
@@ -285,20 +319,23 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
 
     float top = -INFINITY;
     int top_at = 0;
-    // one step; EDGE: of a slice with groups that are not whole
+    // one step; EDGE: of a batch with groups that are not whole
+    float *const po = r.out + own0;                        // used where r.out is given
+    const uint32_t *const my_marks = marked + (tid >> 3);
+    const int mark_shift = 4 * (tid & 7);
     auto one_step = [&](int i, int number, auto is_edge) {
         constexpr bool EDGE = decltype(is_edge)::value;
-        const int k = tid + number * kLogitsThreads, v = v0 + 4 * k;
+        const int v = own0 + number * kStep;
         if (EDGE && (v + 4 <= 0 || v >= a.V)) return;
         float y[4];
         four<EDGE>(r, v, lo[i], hi[i], y);
-        uint32_t bits = mask_bits(m_lo[i], m_hi[i], v);
-        if (some) bits &= ~(marked[k >> 3] >> (4 * (k & 7)));
+        uint32_t bits = EDGE ? mask_bits(m_lo[i], m_hi[i], v) : __funnelshift_r(m_lo[i], m_hi[i], own0);   // by own0 % 32
+        if (some) bits &= ~(my_marks[number * (kStep / 32)] >> mark_shift);
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = bits & (1u << e) ? y[e] : -INFINITY;
         if (r.out) {
             if (!EDGE || (v >= 0 && v + 4 <= a.V)) {
-                __stcs(reinterpret_cast<float4 *>(r.out + v), make_float4(y[0], y[1], y[2], y[3]));
+                __stcs(reinterpret_cast<float4 *>(po + number * kStep), make_float4(y[0], y[1], y[2], y[3]));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -312,7 +349,7 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
     };
 #pragma unroll 1
     for (int s = 0; s < STEPS; s += BATCH) {
-        if (edge) {
+        if (edge(s)) {
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) one_step(i, s + i, std::true_type());
         } else {
@@ -370,7 +407,7 @@ cudaError_t launch(const LogitsArgs &a, bool pdl, cudaStream_t stream)
 {
     constexpr int slice = 4 * kLogitsThreads * STEPS;
     constexpr LogitsPlan plan(slice);
-    static_assert(slice <= 65536 && plan.bytes + 1024 <= 48 * 1024, "16-bit places, and no more than any launch may have");
+    static_assert(slice <= 32768 && plan.bytes + 1024 <= 48 * 1024, "15-bit places, and no more than any launch may have");
     cudaLaunchConfig_t cfg = {};
     // up to 3 elements of shift
     cfg.gridDim = dim3(static_cast<unsigned>((a.V + 3 + slice - 1) / slice), static_cast<unsigned>(a.M));
