@@ -186,6 +186,10 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
         }
     };
     load(0);
+    if (STEPS > BATCH) {                                   // the rest into L2 while the history is looked at: a line a thread
+        const int v = v0 + tid * (kSlice / kLogitsThreads);
+        if (v >= 0 && v < a.V) asm volatile("prefetch.global.L2 [%0];" ::"l"(r.x + v));
+    }
     const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
     const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;

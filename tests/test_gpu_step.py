@@ -582,3 +582,34 @@ def test_attention_status(bi):
     ws.view(torch.int32)[0] = 1
     assert bi.bi_workspace_status(ws) == bi.BI_ERR_TIMEOUT
     assert bi.bi_workspace_status(ws) == bi.BI_OK
+
+
+@pytest.mark.parametrize("M,V,most", [(160, 70000, 3000), (70, 150001, 9000), (620, 9001, 5000), (330, 20000, 2500)])
+def test_logits_long_slices(bi, M, V, most):
+    """Enough rows for long slices, one to ten a row: histories of no token, of ids that are none, of more in a slice than
+    is kept between the passes; against the reference, and against the same rows a few at a time."""
+    rng = np.random.default_rng(M)
+    x = bits(rng, (M, V), 3.0)
+    n = rng.integers(0, most, M)
+    n[:4] = 0, 1, most, min(2 * most, 5000)
+    begin = np.concatenate([[0], np.cumsum(n)])[:-1].astype(np.int32) + 1
+    ids = rng.integers(-5, V + 5, int(n.sum()) + 2).astype(np.int32)
+    ids[begin[2]:begin[2] + most // 2] = V - 1                  # one slice has most of them
+    r = dict(ids=ids, begin=begin, mid=(begin + n // 3).astype(np.int32), end=(begin + n).astype(np.int32),
+             repetition=np.full(M, 1.25, np.float32), presence=rng.normal(size=M).astype(np.float32),
+             frequency=rng.normal(size=M).astype(np.float32), bias_ids=rng.integers(0, V, (M, 20)).astype(np.int32),
+             bias=rng.normal(size=(M, 20)).astype(np.float32))
+    d, dx = {k: dev(v) for k, v in r.items()}, dev(x)
+    ws = bi.new_logits_workspace(M)
+    out, am = torch.empty((M, V), device=DEV), torch.empty(M, dtype=torch.int32, device=DEV)
+    bi.bi_logits_process(dx, bi.logits_rules(**d), out, am, ws)
+    want, best = ref.logits_process(x[:5], V, **{k: v if k == "ids" else v[:5] for k, v in r.items()})
+    same(host(out)[:5], want, "logits")
+    same(host(am)[:5], best, "argmax")
+    for a in range(0, M, 10):
+        part = {k: v if k == "ids" else v[a:a + 10].contiguous() for k, v in d.items()}
+        m = part["begin"].shape[0]
+        o2, a2 = torch.empty((m, V), device=DEV), torch.empty(m, dtype=torch.int32, device=DEV)
+        bi.bi_logits_process(dx[a:a + 10], bi.logits_rules(**part), o2, a2, ws)
+        assert torch.equal(o2, out[a:a + 10]) and torch.equal(a2, am[a:a + 10])
+    assert not ws.any()
