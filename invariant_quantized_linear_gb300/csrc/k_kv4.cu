@@ -229,6 +229,86 @@ struct Rotation {
     }
 };
 
+// q heads that are rotated whole in the half layout: a lane has 4 elements of
+// each half, which are one another's partners.  Elements go two at a time.
+template <int D>
+__device__ __forceinline__ void append_q_whole(const uint16_t *src, uint16_t *dst, const float2 *cs, const uint16_t *norm,
+                                               float eps, int heads, int s0, int s1, int hl, int l)
+{
+    constexpr int L = D / 8, HEADS = 32 / L;
+    src += hl * D + 4 * l;
+    dst += hl * D + 4 * l;
+    auto load = [&](int s, uint2 (&w)[2]) {
+        w[0] = w[1] = make_uint2(0u, 0u);
+        if (s < s1 && s * HEADS + hl < heads) {
+            w[0] = __ldcs(reinterpret_cast<const uint2 *>(src + s * (HEADS * D)));
+            w[1] = __ldcs(reinterpret_cast<const uint2 *>(src + s * (HEADS * D) + D / 2));
+        }
+    };
+    uint2 ahead[kBatch][2];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) load(s0 + i, ahead[i]);
+    f2 co[2], si[2], minus[2], wn[2][2];                   // pairs of elements; norm weights of both halves
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(cs + 4 * l) + i);
+        co[i] = pk(f.x, f.z);
+        si[i] = pk(f.y, f.w);
+        minus[i] = pk(-f.y, -f.w);
+    }
+    if (norm) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(norm + 4 * l + h * (D / 2)));
+            wn[h][0] = pk(bf16_lo(v.x), bf16_hi(v.x));
+            wn[h][1] = pk(bf16_lo(v.y), bf16_hi(v.y));
+        }
+    }
+    const bool up = l & (L / 2);
+#pragma unroll 1
+    for (int begin = s0; begin < s1; begin += kBatch)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int s = begin + i;
+            if (s >= s1) break;
+            f2 x[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                x[h][0] = pk(bf16_lo(ahead[i][h].x), bf16_hi(ahead[i][h].x));
+                x[h][1] = pk(bf16_lo(ahead[i][h].y), bf16_hi(ahead[i][h].y));
+            }
+            load(s + kBatch, ahead[i]);
+            if (norm) {
+                // the order of square_sum: halves, neighbours, then halves again; a lane has two neighbours' sums
+                const float2 p = upk(fma2(x[1][0], x[1][0], mul2(x[0][0], x[0][0]))),
+                             q = upk(fma2(x[1][1], x[1][1], mul2(x[0][1], x[0][1])));
+                const float a = __fadd_rn(p.x, p.y), b = __fadd_rn(q.x, q.y);
+                float v = __fadd_rn(up ? b : a, __shfl_xor_sync(0xffffffffu, up ? a : b, L / 2));
+#pragma unroll
+                for (int o = L / 4; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+                v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, L / 2));
+                const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(v / D, eps)));
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[h][j] = mul2(mul2(x[h][j], pk(r, r)), wn[h][j]);
+            }
+            if (s * HEADS + hl < heads) {
+                uint32_t w[2][2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 lo = upk(add2(mul2(x[0][j], co[j]), mul2(x[1][j], minus[j]))),
+                                 hi = upk(add2(mul2(x[1][j], co[j]), mul2(x[0][j], si[j])));
+                    w[0][j] = to_bf16x2(lo.x, lo.y);
+                    w[1][j] = to_bf16x2(hi.x, hi.y);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<uint2 *>(dst + s * (HEADS * D) + h * (D / 2)) = make_uint2(w[h][0], w[h][1]);
+            }
+        }
+}
+
 // `parts` warps a token, a run of steps each; a step is HEADS heads of one
 // kind: first the steps of the q heads, then of k, then of v.
 template <int D, bool INTERLEAVED>
@@ -254,7 +334,15 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_ke
             if (step * HEADS + hl < a.Hq) *reinterpret_cast<uint4 *>(qo + step * (HEADS * D)) = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    const Rotation<D, INTERLEAVED> turn(a.rope + static_cast<int64_t>(tok.pos) * (a.rot / 2), a.rot, lane);
+    const float2 *const cs = a.rope + static_cast<int64_t>(tok.pos) * (a.rot / 2);
+    const bool q_whole = !INTERLEAVED && a.rot == D;
+    if (q_whole) {
+        if (first < q_steps)
+            append_q_whole<D>(a.q + t * a.ldq, a.q_out + static_cast<int64_t>(t) * a.Hq * D, cs, a.q_norm, a.eps, a.Hq, first,
+                              min(last, q_steps), hl, lane % L);
+        if (last <= q_steps) return;
+    }
+    const Rotation<D, INTERLEAVED> turn(cs, a.rot, lane);
     // The steps of one kind that are this warp's, kBatch loads ahead: body(step of the kind, whether the lane has a head,
     // the lane's words).
     auto each = [&](const uint16_t *base, int64_t ld, int heads, int begin, int n, auto body) {
@@ -286,7 +374,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_ke
         turn.partner(wn, pn, wp);
     };
     uint32_t wn[4], wp[4];
-    if (first < q_steps) {
+    if (!q_whole && first < q_steps) {
         weights(a.q_norm, wn, wp);
         each(a.q, a.ldq, a.Hq, 0, q_steps, [&](int s, bool there, uint32_t (&w)[4]) {
             turn.apply(w, a.q_norm != nullptr, wn, wp, a.eps);
