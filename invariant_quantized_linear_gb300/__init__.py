@@ -294,9 +294,9 @@ def bi_rmsnorm_quantize(h: torch.Tensor, y: torch.Tensor | None, w: torch.Tensor
     """h, y: bf16 [M, >= K] (row strides h.stride(0), y.stride(0)); w: bf16 [K]; h_out: bf16 [M, >= K], given with y
     (it may be h); q: int8 [M, K]; s_a: fp32 [M]."""
     M, K = q.shape
-    _check(lib.bi_rmsnorm_quantize(h.data_ptr(), h.stride(0), _ptr(y), 0 if y is None else y.stride(0), w.data_ptr(), eps,
-                                   M, K, _ptr(h_out), 0 if h_out is None else h_out.stride(0), q.data_ptr(),
-                                   s_a.data_ptr(), flags, _stream(stream)), "bi_rmsnorm_quantize")
+    _check(lib.bi_rmsnorm_quantize(h.data_ptr(), _ld(h), _ptr(y), _ld(y), w.data_ptr(), eps, M, K, _ptr(h_out),
+                                   _ld(h_out), q.data_ptr(), s_a.data_ptr(), flags, _stream(stream)),
+           "bi_rmsnorm_quantize")
 
 
 def bi_kv4_block_bytes(page_size: int, D: int) -> int:
@@ -328,6 +328,11 @@ def kv4_batch(cu_q: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, T: 
     return bi_kv4_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, T, max_q, max_kv)
 
 
+def _ld(t: torch.Tensor | None) -> int:
+    """Row stride; of a single row, whose stride may be anything, its length."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.numel()
+
+
 def _is_heads(t: torch.Tensor, D: int) -> bool:
     """16-bit elements [T, H, D], the heads of a row side by side."""
     return (t.element_size() == 2 and t.dim() == 3 and t.shape[2] == D and t.stride(2) == 1 and
@@ -352,8 +357,8 @@ def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: 
     assert k.shape[1] == v.shape[1] == cache.Hkv
     assert _is_heads(q_out, D) and q_out.shape[1] == q.shape[1] and q_out.shape[0] >= T and q_out.is_contiguous()
     assert rope.dtype == torch.float32 and rope.is_contiguous()
-    _check(lib.bi_rope_append_kv4(q.data_ptr(), q.stride(0), q.shape[1], k.data_ptr(), k.stride(0), v.data_ptr(),
-                                  v.stride(0), _ptr(q_norm), _ptr(k_norm), eps, rope.data_ptr(), rope.shape[0], rot,
+    _check(lib.bi_rope_append_kv4(q.data_ptr(), _ld(q), q.shape[1], k.data_ptr(), _ld(k), v.data_ptr(),
+                                  _ld(v), _ptr(q_norm), _ptr(k_norm), eps, rope.data_ptr(), rope.shape[0], rot,
                                   layout, q_out.data_ptr(), cache, batch, flags, _stream(stream)), "bi_rope_append_kv4")
 
 
@@ -380,7 +385,7 @@ def bi_attention_kv4(q: torch.Tensor, cache: bi_kv4_cache, batch: bi_kv4_batch, 
     """q: bf16 [T, Hq, D] (row stride q.stride(0)); o: bf16 [T, Hq, D] out; ws: from new_attention_kv4_workspace."""
     assert _is_heads(q, cache.D) and _is_heads(o, cache.D) and o.shape == q.shape and q.shape[0] >= batch.T
     assert o.stride(0) == q.shape[1] * cache.D or q.shape[0] == 1
-    _check(lib.bi_attention_kv4(q.data_ptr(), q.stride(0), q.shape[1], cache, batch, scale, o.data_ptr(), ws.data_ptr(),
+    _check(lib.bi_attention_kv4(q.data_ptr(), _ld(q), q.shape[1], cache, batch, scale, o.data_ptr(), ws.data_ptr(),
                                 ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_attention_kv4")
 
 
@@ -417,10 +422,10 @@ def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.T
                       argmax: torch.Tensor | None, ws: torch.Tensor, flags: int = 0, stream=None) -> None:
     """logits: bf16 [M, V] (row stride logits.stride(0)); out: fp32 [M, V] or None; argmax: int32 [M] or None."""
     M, V = logits.shape
-    assert logits.element_size() == 2 and logits.stride(1) == 1
-    assert out is None or (out.dtype == torch.float32 and out.stride(1) == 1)
-    _check(lib.bi_logits_process(logits.data_ptr(), logits.stride(0), M, V, rules, _ptr(out),
-                                 0 if out is None else out.stride(0), _ptr(argmax), ws.data_ptr(),
+    assert logits.element_size() == 2 and (logits.stride(1) == 1 or V == 1)
+    assert out is None or (out.dtype == torch.float32 and (out.stride(1) == 1 or V == 1))
+    _check(lib.bi_logits_process(logits.data_ptr(), _ld(logits), M, V, rules, _ptr(out),
+                                 _ld(out), _ptr(argmax), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_logits_process")
 
 

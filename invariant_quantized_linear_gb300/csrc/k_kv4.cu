@@ -20,6 +20,7 @@ namespace {
 constexpr int kAppendWarps = 4;                      // warps of a CTA
 constexpr int kAppendCtas = 5;                       // CTAs a SM that the registers are to allow
 constexpr int kBatch = 3;                            // heads (of a lane) in flight
+constexpr int kWholeBatch = 4;                       // the same for heads that are rotated whole; a power of two
 constexpr int kTargetWarps = 16;                     // warps a SM that a call is cut into, if it has the heads
 
 __global__ void __launch_bounds__(256) rope_table_kernel(const double *inv_freq, int n_freq, float amp, int n_pos,
@@ -71,10 +72,40 @@ __device__ __forceinline__ float square_sum(const uint32_t (&w)[4], const uint32
     return __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, L / 8));
 }
 
+// The parameter word of a group with elements lo .. hi.
+__device__ __forceinline__ uint32_t group_param(float lo, float hi)
+{
+    return bf16_rne_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)) | (__float_as_uint(lo) & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ bool quick_scale(float s) { return s >= kQuotientMinScale && s <= 0x1p64f; }
+
+// What codes_of needs to divide by a group's scale.
+__device__ __forceinline__ float group_inverse(uint32_t param)
+{
+    const float s = bf16_lo(param);
+    return quick_scale(s) ? __fdiv_rn(1.0f, s) : 0.0f;
+}
+
+// Codes of N elements x (bf16 values) of a group, r its group_inverse.  (x - z) / s by quotient_rn: r = RN(1 / s), and s has
+// 8 bits, so that no quotient lies close enough to the middle of two fp32 numbers to be rounded another way.
+template <int N>
+__device__ __forceinline__ void codes_of(const float (&x)[N], uint32_t param, float r, uint32_t (&c)[N])
+{
+    const float s = bf16_lo(param), z = bf16_hi(param);
+    if (quick_scale(s)) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)                        // rne, as in code_byte; (max - z) / s < 15.5: s is off by 2^-9 at most
+            c[e] = __float_as_uint(__fadd_rn(quotient_rn(__fsub_rn(x[e], z), s, r), 12582912.0f)) & 15u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            c[e] = s > 0.0f ? static_cast<uint32_t>(max(0, min(15, __float2int_rn(__fdiv_rn(__fsub_rn(x[e], z), s))))) : 0u;
+    }
+}
+
 // Codes of the lane's 8 elements x (bf16 values), one nibble each in element
-// order, and the parameters of their group of 64 (8 lanes).  (x - z) / s by
-// quotient_rn: r = RN(1 / s), and s has 8 bits, so that no quotient lies close
-// enough to the middle of two fp32 numbers to be rounded another way.
+// order, and the parameters of their group of 64 (8 lanes).
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t &param)
 {
     float lo = x[0], hi = x[0];
@@ -88,22 +119,11 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t &par
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    const uint32_t sb = bf16_rne_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-    const float s = __uint_as_float(sb << 16);
-    param = sb | (__float_as_uint(lo) & 0xFFFF0000u);
-    uint32_t codes = 0;
-    if (s >= kQuotientMinScale && s <= 0x1p64f) {
-        const float r = __fdiv_rn(1.0f, s);
+    param = group_param(lo, hi);
+    uint32_t c[8], codes = 0;
+    codes_of(x, param, group_inverse(param), c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float u = __fadd_rn(quotient_rn(__fsub_rn(x[e], lo), s, r), 12582912.0f);   // rne, as in code_byte
-            codes |= (__float_as_uint(u) & 15u) << (4 * e);    // (max - z) / s < 15.5: s is off by 2^-9 at most
-        }
-    } else if (s > 0.0f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            codes |= static_cast<uint32_t>(max(0, min(15, __float2int_rn(__fdiv_rn(__fsub_rn(x[e], lo), s))))) << (4 * e);
-    }
+    for (int e = 0; e < 8; ++e) codes |= c[e] << (4 * e);
     return codes;
 }
 
@@ -166,8 +186,7 @@ struct Rotation {
                 si[e] = second ? f.y : -f.y;
             }
         }
-        // partner words of the half layout: word j's comes from word j ^ swap of lane from[j]; a whole head's are the
-        // words D / 2 further (or back)
+        // partner words of the half layout: word j's comes from word j ^ swap of lane from[j]
         swap = half / 2 % 4;                               // 0 or 2: half is a multiple of 4
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -176,15 +195,11 @@ struct Rotation {
         }
     }
 
-    // pn: the words D / 2 further
-    __device__ __forceinline__ void partner(const uint32_t (&w)[4], const uint32_t (&pn)[4], uint32_t (&p)[4]) const
+    __device__ __forceinline__ void partner(const uint32_t (&w)[4], uint32_t (&p)[4]) const
     {
         if constexpr (INTERLEAVED) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) p[j] = (w[j] >> 16) | (w[j] << 16);
-        } else if (full) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = pn[j];
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) p[j] = __shfl_sync(0xffffffffu, swap ? w[j ^ 2] : w[j], from[j]);
@@ -195,12 +210,8 @@ struct Rotation {
     __device__ __forceinline__ void apply(uint32_t (&w)[4], bool norm, const uint32_t (&wn)[4], const uint32_t (&wp)[4],
                                           float eps) const
     {
-        uint32_t p[4], pn[4];
-        if (norm || (!INTERLEAVED && full)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) pn[j] = __shfl_xor_sync(0xffffffffu, w[j], L / 2);
-        }
-        partner(w, pn, p);
+        uint32_t p[4];
+        partner(w, p);
         float x[8], y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -208,6 +219,9 @@ struct Rotation {
             y[e] = elem(p, e);
         }
         if (norm) {
+            uint32_t pn[4];                                // the words D / 2 further
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pn[j] = __shfl_xor_sync(0xffffffffu, w[j], L / 2);
             const float sum = square_sum<D>(w, pn);
             const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(sum / D, eps)));
 #pragma unroll
@@ -229,15 +243,16 @@ struct Rotation {
     }
 };
 
-// q heads that are rotated whole in the half layout: a lane has 4 elements of
-// each half, which are one another's partners.  Elements go two at a time.
-template <int D>
-__device__ __forceinline__ void append_q_whole(const uint16_t *src, uint16_t *dst, const float2 *cs, const uint16_t *norm,
-                                               float eps, int heads, int s0, int s1, int hl, int l)
+// Heads that are rotated whole in the half layout, normed and rotated: a lane
+// has 4 elements of each half, which are one another's partners, and elements go
+// two at a time.  out(step, whether the lane has a head, bf16 pairs of both halves).
+template <int D, class Out>
+__device__ __forceinline__ void turn_whole(const uint16_t *src, const float2 *cs, const uint16_t *norm, float eps, int heads,
+                                           int s0, int s1, Out out)
 {
     constexpr int L = D / 8, HEADS = 32 / L;
+    const int lane = threadIdx.x & 31, l = lane % L, hl = lane / L;
     src += hl * D + 4 * l;
-    dst += hl * D + 4 * l;
     auto load = [&](int s, uint2 (&w)[2]) {
         w[0] = w[1] = make_uint2(0u, 0u);
         if (s < s1 && s * HEADS + hl < heads) {
@@ -245,16 +260,15 @@ __device__ __forceinline__ void append_q_whole(const uint16_t *src, uint16_t *ds
             w[1] = __ldcs(reinterpret_cast<const uint2 *>(src + s * (HEADS * D) + D / 2));
         }
     };
-    uint2 ahead[kBatch][2];
+    uint2 ahead[kWholeBatch][2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) load(s0 + i, ahead[i]);
-    f2 co[2], si[2], minus[2], wn[2][2];                   // pairs of elements; norm weights of both halves
+    for (int i = 0; i < kWholeBatch; ++i) load(s0 + i, ahead[i]);
+    f2 co[2], si[2], wn[2][2];                             // pairs of elements; norm weights of both halves
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float4 f = __ldg(reinterpret_cast<const float4 *>(cs + 4 * l) + i);
         co[i] = pk(f.x, f.z);
         si[i] = pk(f.y, f.w);
-        minus[i] = pk(-f.y, -f.w);
     }
     if (norm) {
 #pragma unroll
@@ -265,21 +279,28 @@ __device__ __forceinline__ void append_q_whole(const uint16_t *src, uint16_t *ds
         }
     }
     const bool up = l & (L / 2);
+    auto pairs = [](const uint2 &w, f2 (&x)[2]) {
+        x[0] = pk(bf16_lo(w.x), bf16_hi(w.x));
+        x[1] = pk(bf16_lo(w.y), bf16_hi(w.y));
+    };
 #pragma unroll 1
-    for (int begin = s0; begin < s1; begin += kBatch)
+    for (int begin = s0; begin < s1; begin += kWholeBatch) {
+        uint2 now[kWholeBatch][2];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int s = begin + i;
-            if (s >= s1) break;
-            f2 x[2][2];
+        for (int i = 0; i < kWholeBatch; ++i) {
+            now[i][0] = ahead[i][0];
+            now[i][1] = ahead[i][1];
+            load(begin + kWholeBatch + i, ahead[i]);
+        }
+        // 1 / sqrt of the batch's heads: lane i of each four computes the i-th, so that one root and one division serve all
+        float r = 0.0f;
+        if (norm) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                x[h][0] = pk(bf16_lo(ahead[i][h].x), bf16_hi(ahead[i][h].x));
-                x[h][1] = pk(bf16_lo(ahead[i][h].y), bf16_hi(ahead[i][h].y));
-            }
-            load(s + kBatch, ahead[i]);
-            if (norm) {
+            for (int i = 0; i < kWholeBatch; ++i) {
                 // the order of square_sum: halves, neighbours, then halves again; a lane has two neighbours' sums
+                f2 x[2][2];
+                pairs(now[i][0], x[0]);
+                pairs(now[i][1], x[1]);
                 const float2 p = upk(fma2(x[1][0], x[1][0], mul2(x[0][0], x[0][0]))),
                              q = upk(fma2(x[1][1], x[1][1], mul2(x[0][1], x[0][1])));
                 const float a = __fadd_rn(p.x, p.y), b = __fadd_rn(q.x, q.y);
@@ -287,31 +308,95 @@ __device__ __forceinline__ void append_q_whole(const uint16_t *src, uint16_t *ds
 #pragma unroll
                 for (int o = L / 4; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
                 v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, L / 2));
-                const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(v / D, eps)));
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) x[h][j] = mul2(mul2(x[h][j], pk(r, r)), wn[h][j]);
+                if (lane % kWholeBatch == i) r = v;
             }
-            if (s * HEADS + hl < heads) {
-                uint32_t w[2][2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 lo = upk(add2(mul2(x[0][j], co[j]), mul2(x[1][j], minus[j]))),
-                                 hi = upk(add2(mul2(x[1][j], co[j]), mul2(x[0][j], si[j])));
-                    w[0][j] = to_bf16x2(lo.x, lo.y);
-                    w[1][j] = to_bf16x2(hi.x, hi.y);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<uint2 *>(dst + s * (HEADS * D) + h * (D / 2)) = make_uint2(w[h][0], w[h][1]);
-            }
+            r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(r / D, eps)));
         }
+#pragma unroll
+        for (int i = 0; i < kWholeBatch; ++i) {
+            const int s = begin + i;
+            if (s >= s1) break;
+            f2 x[2][2];
+            pairs(now[i][0], x[0]);
+            pairs(now[i][1], x[1]);
+            if (norm) {
+                const float ri = __shfl_sync(0xffffffffu, r, (lane & ~(kWholeBatch - 1)) + i);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[h][j] = mul2(mul2(x[h][j], pk(ri, ri)), wn[h][j]);
+            }
+            uint32_t w[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // the sums one at a time: a packed sum of packed products is contracted to one rounding
+                const float2 ac = upk(mul2(x[0][j], co[j])), bs = upk(mul2(x[1][j], si[j])),
+                             bc = upk(mul2(x[1][j], co[j])), as = upk(mul2(x[0][j], si[j]));
+                w[0][j] = to_bf16x2(__fsub_rn(ac.x, bs.x), __fsub_rn(ac.y, bs.y));
+                w[1][j] = to_bf16x2(__fadd_rn(bc.x, as.x), __fadd_rn(bc.y, as.y));
+            }
+            out(s, s * HEADS + hl < heads, w);
+        }
+    }
+}
+
+// Codes and parameters of a key whose halves a lane holds 4 elements of, w as turn_whole gives them: the word of the
+// first half for the lane and its odd neighbour (of the second half, if the lane is the odd one), and the parameters of
+// the lane's group (of the group of the half that the lane's own half of the lanes stands for, if there are two).
+template <int D>
+__device__ __forceinline__ uint32_t quantise_whole(const uint32_t (&w)[2][2], uint32_t &param)
+{
+    constexpr int L = D / 8;
+    const int l = threadIdx.x % L;
+    float x[2][4], lo[2], hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            x[h][2 * j] = bf16_lo(w[h][j]);
+            x[h][2 * j + 1] = bf16_hi(w[h][j]);
+        }
+        lo[h] = fminf(fminf(x[h][0], x[h][1]), fminf(x[h][2], x[h][3]));
+        hi[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+    }
+    const bool up = l & (L / 2);
+    float a, b;                                            // the smallest and the largest of the lane's group
+    if (D == 2 * kKv4Group) {
+        a = fminf(up ? lo[1] : lo[0], __shfl_xor_sync(0xffffffffu, up ? lo[0] : lo[1], L / 2));
+        b = fmaxf(up ? hi[1] : hi[0], __shfl_xor_sync(0xffffffffu, up ? hi[0] : hi[1], L / 2));
+    } else {
+        a = fminf(lo[0], lo[1]);
+        b = fmaxf(hi[0], hi[1]);
+    }
+#pragma unroll
+    for (int o = kKv4Group / 16; o > 0; o >>= 1) {
+        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+    }
+    param = group_param(a, b);
+    const float r = group_inverse(param);
+    uint32_t other = param, half[2];
+    float r_other = r;
+    if (D == 2 * kKv4Group) {
+        other = __shfl_xor_sync(0xffffffffu, param, L / 2);
+        r_other = __shfl_xor_sync(0xffffffffu, r, L / 2);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool mine = up == (h == 1);
+        uint32_t c[4];
+        codes_of(x[h], mine ? param : other, mine ? r : r_other, c);
+        half[h] = c[0] | c[2] << 4 | c[1] << 16 | c[3] << 20;   // where elements 0-3 stand in a key word; 4-7 8 bits up
+    }
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, l & 1 ? half[0] : half[1], 1);
+    return l & 1 ? got | half[1] << 8 : half[0] | got << 8;
 }
 
 // `parts` warps a token, a run of steps each; a step is HEADS heads of one
 // kind: first the steps of the q heads, then of k, then of v.
-template <int D, bool INTERLEAVED>
+// LAYOUT: of the rotation's pairs; WHOLE: HALF with all of a head rotated.
+enum { WHOLE, HALF, INTERLEAVED };
+template <int D, int LAYOUT>
 __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_kernel(RopeAppendArgs a, int parts, int pdl)
 {
     constexpr int L = D / 8, HEADS = 32 / L, G = D / kKv4Group;
@@ -335,14 +420,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_ke
         return;
     }
     const float2 *const cs = a.rope + static_cast<int64_t>(tok.pos) * (a.rot / 2);
-    const bool q_whole = !INTERLEAVED && a.rot == D;
-    if (q_whole) {
-        if (first < q_steps)
-            append_q_whole<D>(a.q + t * a.ldq, a.q_out + static_cast<int64_t>(t) * a.Hq * D, cs, a.q_norm, a.eps, a.Hq, first,
-                              min(last, q_steps), hl, lane % L);
-        if (last <= q_steps) return;
-    }
-    const Rotation<D, INTERLEAVED> turn(cs, a.rot, lane);
     // The steps of one kind that are this warp's, kBatch loads ahead: body(step of the kind, whether the lane has a head,
     // the lane's words).
     auto each = [&](const uint16_t *base, int64_t ld, int heads, int begin, int n, auto body) {
@@ -365,23 +442,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_ke
             body(s, s * HEADS + hl < heads, w);
         }
     };
-    auto weights = [&](const uint16_t *norm, uint32_t (&wn)[4], uint32_t (&wp)[4]) {
-        uint32_t pn[4];
-        const uint4 v = norm ? __ldg(reinterpret_cast<const uint4 *>(norm + d)) : make_uint4(0u, 0u, 0u, 0u);
-        wn[0] = v.x, wn[1] = v.y, wn[2] = v.z, wn[3] = v.w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pn[j] = __shfl_xor_sync(0xffffffffu, wn[j], L / 2);
-        turn.partner(wn, pn, wp);
-    };
-    uint32_t wn[4], wp[4];
-    if (!q_whole && first < q_steps) {
-        weights(a.q_norm, wn, wp);
-        each(a.q, a.ldq, a.Hq, 0, q_steps, [&](int s, bool there, uint32_t (&w)[4]) {
-            turn.apply(w, a.q_norm != nullptr, wn, wp, a.eps);
-            if (there) *reinterpret_cast<uint4 *>(qo + s * (HEADS * D)) = make_uint4(w[0], w[1], w[2], w[3]);
-        });
-    }
-    if (last <= q_steps) return;
     const int P = 1 << a.c.page_shift;
     const Places<D> at(d, tok.pos & (P - 1), P);
     unsigned char *const block = kv4_block<D>(a.c, max(tok.page, 0), hl);
@@ -401,12 +461,52 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_ke
         }
         if (d % kKv4Group == 0) *reinterpret_cast<uint32_t *>(to + at.par + (key ? 0 : 4 * G)) = param;
     };
-    if (first < q_steps + kv_steps) {
-        weights(a.k_norm, wn, wp);
-        each(a.k, a.ldk, a.c.Hkv, q_steps, kv_steps, [&](int s, bool there, uint32_t (&w)[4]) {
-            turn.apply(w, a.k_norm != nullptr, wn, wp, a.eps);
-            quantise(s, there, w, true);
-        });
+    if constexpr (LAYOUT == WHOLE) {
+        const int l = lane % L;
+        uint16_t *const qw = a.q_out + (static_cast<int64_t>(t) * a.Hq + hl) * D + 4 * l;
+        if (first < q_steps)
+            turn_whole<D>(a.q + t * a.ldq, cs, a.q_norm, a.eps, a.Hq, first, min(last, q_steps),
+                          [&](int s, bool there, const uint32_t (&w)[2][2]) {
+                              if (!there) return;
+                              uint16_t *to = qw + s * (HEADS * D);
+                              *reinterpret_cast<uint2 *>(to) = make_uint2(w[0][0], w[0][1]);
+                              *reinterpret_cast<uint2 *>(to + D / 2) = make_uint2(w[1][0], w[1][1]);
+                          });
+        const int k0 = max(first - q_steps, 0), k1 = min(last - q_steps, kv_steps);
+        if (k0 < k1) {
+            const Places<D> word(4 * (l & ~1) + (l & 1) * (D / 2), tok.pos & (P - 1), P);
+            turn_whole<D>(a.k + t * a.ldk, cs, a.k_norm, a.eps, a.c.Hkv, k0, k1,
+                          [&](int s, bool there, const uint32_t (&w)[2][2]) {
+                              uint32_t param;
+                              const uint32_t codes = quantise_whole<D>(w, param);
+                              if (!there || tok.page < 0) return;
+                              unsigned char *to = block + s * (HEADS * Kv4Layout::block(P, D));
+                              *reinterpret_cast<uint32_t *>(to + word.key) = codes;
+                              if (l % 8 == 0) *reinterpret_cast<uint32_t *>(to + at.par) = param;
+                          });
+        }
+    } else {
+        const Rotation<D, LAYOUT == INTERLEAVED> turn(cs, a.rot, lane);
+        auto weights = [&](const uint16_t *norm, uint32_t (&wn)[4], uint32_t (&wp)[4]) {
+            const uint4 v = norm ? __ldg(reinterpret_cast<const uint4 *>(norm + d)) : make_uint4(0u, 0u, 0u, 0u);
+            wn[0] = v.x, wn[1] = v.y, wn[2] = v.z, wn[3] = v.w;
+            turn.partner(wn, wp);
+        };
+        uint32_t wn[4], wp[4];
+        if (first < q_steps) {
+            weights(a.q_norm, wn, wp);
+            each(a.q, a.ldq, a.Hq, 0, q_steps, [&](int s, bool there, uint32_t (&w)[4]) {
+                turn.apply(w, a.q_norm != nullptr, wn, wp, a.eps);
+                if (there) *reinterpret_cast<uint4 *>(qo + s * (HEADS * D)) = make_uint4(w[0], w[1], w[2], w[3]);
+            });
+        }
+        if (first < q_steps + kv_steps && last > q_steps) {
+            weights(a.k_norm, wn, wp);
+            each(a.k, a.ldk, a.c.Hkv, q_steps, kv_steps, [&](int s, bool there, uint32_t (&w)[4]) {
+                turn.apply(w, a.k_norm != nullptr, wn, wp, a.eps);
+                quantise(s, there, w, true);
+            });
+        }
     }
     each(a.v, a.ldv, a.c.Hkv, q_steps + kv_steps, kv_steps,
          [&](int s, bool there, uint32_t (&w)[4]) { quantise(s, there, w, false); });
@@ -468,7 +568,7 @@ int parts_of(int T, int steps, int sms)
     return (steps + per - 1) / per;
 }
 
-template <int D, bool INTERLEAVED>
+template <int D, int LAYOUT>
 cudaError_t launch_append(const RopeAppendArgs &a, int sms, bool pdl, cudaStream_t stream)
 {
     constexpr int HEADS = 32 / (D / 8);
@@ -483,7 +583,7 @@ cudaError_t launch_append(const RopeAppendArgs &a, int sms, bool pdl, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, INTERLEAVED>, a, parts, pdl ? 1 : 0);
+    return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, LAYOUT>, a, parts, pdl ? 1 : 0);
 }
 
 }  // namespace
@@ -501,9 +601,14 @@ cudaError_t launch_rope_table(const double *inv_freq, int n_freq, float amp, int
 cudaError_t launch_rope_append_kv4(const RopeAppendArgs &a, int D, bool interleaved, int sms, bool pdl,
                                    cudaStream_t stream)
 {
+    const int layout = interleaved ? INTERLEAVED : a.rot == D ? WHOLE : HALF;
     if (D == 64)
-        return interleaved ? launch_append<64, true>(a, sms, pdl, stream) : launch_append<64, false>(a, sms, pdl, stream);
-    return interleaved ? launch_append<128, true>(a, sms, pdl, stream) : launch_append<128, false>(a, sms, pdl, stream);
+        return layout == WHOLE  ? launch_append<64, WHOLE>(a, sms, pdl, stream)
+               : layout == HALF ? launch_append<64, HALF>(a, sms, pdl, stream)
+                                : launch_append<64, INTERLEAVED>(a, sms, pdl, stream);
+    return layout == WHOLE  ? launch_append<128, WHOLE>(a, sms, pdl, stream)
+           : layout == HALF ? launch_append<128, HALF>(a, sms, pdl, stream)
+                            : launch_append<128, INTERLEAVED>(a, sms, pdl, stream);
 }
 
 cudaError_t launch_kv4_gather(const Kv4View &c, int D, uint16_t *k_out, uint16_t *v_out, int sms, cudaStream_t stream)

@@ -613,3 +613,41 @@ def test_logits_long_slices(bi, M, V, most):
         bi.bi_logits_process(dx[a:a + 10], bi.logits_rules(**part), o2, a2, ws)
         assert torch.equal(o2, out[a:a + 10]) and torch.equal(a2, am[a:a + 10])
     assert not ws.any()
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,P,norm", [
+    ([(300, 300), (220, 500)], 64, 8, 128, 16, True),          # several batches of q heads a warp, the last one short
+    ([(1300, 1300)], 13, 3, 64, 32, True),
+    ([(2500, 2500)], 7, 1, 64, 64, True),                       # a warp a token
+    ([(130, 130)], 9, 9, 128, 128, False),
+    ([(1, 77), (2, 5)], 1, 1, 128, 16, True)])
+def test_append_whole_heads(bi, seqs, Hq, Hkv, D, P, norm):
+    """All of a head rotated in the half layout: heads of many and of few tokens, odd counts, one kv head."""
+    test_append_and_gather(bi, seqs, Hq, Hkv, D, P, D, False, norm)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rot", [16, "D"])
+def test_append_scales(bi, D, rot):
+    """Groups of every kind at position 0, where a rotation changes nothing but a zero's sign: zeros of both signs,
+    constants, scales that are subnormal, tiny and huge, one element apart from the rest."""
+    rng = np.random.default_rng(D)
+    Hkv, P = 24, 16
+    x = rng.normal(size=(2, Hkv, D)).astype(np.float32) * 2.0 ** np.linspace(-126, 100, Hkv)[:, None].astype(np.float32)
+    x[:, 0], x[:, 1], x[:, 2] = 0.0, -0.0, -3.5
+    x[:, 3], x[:, 3, D // 2 + 1] = 1.0, 1.0078125
+    x[:, 4, ::2], x[:, 4, 1::2] = 0.0, 1e-40
+    x[:, 5, 1:], x[:, 5, 0] = 2.0 ** -9, 300.0
+    x[:, 6, :D // 2], x[:, 6, D // 2:] = 2.0 ** -120, 2.0 ** 90
+    rot = D if rot == "D" else rot
+    b = Batch(bi, [(1, 1)], Hkv, D, P)
+    k, v = ref.bf16_bits(x)
+    want = b.pool.copy()
+    rope = np.stack((np.ones((1, rot // 2)), np.zeros((1, rot // 2))), -1).astype(np.float32)
+    k_ref = ref.bf16_round(ref.rotate(ref.f32(k)[None], rope, rot, False))[0]
+    for h in range(Hkv):
+        ref.write_position(want[b.pages[0, 0], 0, h], P, D, 0, k_ref[h], ref.f32(v[h]))
+    b.to_device()
+    q_out = torch.empty((1, 1, D), dtype=torch.int16, device=DEV)
+    bi.bi_rope_append_kv4(dev(k[None, :1]), dev(k[None]), dev(v[None]), dev(rope), rot, bi.BI_ROPE_HALF, q_out, b.cache, b.batch)
+    same(host(b.d_pool), want, "cache bytes")
