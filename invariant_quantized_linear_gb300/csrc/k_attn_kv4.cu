@@ -15,8 +15,13 @@
 // (16 of an mma.m16n8k16) and head elements fill the rows, and the few query
 // rows the columns, 8 at a time: a decode step of a group of 4 heads wastes
 // half a tile instead of three quarters.  The cache's layout puts what a lane
-// needs of a 16-position tile into 16 bytes of its own, so a warp copies its
-// codes to shared memory (cp.async) and reads them back with no exchange.
+// needs of a tile's 8 positions into D / 8 bytes of its own.  A warp has its
+// blocks copied to shared memory as they lie (bulk copies on two barriers: keys
+// with parameters, values; the next block's follow as soon as this one's are
+// read) and each lane loads its own words, with no exchange.  Values' words of
+// four lanes share banks (head size 128); copies that would spread them, a
+// quarter of a block each, cost what they save (126.7 for 127.3 us, b 96, 8191
+// positions; head size 64, b 6, 40000: 50.8 for 49.0 us).
 //
 // q is scaled by a power of two a row so that its largest element is just
 // below 2^15: in f16 it is exact down to 2^-24 of that.  The weights p s go
@@ -40,13 +45,21 @@
 // the row does not see; which warp computes what may therefore go by the size
 // of the call:
 //   a span a CTA, a chunk a warp, the fold in registers: least work a position,
-//     four CTAs a SM overlap one another's latencies;
+//     2 to 5 CTAs a SM overlap one another's latencies;
 //   a span a cluster of 8 CTAs, a block a warp, the fold over the cluster's
 //     shared memory: for calls that leave SMs idle, where a chunk's eight
 //     blocks one after the other would be most of the time.
 // The CTA that finishes a row block's last span joins the spans (a counter in
 // the workspace); a second launch does where a row has many spans or the
 // counters do not suffice.
+//
+// Bound: HBM by its bytes (0.5625 B an element) up to 16 query rows a kv head;
+// what it reaches is set by instructions and by the latency of a block's chain
+// (copies, products, maxima, exponentials, products) with the 8 to 20 warps a SM
+// that registers allow.  Measured (32 q and 8 kv heads of 128, caches out of L2):
+// b 96, up to 8191 positions 126 us, 4.56 TB/s of codes and parameters; b 1,
+// 131072: 43 us, 3.5 TB/s; b 64, 8 tokens, 4096: 140 us; b 1, 517: 6.4 us; 28 and
+// 4 heads of 64, b 6, 5 tokens, up to 40000: 49 us.
 #include "ptx.cuh"
 #include "row_ops.cuh"
 #include "step.cuh"
@@ -1065,7 +1078,8 @@ cudaError_t launch_attention_kv4(const AttnKv4Args &a, int D, bool pdl, cudaStre
     p.magic = (1ull << 32) / GH + 1;
     p.spans = spans_of(a.c.max_kv);
     p.pdl = pdl ? 1 : 0;
-    // 16 rows a CTA where there are as many; a span a cluster while the spans alone leave SMs idle
+    // 16 rows a CTA where there are as many.  A span a cluster while the spans alone leave SMs idle: it takes 5.5 us and
+    // 0.13 us more for each span of 8 rows (152 SMs), a span a CTA 18.8 us up to a span a SM; they meet at 105 spans.
     const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv;
     const bool two = rows > 8;
     p.row_blocks = two ? (rows + 15) / 16 : (rows + 7) / 8;

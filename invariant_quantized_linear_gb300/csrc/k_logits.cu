@@ -432,9 +432,14 @@ size_t logits_workspace(int M) { return sizeof(RowKey) * static_cast<size_t>(M);
 
 cudaError_t launch_logits_process(const LogitsArgs &a, int sms, bool pdl, cudaStream_t stream)
 {
-    // short slices while the long ones would leave SMs idle: each slice reads the row's history again
-    const int64_t slices = static_cast<int64_t>(a.M) * ((a.V + 16383) / 16384);
-    return slices < 4 * sms ? launch<2, 2>(a, pdl, stream) : launch<16, 4>(a, pdl, stream);
+    // The shortest slices of which the SMs hold all at once: each slice reads the row's history again.  (Histories of
+    // 1000: 5 x 151936 6.7, 7.6, 8.2 and 9.6 us with slices of 2048, 4096, 8192 and 16384; 12 x 128259 10.7, 8.4, 9.0 and
+    // 10.2; 24 x 128259 16.0, 12.6, 10.9 and 12.0; 150 x 32003 23.6, 16.4, 13.3 and 12.7.)
+    auto fits = [&](int slice) { return static_cast<int64_t>(a.M) * ((a.V + slice - 1) / slice) <= kLogitsCtas * sms; };
+    return fits(2048)   ? launch<2, 2>(a, pdl, stream)
+           : fits(4096) ? launch<4, 4>(a, pdl, stream)
+           : fits(8192) ? launch<8, 4>(a, pdl, stream)
+                        : launch<16, 4>(a, pdl, stream);
 }
 
 }  // namespace bi
