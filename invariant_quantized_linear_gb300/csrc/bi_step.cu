@@ -113,7 +113,8 @@ bi_status bi_rmsnorm_quantize(const uint16_t *h, int64_t ldh, const uint16_t *y,
             overlaps(q, qb, y, yb) || overlaps(s_a, sb, y, yb) || overlaps(q, qb, h_out, ob) || overlaps(s_a, sb, h_out, ob))
             return BI_ERR_INVALID_ARG;
     }
-    st = device_info(nullptr);
+    int sms = 0;
+    st = device_info(&sms);
     if (st != BI_OK) return st;
     bi::NormArgs a;
     a.h = h;
@@ -128,7 +129,7 @@ bi_status bi_rmsnorm_quantize(const uint16_t *h, int64_t ldh, const uint16_t *y,
     a.K = K;
     a.q = q;
     a.s_a = s_a;
-    return from_cuda(bi::launch_rmsnorm_quantize(a, (flags & BI_FLAG_PDL) != 0, stream));
+    return from_cuda(bi::launch_rmsnorm_quantize(a, sms, (flags & BI_FLAG_PDL) != 0, stream));
 }
 
 size_t bi_kv4_block_bytes(int page_size, int D)

@@ -6,7 +6,9 @@
 // rounding of r, and r enters the scale alone, s_a = st r.
 //
 // Bound: HBM; 7 bytes an element (h, y read; h', q written).  One CTA a row,
-// the row held in registers between the two reductions and the codes.
+// the row held in registers between the two reductions and the codes (8192 rows
+// of 4096: 42 us, 5.6 TB/s, where the codes' instructions show beside the copies;
+// one row 2.7 us, a launch's latency, two passes over a barrier and the memory's).
 #include "ptx.cuh"
 #include "row_ops.cuh"
 #include "step.cuh"
@@ -15,8 +17,9 @@ namespace bi {
 
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kFold = 256;              // the squares of chunks of 8 are added for every kFold-th chunk, then over kFold threads
 
+template <int THREADS>
 __device__ __forceinline__ float2 block_sum_max(float s, float m, float2 *red)
 {
 #pragma unroll
@@ -30,7 +33,7 @@ __device__ __forceinline__ float2 block_sum_max(float s, float m, float2 *red)
     s = 0.0f;
     m = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kNormThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         s = __fadd_rn(s, red[w].x);
         m = fmaxf(m, red[w].y);
     }
@@ -99,10 +102,14 @@ __device__ __forceinline__ uint2 codes8(const float (&t)[8], float st, float r)
 __device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
 // C chunks of 8 elements a thread in registers; C = 0: any K, the row read twice.
-template <int C>
-__global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(NormArgs a, int pdl)
+// The sum of a row does not depend on THREADS: chunk j goes to sum j % kFold, in order; then the kFold sums, in the order
+// of warps of 32.  With fewer threads than kFold the others' sums are zeros, with more they are handed over.
+template <int C, int THREADS>
+__global__ void __launch_bounds__(THREADS) rmsnorm_quant_kernel(NormArgs a, int pdl)
 {
-    __shared__ float2 red[kNormThreads / 32];
+    static_assert(THREADS == kFold || C == 1 || THREADS > kFold, "a thread has every chunk of its sums");
+    __shared__ float2 red[THREADS / 32];
+    __shared__ float handed[THREADS > kFold ? C * THREADS : 1];
     if (pdl) {
         pdl_launch_dependents();
         pdl_wait();
@@ -120,17 +127,30 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(NormArgs a,
     if constexpr (C > 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = (c * kNormThreads + threadIdx.x) * 8;
+            const int k = (c * THREADS + threadIdx.x) * 8;
+            float sum = 0.0f;
             if (k < K) {
                 const uint4 h = load(k);
                 if (yr) *reinterpret_cast<uint4 *>(a.h_out + row * a.ldo + k) = h;
-                norm8(h, ldg16(a.w + k), t[c], s, m);
+                norm8(h, ldg16(a.w + k), t[c], sum, m);
             }
+            if constexpr (THREADS > kFold) handed[c * THREADS + threadIdx.x] = sum;
+            else s = __fadd_rn(s, sum);
+        }
+        if constexpr (THREADS > kFold) {
+            __syncthreads();
+            if (threadIdx.x < kFold)
+#pragma unroll
+                for (int j = 0; j < C * THREADS / kFold; ++j) s = __fadd_rn(s, handed[j * kFold + threadIdx.x]);
         }
     } else {
-        for (int k = threadIdx.x * 8; k < K; k += kNormThreads * 8) norm8(load(k), ldg16(a.w + k), t[0], s, m);
+        for (int k = threadIdx.x * 8; k < K; k += THREADS * 8) {
+            float sum = 0.0f;
+            norm8(load(k), ldg16(a.w + k), t[0], sum, m);
+            s = __fadd_rn(s, sum);
+        }
     }
-    const float2 r = block_sum_max(s, m, red);
+    const float2 r = block_sum_max<THREADS>(s, m, red);
     const float st = r.y == 0.0f ? 1.0f : __fdiv_rn(r.y, 127.0f);
     const bool plain = st >= kQuotientMinScale && st <= 0x1p64f;
     const float inv = __fdiv_rn(1.0f, st);
@@ -139,11 +159,11 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(NormArgs a,
     if constexpr (C > 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = (c * kNormThreads + threadIdx.x) * 8;
+            const int k = (c * THREADS + threadIdx.x) * 8;
             if (k < K) *reinterpret_cast<uint2 *>(qr + k) = codes(t[c]);
         }
     } else {
-        for (int k = threadIdx.x * 8; k < K; k += kNormThreads * 8) {
+        for (int k = threadIdx.x * 8; k < K; k += THREADS * 8) {
             const uint4 h = load(k);                  // h_out may be h: it is written after its last read
             if (yr) *reinterpret_cast<uint4 *>(a.h_out + row * a.ldo + k) = h;
             norm8(h, ldg16(a.w + k), t[0], s, m);
@@ -156,26 +176,43 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(NormArgs a,
     }
 }
 
-}  // namespace
-
-cudaError_t launch_rmsnorm_quantize(const NormArgs &a, bool pdl, cudaStream_t stream)
+template <int C, int THREADS>
+cudaError_t launch(const NormArgs &a, bool pdl, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.M));
-    cfg.blockDim = dim3(kNormThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    const int p = pdl ? 1 : 0;
-    switch ((a.K + kNormThreads * 8 - 1) / (kNormThreads * 8)) {
-    case 1: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<1>, a, p);
-    case 2: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<2>, a, p);
-    case 3: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<3>, a, p);
-    case 4: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<4>, a, p);
-    default: return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<0>, a, p);
+    return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<C, THREADS>, a, pdl ? 1 : 0);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_quantize(const NormArgs &a, int sms, bool pdl, cudaStream_t stream)
+{
+    // A chunk a thread while that fills warps (8192 rows of 1024: 10.2 us, 12.7 with 256 threads).  Rows that leave an SM at
+    // most two CTAs are bound by latency and take 512 threads, longer calls 256: 4 x 8192 3.7 us (256: 4.1), 150 x 4096 3.0
+    // (3.6), 300 x 5136 4.3 (4.3), 600 x 5136 6.6 (5.1), 2048 x 4096 11.8 (9.4).
+    if (a.K <= 1024) return launch<1, 128>(a, pdl, stream);
+    if (a.M <= 2 * sms && a.K > 2048 && a.K <= 16384)
+        switch ((a.K + 4095) / 4096) {
+        case 1: return launch<1, 512>(a, pdl, stream);
+        case 2: return launch<2, 512>(a, pdl, stream);
+        case 3: return launch<3, 512>(a, pdl, stream);
+        default: return launch<4, 512>(a, pdl, stream);
+        }
+    // Above 6144 the registers of a row in 256 threads cost more than a second reading from L2 (2048 x 8192: 25.0 us, held
+    // 26.8; 2048 x 16384: 50, held 67; 2048 x 5136: 14.3, held 11.6).
+    switch ((a.K + 2047) / 2048) {
+    case 1: return launch<1, 256>(a, pdl, stream);
+    case 2: return launch<2, 256>(a, pdl, stream);
+    case 3: return launch<3, 256>(a, pdl, stream);
+    default: return launch<0, 256>(a, pdl, stream);
     }
 }
 

@@ -20,7 +20,7 @@ struct NormArgs {
     float *s_a;
 };
 
-cudaError_t launch_rmsnorm_quantize(const NormArgs &a, bool pdl, cudaStream_t stream);
+cudaError_t launch_rmsnorm_quantize(const NormArgs &a, int sms, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------------------ 4-bit cache
 

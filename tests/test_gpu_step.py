@@ -651,3 +651,22 @@ def test_append_scales(bi, D, rot):
     q_out = torch.empty((1, 1, D), dtype=torch.int16, device=DEV)
     bi.bi_rope_append_kv4(dev(k[None, :1]), dev(k[None]), dev(v[None]), dev(rope), rot, bi.BI_ROPE_HALF, q_out, b.cache, b.batch)
     same(host(b.d_pool), want, "cache bytes")
+
+
+@pytest.mark.parametrize("K", [1024, 2064, 4096, 5136, 8192, 10256, 16384])
+def test_norm_forms_give_the_same_bits(bi, K):
+    """Rows of a call large enough for one form against the same rows alone, which take another."""
+    rng = np.random.default_rng(K)
+    M = 700
+    h, y, w = dev(bits(rng, (M, K), 2.0)), dev(bits(rng, (M, K))), dev(bits(rng, K))
+
+    def go(a, b):
+        n = b - a
+        o, q, s = torch.empty((n, K), dtype=torch.int16, device=DEV), torch.empty((n, K), dtype=torch.int8, device=DEV), \
+            torch.empty(n, device=DEV)
+        bi.bi_rmsnorm_quantize(h[a:b], y[a:b], w, 1e-5, o, q, s)
+        return o, q, s
+    whole = go(0, M)
+    for a, b in ((0, 1), (1, 300), (300, 500), (699, 700)):
+        for x, z in zip(go(a, b), whole):
+            assert torch.equal(x, z[a:b])
