@@ -294,9 +294,13 @@ def bi_rmsnorm_quantize(h: torch.Tensor, y: torch.Tensor | None, w: torch.Tensor
     """h, y: bf16 [M, >= K] (row strides h.stride(0), y.stride(0)); w: bf16 [K]; h_out: bf16 [M, >= K], given with y
     (it may be h); q: int8 [M, K]; s_a: fp32 [M]."""
     M, K = q.shape
-    _check(lib.bi_rmsnorm_quantize(h.data_ptr(), _ld(h), _ptr(y), _ld(y), w.data_ptr(), eps, M, K, _ptr(h_out),
-                                   _ld(h_out), q.data_ptr(), s_a.data_ptr(), flags, _stream(stream)),
-           "bi_rmsnorm_quantize")
+    ldh = ldy = ldo = K                                    # a single row's stride may be anything
+    if M > 1:
+        ldh = h.stride(0)
+        if y is not None:
+            ldy, ldo = y.stride(0), h_out.stride(0)
+    _check(lib.bi_rmsnorm_quantize(h.data_ptr(), ldh, _ptr(y), ldy, w.data_ptr(), eps, M, K, _ptr(h_out), ldo,
+                                   q.data_ptr(), s_a.data_ptr(), flags, _stream(stream)), "bi_rmsnorm_quantize")
 
 
 def bi_kv4_block_bytes(page_size: int, D: int) -> int:
@@ -328,15 +332,13 @@ def kv4_batch(cu_q: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, T: 
     return bi_kv4_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, T, max_q, max_kv)
 
 
-def _ld(t: torch.Tensor | None) -> int:
-    """Row stride; of a single row, whose stride may be anything, its length."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.numel()
-
-
-def _is_heads(t: torch.Tensor, D: int) -> bool:
-    """16-bit elements [T, H, D], the heads of a row side by side."""
-    return (t.element_size() == 2 and t.dim() == 3 and t.shape[2] == D and t.stride(2) == 1 and
-            (t.stride(1) == D or t.shape[1] == 1))
+def _heads(t: torch.Tensor, T: int, H: int, D: int) -> int:
+    """The row stride of 16-bit elements [>= T, H, D], the heads of a row side by side; of a single row, whose stride may
+    be anything, its length."""
+    n, h, d = t.shape
+    ld, sh, sd = t.stride()
+    assert n >= T and h == H and d == D and sd == 1 and (sh == D or h == 1) and t.element_size() == 2
+    return ld if n > 1 else H * D
 
 
 def bi_rope_table(inv_freq: torch.Tensor, rope: torch.Tensor, amp: float = 1.0, stream=None) -> None:
@@ -352,22 +354,19 @@ def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: 
                        k_norm: torch.Tensor | None = None, eps: float = 0.0, flags: int = 0, stream=None) -> None:
     """q: bf16 [T, Hq, D], k, v: bf16 [T, Hkv, D] (row strides stride(0); parts of one packed tensor will do);
     rope: fp32 [positions, rot / 2, 2]; q_norm, k_norm: bf16 [D] or None; q_out: bf16 [T, Hq, D]."""
-    T, D = batch.T, cache.D
-    assert _is_heads(q, D) and _is_heads(k, D) and _is_heads(v, D) and min(q.shape[0], k.shape[0], v.shape[0]) >= T
-    assert k.shape[1] == v.shape[1] == cache.Hkv
-    assert _is_heads(q_out, D) and q_out.shape[1] == q.shape[1] and q_out.shape[0] >= T and q_out.is_contiguous()
-    assert rope.dtype == torch.float32 and rope.is_contiguous()
-    _check(lib.bi_rope_append_kv4(q.data_ptr(), _ld(q), q.shape[1], k.data_ptr(), _ld(k), v.data_ptr(),
-                                  _ld(v), _ptr(q_norm), _ptr(k_norm), eps, rope.data_ptr(), rope.shape[0], rot,
-                                  layout, q_out.data_ptr(), cache, batch, flags, _stream(stream)), "bi_rope_append_kv4")
+    T, D, Hq, Hkv = batch.T, cache.D, q.shape[1], cache.Hkv
+    ldq, ldk, ldv = _heads(q, T, Hq, D), _heads(k, T, Hkv, D), _heads(v, T, Hkv, D)
+    assert _heads(q_out, T, Hq, D) == Hq * D and rope.is_contiguous()
+    _check(lib.bi_rope_append_kv4(q.data_ptr(), ldq, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(q_norm),
+                                  _ptr(k_norm), eps, rope.data_ptr(), rope.shape[0], rot, layout, q_out.data_ptr(),
+                                  cache, batch, flags, _stream(stream)), "bi_rope_append_kv4")
 
 
 def bi_kv4_gather(cache: bi_kv4_cache, batch: bi_kv4_batch, k_out: torch.Tensor, v_out: torch.Tensor,
                   stream=None) -> None:
     """k_out, v_out: bf16 [T, Hkv, D], the cached values of the batch's token rows."""
-    for t in (k_out, v_out):
-        assert t.element_size() == 2 and t.is_contiguous()
-        assert t.shape[1:] == (cache.Hkv, cache.D) and t.shape[0] >= batch.T
+    T, Hkv, D = batch.T, cache.Hkv, cache.D
+    assert _heads(k_out, T, Hkv, D) == _heads(v_out, T, Hkv, D) == Hkv * D
     _check(lib.bi_kv4_gather(cache, batch, k_out.data_ptr(), v_out.data_ptr(), _stream(stream)), "bi_kv4_gather")
 
 
@@ -383,10 +382,11 @@ def new_attention_kv4_workspace(Hq: int, cache: bi_kv4_cache, batch: bi_kv4_batc
 def bi_attention_kv4(q: torch.Tensor, cache: bi_kv4_cache, batch: bi_kv4_batch, scale: float, o: torch.Tensor,
                      ws: torch.Tensor, flags: int = 0, stream=None) -> None:
     """q: bf16 [T, Hq, D] (row stride q.stride(0)); o: bf16 [T, Hq, D] out; ws: from new_attention_kv4_workspace."""
-    assert _is_heads(q, cache.D) and _is_heads(o, cache.D) and o.shape == q.shape and q.shape[0] >= batch.T
-    assert o.stride(0) == q.shape[1] * cache.D or q.shape[0] == 1
-    _check(lib.bi_attention_kv4(q.data_ptr(), _ld(q), q.shape[1], cache, batch, scale, o.data_ptr(), ws.data_ptr(),
-                                ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_attention_kv4")
+    T, Hq, D = batch.T, q.shape[1], cache.D
+    ldq = _heads(q, T, Hq, D)
+    assert _heads(o, T, Hq, D) == Hq * D
+    _check(lib.bi_attention_kv4(q.data_ptr(), ldq, Hq, cache, batch, scale, o.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                flags, _stream(stream)), "bi_attention_kv4")
 
 
 def logits_rules(ids: torch.Tensor | None = None, begin: torch.Tensor | None = None, mid: torch.Tensor | None = None,
@@ -422,11 +422,16 @@ def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.T
                       argmax: torch.Tensor | None, ws: torch.Tensor, flags: int = 0, stream=None) -> None:
     """logits: bf16 [M, V] (row stride logits.stride(0)); out: fp32 [M, V] or None; argmax: int32 [M] or None."""
     M, V = logits.shape
-    assert logits.element_size() == 2 and (logits.stride(1) == 1 or V == 1)
-    assert out is None or (out.dtype == torch.float32 and (out.stride(1) == 1 or V == 1))
-    _check(lib.bi_logits_process(logits.data_ptr(), _ld(logits), M, V, rules, _ptr(out),
-                                 _ld(out), _ptr(argmax), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), flags, _stream(stream)), "bi_logits_process")
+    ldl, sl = logits.stride()
+    assert (sl == 1 or V == 1) and logits.element_size() == 2
+    ldo = V
+    if out is not None:
+        ldo, so = out.stride()
+        assert (so == 1 or V == 1) and out.dtype == torch.float32
+    if M == 1:                                             # a single row's stride may be anything
+        ldl = ldo = V
+    _check(lib.bi_logits_process(logits.data_ptr(), ldl, M, V, rules, _ptr(out), ldo, _ptr(argmax), ws.data_ptr(),
+                                 ws.nbytes, flags, _stream(stream)), "bi_logits_process")
 
 
 def bi_probe_read(buf: torch.Tensor, out: torch.Tensor, stream=None) -> None:
