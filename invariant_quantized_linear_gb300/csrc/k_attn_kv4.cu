@@ -1078,10 +1078,11 @@ cudaError_t launch_attention_kv4(const AttnKv4Args &a, int D, bool pdl, cudaStre
     p.magic = (1ull << 32) / GH + 1;
     p.spans = spans_of(a.c.max_kv);
     p.pdl = pdl ? 1 : 0;
-    // 16 rows a CTA where there are as many.  A span a cluster while the spans alone leave SMs idle: it takes 5.5 us and
+    // 16 rows a CTA where there are as many, 8 while their clusters leave an SM at most two CTAs (b 1, 8 tokens, 2000
+    // positions: 8.7 us, with 16 rows 9.8; b 1, 4 tokens, 4104, above that: 12.3, with 16 11.7).  A span a cluster while the spans alone leave SMs idle: it takes 5.5 us and
     // 0.13 us more for each span of 8 rows (152 SMs), a span a CTA 18.8 us up to a span a SM; they meet at 105 spans.
     const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv;
-    const bool two = rows > 8;
+    const bool two = rows > 8 && kCluster * heads * ((rows + 7) / 8) * p.spans > 2 * a.sms;
     p.row_blocks = two ? (rows + 15) / 16 : (rows + 7) / 8;
     const bool split = 3 * heads * p.row_blocks * p.spans <= 2 * a.sms;
     p.count = heads * p.row_blocks * (split ? kCluster : 1) <= kCounters && p.spans <= kJoinSpans;
