@@ -670,3 +670,84 @@ def test_norm_forms_give_the_same_bits(bi, K):
     for a, b in ((0, 1), (1, 300), (300, 500), (699, 700)):
         for x, z in zip(go(a, b), whole):
             assert torch.equal(x, z[a:b])
+
+
+LONG = [
+    # sequences (new, total), Hq, Hkv, D, page, bound on the positions
+    ([(1, 4104)], 32, 8, 128, 64, 4104),                   # three spans of clusters, joined rank by rank
+    ([(8, 4104)], 32, 8, 128, 16, 9000),                   # 32 rows, a bound past the sequence
+    ([(1, 33000), (2, 32768), (1, 32769)], 2, 1, 64, 128, 33000),   # 17 spans: joined by a launch of its own
+    ([(5, 40000), (3, 70)], 7, 1, 64, 128, 40000),         # 35 rows: two blocks of 16 and one of 3
+    ([(1, 5000 - 7 * i) for i in range(40)], 8, 4, 128, 16, 5000),  # a span a CTA, joined by counters
+    ([(3, 2500 + i) for i in range(30)], 12, 2, 128, 32, 4000),     # 18 rows: a block of 16 and one of 2
+    ([(2, 2049 + 300 * i) for i in range(24)], 10, 2, 64, 16, 9000),
+    ([(130, 2200), (64, 64)], 4, 2, 128, 64, 2200),        # a prefill: hundreds of rows
+]
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,P,bound", LONG)
+def test_attention_long(bi, seqs, Hq, Hkv, D, P, bound):
+    """Contexts of several spans, filled by the append, in every split of the work; each sequence alone has the same bits."""
+    rng = np.random.default_rng(Hq * D + bound)
+    gen = torch.Generator(device=DEV).manual_seed(bound)
+    total = [n for _, n in seqs]
+    b = Batch(bi, [(n, n) for n in total], Hkv, D, P, seed=2)
+    b.to_device()
+    kv_in = torch.randn((2, b.T, Hkv, D), device=DEV, generator=gen).bfloat16()
+    none = torch.zeros((b.T, 1, D), dtype=torch.bfloat16, device=DEV)
+    bi.bi_rope_append_kv4(none, kv_in[0], kv_in[1], torch.zeros((max(total), 1, 2), device=DEV), 0, bi.BI_ROPE_HALF,
+                          torch.empty_like(none), b.cache, b.batch)
+    b.pool = b.d_pool.cpu().numpy()
+    b.seqs = seqs
+    b.cu = np.concatenate([[0], np.cumsum([q for q, _ in seqs])]).astype(np.int32)
+    b.T = int(b.cu[-1])
+    b.d[0] = torch.from_numpy(b.cu).to(DEV)
+    most = max(q for q, _ in seqs)
+    b.batch = bi.kv4_batch(*b.d, b.T, most, bound)
+    q = bits(rng, (b.T, Hq, D), 1.5)
+    o = attend(bi, b, q, D ** -0.5)
+    got = torch.from_numpy(ref.f32(host(o))).to(DEV).double()
+    for s in sorted({0, 1 % len(seqs), len(seqs) - 1}):
+        n_q, n = seqs[s]
+        k, v, ok = ref.read_sequence(b.pool[:, 0], P, D, b.pages[s], n)
+        assert ok.all()
+        k, v = (torch.from_numpy(x).to(DEV).double().repeat_interleave(Hq // Hkv, 1) for x in (k, v))
+        x = torch.from_numpy(ref.f32(q[b.cu[s]:b.cu[s] + n_q])).to(DEV).double()
+        scores = torch.einsum("qhd,nhd->qhn", x, k) * D ** -0.5
+        hidden = torch.arange(n, device=DEV)[None] > n - n_q + torch.arange(n_q, device=DEV)[:, None]
+        scores.masked_fill_(hidden[:, None], float("-inf"))
+        p = scores.softmax(-1)
+        want, mag = torch.einsum("qhn,nhd->qhd", p, v), torch.einsum("qhn,nhd->qhd", p, v.abs())
+        big = (torch.einsum("qhd,nhd->qhn", x.abs(), k.abs()) * D ** -0.5).amax(-1, keepdim=True)
+        tol = want.abs() * 2.0 ** -8 + mag * (2.0 ** -10 + 2 * (D + 16) * 2.0 ** -24 * (big + 1))
+        assert ((got[b.cu[s]:b.cu[s] + n_q] - want).abs() <= tol).all(), "sequence %d" % s
+        alone = Batch.__new__(Batch)
+        alone.T, alone.D, alone.cache = n_q, D, b.cache
+        alone.d = [torch.tensor(y, dtype=torch.int32, device=DEV) for y in ([0, n_q], [n], [b.pages[s].tolist()])]
+        alone.batch = bi.kv4_batch(*alone.d, n_q, n_q, n)
+        same(host(attend(bi, alone, q[b.cu[s]:b.cu[s] + n_q], D ** -0.5)), host(o)[b.cu[s]:b.cu[s] + n_q], "alone")
+
+
+def test_cache_past_32_bits(bi):
+    """Pages beyond the first 4 GiB of a pool: the same bytes, gathered values and attention as in a small pool."""
+    Hq, Hkv, D, P, n = 16, 8, 128, 128, 700
+    far = 2 ** 32 // (Hkv * bi.bi_kv4_block_bytes(P, D)) + 20
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    qkv = torch.randn((n, Hq + 2 * Hkv, D), device=DEV, generator=gen).bfloat16()
+    rope = torch.zeros((n, D // 2, 2), device=DEV)
+    bi.bi_rope_table(1e4 ** (-torch.arange(0, D, 2, dtype=torch.float64, device=DEV) / D), rope)
+    outs = []
+    for pages, where in ((10, range(6)), (far, range(far - 6, far))):
+        pool = torch.empty((pages, Hkv, bi.bi_kv4_block_bytes(P, D)), dtype=torch.uint8, device=DEV)
+        pool[list(where)] = 0
+        table = torch.tensor([list(where)], dtype=torch.int32, device=DEV)
+        cu, length = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, n], [n]))
+        c, batch = bi.kv4_cache(pool, P, D), bi.kv4_batch(cu, length, table, n, n, n)
+        q, k, v = (torch.empty((n, h, D), dtype=torch.bfloat16, device=DEV) for h in (Hq, Hkv, Hkv))
+        o = torch.empty_like(q)
+        bi.bi_rope_append_kv4(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], rope, D, bi.BI_ROPE_HALF, q, c, batch)
+        bi.bi_kv4_gather(c, batch, k, v)
+        bi.bi_attention_kv4(q, c, batch, D ** -0.5, o, bi.new_attention_kv4_workspace(Hq, c, batch))
+        outs.append([pool[list(where)], q, k, v, o])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
