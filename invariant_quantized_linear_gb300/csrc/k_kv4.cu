@@ -23,9 +23,9 @@ namespace bi {
 namespace {
 
 constexpr int kAppendWarps = 4;                      // warps of a CTA
-constexpr int kAppendCtas = 5;                       // CTAs a SM that the registers are to allow
+constexpr int kAppendCtas = 5;                       // CTAs a SM that the registers are to allow (8193 tokens: 44 us, 4 and 6: 48)
 constexpr int kBatch = 3;                            // heads (of a lane) in flight
-constexpr int kWholeBatch = 4;                       // the same for heads that are rotated whole; a power of two
+constexpr int kWholeBatch = 4;                       // the same for heads that are rotated whole; a power of two (2: 48 us)
 
 __global__ void __launch_bounds__(256) rope_table_kernel(const double *inv_freq, int n_freq, float amp, int n_pos,
                                                          float2 *rope)
