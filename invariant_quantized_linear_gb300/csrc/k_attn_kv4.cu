@@ -117,6 +117,15 @@ __device__ __forceinline__ void code_operands(uint32_t w, uint32_t (&o)[4])
     o[3] = w & 0x00F000F0u;
 }
 
+// The same with the even nibbles not taken out of their bytes: c0 + 16 c1, 16 c1 and so on.
+__device__ __forceinline__ void byte_operands(uint32_t w, uint32_t (&o)[4])
+{
+    o[0] = w & 0x00FF00FFu;
+    o[1] = w & 0x00F000F0u;
+    o[2] = __byte_perm(w, 0u, 0x4341);
+    o[3] = o[2] & 0x00F000F0u;
+}
+
 __device__ __forceinline__ float pow2_int(int e) { return __int_as_float((e + 127) << 23); }   // -126 .. 127
 
 // Shared memory of a CTA for head size D and NB blocks of 8 query rows.
@@ -466,34 +475,49 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         wait(0, blk);
         const unsigned char *par = mine + 2 * P::kCodes;
 
-        // ---- the values' scales and z / s, two positions a lane; nothing for positions that no row sees
+        // ---- the values' scales and z / s of positions 2 lane and 2 lane + 1; nothing for positions that no row sees
         uint32_t top_scale = 0;
+        {
+            uint32_t w[2][G];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int y = lane + 32 * i;
-            uint32_t w[2 * G];
-            lds_words<8 * G>(par + y * 8 * G, w);
-            const bool seen = ((there >> (y >> 4)) & 1u) && pb + y < n_most;
+            for (int i = 0; i < 2; ++i) {
+                uint32_t v[2 * G];
+                lds_words<8 * G>(par + (2 * lane + i) * 8 * G, v);
+#pragma unroll
+                for (int k = 0; k < G; ++k) w[i][k] = v[G + k];
+            }
+            if (!full) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!((there >> (lane >> 3)) & 1u) || pb + 2 * lane + i >= n_most) {
+#pragma unroll
+                        for (int k = 0; k < G; ++k) w[i][k] = 0;
+                    }
+            }
             // position y of tile y / 16 is element 2 t + (i & 1) + 8 (i / 2) of its rows, kept as 4 t + i
-            const int at = (y & 6) * 2 + (y & 1) + (y & 8) / 4;
-            float sv[G];
+            unsigned char *at = ratio + (lane >> 3) * (G * 64) + (lane & 3) * 8 + (lane & 4);
+            float sv[2][G];
 #pragma unroll
             for (int k = 0; k < G; ++k) {
-                const float zv = bf16_hi(w[G + k]);
-                const float v = w[G + k] & 0x7FFFu ? bf16_lo(w[G + k]) : 0.125f * fabsf(zv);
-                const bool some = seen && v >= kMinScale;
-                sv[k] = some ? v : 0.0f;
-                const float r = some ? __fdividef(zv, v) : 0.0f;
-                const __half hi = __float2half_rn(r), lo = __float2half_rn(r - __half2float(hi));
-                __half *dst = reinterpret_cast<__half *>(ratio + ((y >> 4) * G + k) * 64) + at;
-                dst[0] = hi;
-                dst[16] = lo;
-                top_scale = max(top_scale, __float_as_uint(sv[k]));
+                float r[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float sc = bf16_lo(w[i][k]), zv = bf16_hi(w[i][k]), v = sc != 0.0f ? sc : 0.125f * fabsf(zv);
+                    const bool some = v >= kMinScale;
+                    sv[i][k] = some ? v : 0.0f;
+                    r[i] = some ? __fdividef(zv, v) : 0.0f;
+                    top_scale = max(top_scale, __float_as_uint(sv[i][k]));
+                }
+                const __half2 hi = __floats2half2_rn(r[0], r[1]);
+                const float2 back = __half22float2(hi);
+                const __half2 lo = __floats2half2_rn(r[0] - back.x, r[1] - back.y);
+                *reinterpret_cast<__half2 *>(at + k * 64) = hi;
+                *reinterpret_cast<__half2 *>(at + k * 64 + 32) = lo;
             }
             if constexpr (G == 2)
-                *reinterpret_cast<float2 *>(scale + y * 8) = make_float2(sv[0], sv[G - 1]);
+                *reinterpret_cast<float4 *>(scale + lane * 16) = make_float4(sv[0][0], sv[0][G - 1], sv[1][0], sv[1][G - 1]);
             else
-                *reinterpret_cast<float *>(scale + y * 4) = sv[0];
+                *reinterpret_cast<float2 *>(scale + lane * 8) = make_float2(sv[0][0], sv[1][0]);
         }
 
         // ---- scores: the tiles' chains of products side by side
@@ -697,8 +721,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
 #pragma unroll
                     for (int tile = 0; tile < kTiles; ++tile) {
                         uint32_t x0[4], x1[4];
-                        code_operands(vw[2 * tile][2 * k + j], x0);
-                        code_operands(vw[2 * tile + 1][2 * k + j], x1);
+                        byte_operands(vw[2 * tile][2 * k + j], x0);
+                        byte_operands(vw[2 * tile + 1][2 * k + j], x1);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -715,8 +739,10 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
                             f2 *u = o[k][2 * j + h][nb];   // elements 2 h and 2 h + 1 of the word, two rows each
-                            u[0] = fma2(pk(acc[h][nb][0], acc[h][nb][1]), wo[nb], mul2(u[0], wa[nb]));
-                            u[1] = fma2(pk(acc[h][nb][2], acc[h][nb][3]), wq[nb], mul2(u[1], wa[nb]));
+                            const f2 odd = pk(acc[h][nb][2], acc[h][nb][3]),
+                                     even = fma2(odd, pk(-1.0f, -1.0f), pk(acc[h][nb][0], acc[h][nb][1]));
+                            u[0] = fma2(even, wo[nb], mul2(u[0], wa[nb]));
+                            u[1] = fma2(odd, wq[nb], mul2(u[1], wa[nb]));
                         }
                 }
         }
