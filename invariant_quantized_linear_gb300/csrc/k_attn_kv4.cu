@@ -9,7 +9,9 @@
 // an f16 word is the subnormal c 2^-24 and one nibble up c 2^-20, both exact
 // and taken by the tensor cores as they are.  One AND makes two operands, one
 // shift serves four.  The factors 16 of the odd nibbles are undone in q (keys)
-// and in the result (values).
+// and in the result (values).  A value's even nibble stays in its byte, with the
+// odd one: their sums' difference, in fp32, is the even nibbles' (an error of 2^-18
+// of the group's range, below the weights' 2^-11), and one operation less a word.
 //
 // Operands are transposed, S^T = K q^T and O^T = V^T P^T, so that positions
 // (16 of an mma.m16n8k16) and head elements fill the rows, and the few query
@@ -54,12 +56,12 @@
 // counters do not suffice.
 //
 // Bound: HBM by its bytes (0.5625 B an element) up to 16 query rows a kv head;
-// what it reaches is set by instructions and by the latency of a block's chain
-// (copies, products, maxima, exponentials, products) with the 8 to 20 warps a SM
-// that registers allow.  Measured (32 q and 8 kv heads of 128, caches out of L2):
-// b 96, up to 8191 positions 126 us, 4.56 TB/s of codes and parameters; b 1,
-// 131072: 43 us, 3.5 TB/s; b 64, 8 tokens, 4096: 140 us; b 1, 517: 6.4 us; 28 and
-// 4 heads of 64, b 6, 5 tokens, up to 40000: 49 us.
+// within a span it reads 6.2 TB/s, instructions, shared memory and HBM all near
+// their rates; a CTA's start and end (3.1 us) and the last wave are the rest.
+// Measured (32 q and 8 kv heads of 128, caches out of L2): b 304, 2048 positions
+// each 131 us, 5.5 TB/s of codes and parameters; b 96, up to 8191: 125 us, 4.6; b 1,
+// 131072: 43 us, 3.5; b 64, 8 tokens, 4096: 137 us; b 1, 517: 6.4 us; 28 and 4 heads
+// of 64, b 6, 5 tokens, up to 40000: 47.5 us.
 #include "ptx.cuh"
 #include "row_ops.cuh"
 #include "step.cuh"
@@ -956,8 +958,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
     }
 }
 
-// CTAs a SM: the registers decide.  16 rows of head size 128 spill 300 bytes at three (b 64, q 8, 4096 positions:
-// 148 us, at two 140); 8 rows of it, or 16 of head size 64, wait less for one another's copies at three than at four
+// CTAs a SM: the registers decide.  16 rows of head size 128 spill at three (b 64, q 8, 4096 positions: 148 us, at
+// two 140); 8 rows of it, or 16 of head size 64, wait less for one another's copies at three than at four
 // (b 96, 8191: 128 and 131 us; head size 64, b 6, q 5, 40000: 50 and 53); head size 64 wants five (b 64, 8192: 33 us, at
 // four 37).
 template <int D, int NB, bool SPLIT>
