@@ -160,7 +160,8 @@ bi_status bi_rope_append_kv4(const uint16_t *q, int64_t ldq, int Hq, const uint1
     if (st != BI_OK) return st;
     const int64_t D = cache->D, T = batch->T, wq = Hq * D, wk = cache->Hkv * D;
     if (!q || !k || !v || !q_out || !rope || Hq < 1 || Hq > kMaxHeads || ldq < wq || ldk < wk || ldv < wk || n_pos < 1 ||
-        rot < 0 || rot > D || (rot % (layout == BI_ROPE_HALF ? 8 : 4)) != 0 || (layout != BI_ROPE_HALF && layout != BI_ROPE_INTERLEAVED) ||
+        rot < 0 || rot > D || (rot % (layout == BI_ROPE_HALF ? 8 : 4)) != 0 ||
+        (layout != BI_ROPE_HALF && layout != BI_ROPE_INTERLEAVED) ||
         !finite_at_least(eps, 0.0f))
         return BI_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope) ||

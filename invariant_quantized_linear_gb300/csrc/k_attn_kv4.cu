@@ -530,7 +530,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
             for (int i = 0; i < 2 * kTiles; ++i) lds_words<P::kPiece>(mine + (i * 32 + lane) * P::kPiece, kw[i]);
             uint32_t tq[NB];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) tq[nb] = *reinterpret_cast<const uint32_t *>(smem + P::kT + (8 * nb + g) * 16 + 4 * t);
+            for (int nb = 0; nb < NB; ++nb)
+                tq[nb] = *reinterpret_cast<const uint32_t *>(smem + P::kT + (8 * nb + g) * 16 + 4 * t);
 #pragma unroll
             for (int tile = 0; tile < kTiles; ++tile) {
 #pragma unroll
@@ -559,7 +560,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
                         uint32_t q[NB][2];
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
-                            lds_words<8>(smem + P::kQ + (8 * nb + g) * P::kQRow + (64 * k + 16 * t + 8 * j + 4 * h) * 2, q[nb]);
+                            lds_words<8>(smem + P::kQ + (8 * nb + g) * P::kQRow + (64 * k + 16 * t + 8 * j + 4 * h) * 2,
+                                         q[nb]);
 #pragma unroll
                         for (int tile = 0; tile < kTiles; ++tile) {
                             uint32_t x0[4], x1[4];
@@ -581,7 +583,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
                             float *u = s[tile][nb] + 2 * half;
-                            const float2 v = upk(fma2(pk(sk, sk), pk(acc[tile][nb][2 * half], acc[tile][nb][2 * half + 1]), pk(u[0], u[1])));
+                            const float *x = acc[tile][nb] + 2 * half;
+                            const float2 v = upk(fma2(pk(sk, sk), pk(x[0], x[1]), pk(u[0], u[1])));
                             u[0] = v.x;
                             u[1] = v.y;
                         }
@@ -611,7 +614,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         float mb[NB][2];
         int es[NB][2];
         if (full) {
-            const int e_all = max(kMinExp, static_cast<int>(__reduce_max_sync(0xffffffffu, top_scale) >> 23) - 126);   // s < 2^e
+            // s < 2^e
+            const int e_all = max(kMinExp, static_cast<int>(__reduce_max_sync(0xffffffffu, top_scale) >> 23) - 126);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) es[nb][0] = es[nb][1] = e_all;
         } else {
@@ -714,7 +718,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         {
             uint32_t vw[2 * kTiles][W];
 #pragma unroll
-            for (int i = 0; i < 2 * kTiles; ++i) lds_words<P::kPiece>(mine + P::kCodes + (i * 4 + t) * Kv4Layout::v_pair(D) + g * P::kPiece, vw[i]);
+            for (int i = 0; i < 2 * kTiles; ++i)
+                lds_words<P::kPiece>(mine + P::kCodes + (i * 4 + t) * Kv4Layout::v_pair(D) + g * P::kPiece, vw[i]);
 #pragma unroll
             for (int k = 0; k < G; ++k)
 #pragma unroll
@@ -1107,8 +1112,9 @@ cudaError_t launch_attention_kv4(const AttnKv4Args &a, int D, bool pdl, cudaStre
     p.spans = spans_of(a.c.max_kv);
     p.pdl = pdl ? 1 : 0;
     // 16 rows a CTA where there are as many, 8 while their clusters leave an SM at most two CTAs (b 1, 8 tokens, 2000
-    // positions: 8.7 us, with 16 rows 9.8; b 1, 4 tokens, 4104, above that: 12.3, with 16 11.7).  A span a cluster while the spans alone leave SMs idle: it takes 5.5 us and
-    // 0.13 us more for each span of 8 rows (152 SMs), a span a CTA 18.8 us up to a span a SM; they meet at 105 spans.
+    // positions: 8.7 us, with 16 rows 9.8; b 1, 4 tokens, 4104, above that: 12.3, with 16 11.7).  A span a cluster while the
+    // spans alone leave SMs idle: it takes 5.5 us and 0.13 us more for each span of 8 rows (152 SMs), a span a CTA 18.8 us
+    // up to a span a SM; they meet at 105 spans.
     const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv;
     const bool two = rows > 8 && kCluster * heads * ((rows + 7) / 8) * p.spans > 2 * a.sms;
     p.row_blocks = two ? (rows + 15) / 16 : (rows + 7) / 8;

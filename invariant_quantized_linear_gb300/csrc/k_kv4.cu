@@ -23,7 +23,7 @@ namespace bi {
 namespace {
 
 constexpr int kAppendWarps = 4;                      // warps of a CTA
-constexpr int kAppendCtas = 5;                       // CTAs a SM that the registers are to allow (8193 tokens: 44 us, 4 and 6: 48)
+constexpr int kAppendCtas = 5;                       // CTAs a SM that the registers are to allow (4 and 6: 48 us for 44)
 constexpr int kBatch = 3;                            // heads (of a lane) in flight
 constexpr int kWholeBatch = 4;                       // the same for heads that are rotated whole; a power of two (2: 48 us)
 
@@ -99,7 +99,7 @@ __device__ __forceinline__ void codes_of(const float (&x)[N], uint32_t param, fl
     const float s = bf16_lo(param), z = bf16_hi(param);
     if (quick_scale(s)) {
 #pragma unroll
-        for (int e = 0; e < N; ++e)                        // rne, as in code_byte; (max - z) / s < 15.5: s is off by 2^-9 at most
+        for (int e = 0; e < N; ++e)                        // rne, as in code_byte; below 15.5: s is off by 2^-9 at most
             c[e] = __float_as_uint(__fadd_rn(quotient_rn(__fsub_rn(x[e], z), s, r), 12582912.0f)) & 15u;
     } else {
 #pragma unroll

@@ -17,7 +17,7 @@ namespace bi {
 
 namespace {
 
-constexpr int kFold = 256;              // the squares of chunks of 8 are added for every kFold-th chunk, then over kFold threads
+constexpr int kFold = 256;              // sums of squares of a row: chunk j of 8 elements goes to sum j % kFold
 
 template <int THREADS>
 __device__ __forceinline__ float2 block_sum_max(float s, float m, float2 *red)
@@ -102,8 +102,8 @@ __device__ __forceinline__ uint2 codes8(const float (&t)[8], float st, float r)
 __device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
 // C chunks of 8 elements a thread in registers; C = 0: any K, the row read twice.
-// The sum of a row does not depend on THREADS: chunk j goes to sum j % kFold, in order; then the kFold sums, in the order
-// of warps of 32.  With fewer threads than kFold the others' sums are zeros, with more they are handed over.
+// The sum of a row does not depend on THREADS: chunks to their sums in order, then the kFold sums in the order of warps
+// of 32.  With fewer threads than kFold the others' sums are zeros, with more they are handed over.
 template <int C, int THREADS>
 __global__ void __launch_bounds__(THREADS) rmsnorm_quant_kernel(NormArgs a, int pdl)
 {
