@@ -78,7 +78,7 @@ def calls(bi):
         "append": lambda c, b, **o: (lambda a: L.bi_rope_append_kv4(
             a["q"], a["ldq"], a["Hq"], a["k"], a["ldk"], a["v"], a["ldv"], a["qn"], a["kn"], a["eps"], a["rope"], a["n_pos"],
             a["rot"], a["layout"], a["out"], c, b, 0, None))(
-            {**dict(q=FAR, ldq=2048, Hq=8, k=FAR + 2048, ldk=2048, v=FAR + 3072, ldv=2048, qn=None, kn=None, eps=1e-6,
+            {**dict(q=FAR, ldq=2048, Hq=8, k=FAR + 2048, ldk=2048, v=FAR + 2048 + 1024, ldv=2048, qn=None, kn=None, eps=1e-6,
                     rope=FAKE, n_pos=100, rot=64, layout=0, out=2 * FAR), **o}),
         "gather": lambda c, b, **o: (lambda a: L.bi_kv4_gather(c, b, a["k"], a["v"], None))(
             {**dict(k=FAR, v=2 * FAR), **o}),
