@@ -16,7 +16,7 @@
 // 128259 take 48 us without rules, 6.4 TB/s.  A history is read once per slice,
 // from L2 after the first, and its four barriers and two looks are what the
 // stream of other CTAs hides in part only: 84 us with histories of 3000, biases
-// and masks (3.7 TB/s).  5 rows of 151936: 7.2 us.  Measured and not kept: the
+// and masks (3.7 TB/s).  5 rows of 151936: 7.0 us.  Measured and not kept: the
 // slices of a row as a cluster that sorts the history once (104 us), ids taken
 // in turn by a warp's lanes (84, small calls slower), CTAs of 128 or 512 threads
 // (89, 88), slices as long as balanced waves allow (85).  Rows of an odd vocabulary start
@@ -207,32 +207,38 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
     // f(i, element of the slice) for the history's: aligned fours from vb to ve, at most three ids before and after them
     const int head = hist ? static_cast<int>((0u - static_cast<unsigned>(reinterpret_cast<uintptr_t>(a.r.ids + begin) >> 2)) & 3u) : 0;
     const int vb = min(begin + head, max(begin, end)), ve = vb + (max(end - vb, 0) & ~3);
-    auto history = [&](auto f) {
+    auto load_ids = [&](int i0, int4 (&id)[kIds]) {
+#pragma unroll
+        for (int j = 0; j < kIds; ++j) {
+            const int i = i0 + 4 * j * kLogitsThreads;
+            id[j] = i < ve ? __ldg(reinterpret_cast<const int4 *>(a.r.ids + i)) : make_int4(-1, -1, -1, -1);
+        }
+    };
+    int4 ids[kIds];                                        // the first, on their way while the marks are cleared
+    if (hist) load_ids(vb + 4 * tid, ids);
+    const int bias0 = bias && tid < a.r.n_bias ? __ldg(a.r.bias_ids + static_cast<int64_t>(row) * a.r.n_bias + tid) : -1;
+    auto history = [&](auto f, bool loaded) {
         auto one = [&](int i, int id) {
-            if (static_cast<unsigned>(id) - first < n_ids && id >= 0) f(i, id - v0);
+            if (static_cast<unsigned>(id) - first < n_ids) f(i, id - v0);
         };
         if (tid < vb - begin) one(begin + tid, __ldg(a.r.ids + begin + tid));
         if (tid < end - ve) one(ve + tid, __ldg(a.r.ids + ve + tid));
         for (int i0 = vb + 4 * tid; i0 < ve; i0 += 4 * kIds * kLogitsThreads) {
-            int4 id[kIds];                                 // loads first: a mark in between would hold up the next
+            if (!loaded) load_ids(i0, ids);                // loads first: a mark in between would hold up the next
+            loaded = false;
 #pragma unroll
             for (int j = 0; j < kIds; ++j) {
                 const int i = i0 + 4 * j * kLogitsThreads;
-                id[j] = i < ve ? __ldg(reinterpret_cast<const int4 *>(a.r.ids + i)) : make_int4(-1, -1, -1, -1);
-            }
-#pragma unroll
-            for (int j = 0; j < kIds; ++j) {
-                const int i = i0 + 4 * j * kLogitsThreads;
-                one(i, id[j].x);
-                one(i + 1, id[j].y);
-                one(i + 2, id[j].z);
-                one(i + 3, id[j].w);
+                one(i, ids[j].x);
+                one(i + 1, ids[j].y);
+                one(i + 2, ids[j].z);
+                one(i + 3, ids[j].w);
             }
         }
     };
     auto biases = [&](auto f) {
         for (int i = tid; i < a.r.n_bias; i += kLogitsThreads) {
-            const int id = __ldg(a.r.bias_ids + static_cast<int64_t>(row) * a.r.n_bias + i);
+            const int id = i == tid ? bias0 : __ldg(a.r.bias_ids + static_cast<int64_t>(row) * a.r.n_bias + i);
             if (id >= first && id < past) f(i, id - v0);
         }
     };
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
                 atomicOr(&marked[k >> 5], 1u << (k & 31));
                 const int at = atomicAdd(&n_met, 1);
                 if (at < kMet) met[at] = static_cast<uint16_t>(k | (i >= mid ? 0x8000 : 0));
-            });
+            }, true);
         if (bias) biases(mark);
         __syncthreads();
         // ranks: a run of words a thread, over the warp, over the warps
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kLogitsThreads, kLogitsCtas) logits_kernel(Log
             if (m <= kMet) {
                 for (int i = tid; i < m; i += kLogitsThreads) count(met[i] & 0x8000u, met[i] & 0x7FFF);
             } else {
-                history([&](int i, int k) { count(i >= mid, k); });
+                history([&](int i, int k) { count(i >= mid, k); }, false);
             }
         }
         if (bias)
