@@ -250,12 +250,18 @@ __device__ __forceinline__ void stage_queries(const AttnKv4Args &a, unsigned cha
     // up = 2^(14 - floor(log2 top)), kept in fp32's range
     const int ex = max(-100, min(127, static_cast<int>(__float_as_uint(top) >> 23) - 127));
     const float up = pow2_int(14 - ex);
-    float sum = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        x[e] *= up;
-        sum += x[e];
-    }
+    for (int e = 0; e < E; ++e) x[e] *= up;
+    // A group's sum in an order that does not depend on E, and so not on the form that a call takes: fours, neighbouring
+    // fours, neighbours of those and so on, in the lane as long as it holds several.
+    float part[E / 4];
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e) part[e] = (x[4 * e] + x[4 * e + 1]) + (x[4 * e + 2] + x[4 * e + 3]);
+#pragma unroll
+    for (int o = 1; o < E / 4; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < E / 4; e += 2 * o) part[e] += part[e + o];
+    float sum = part[0];
 #pragma unroll
     for (int e = 0; e < E / 4; ++e) {                      // a lane's elements begin with an even pair
         const __half2 h0 = __floats2half2_rn(x[4 * e], x[4 * e + 1]),
@@ -264,7 +270,7 @@ __device__ __forceinline__ void stage_queries(const AttnKv4Args &a, unsigned cha
             make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
     }
 #pragma unroll
-    for (int o = kKv4Group / E / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 1; o < kKv4Group / E; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (at % kKv4Group == 0) {
         // three parts of 8 bits: all 24 of the sum
         uint16_t *dst = reinterpret_cast<uint16_t *>(smem + P::kT + rl * 16) + 3 * (at / kKv4Group);
