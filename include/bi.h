@@ -374,9 +374,12 @@ BI_API bi_status bi_rmsnorm_quantize(const uint16_t *h, int64_t ldh, const uint1
  *   c = clamp(rne((x - z) / s), 0, 15)  (fp32, IEEE division; 0 when s = 0)
  *   the value held is z + s * c.
  * x are bf16 values, so z is exact, and s is 0 or at least |z| / 4096, which a
- * cache filled in another way has to keep to.  Finite x only (other values give
- * codes and parameters without meaning, in their own group); values whose s lies
- * outside 2^-110 .. 2^118 lose precision in the attention.
+ * cache filled in another way has to keep to.  x and max x - min x have to be
+ * finite in fp32: other values give codes and parameters without meaning, in
+ * their own group (a value group whose s or z is not finite leaves no finite
+ * element of that group to the attention's rows that see its position, and
+ * touches no other row or group).
+ * Values whose s lies outside 2^-110 .. 2^118 lose precision in the attention.
  * Inside a block, P = page_size, G = D / 64, all words little-endian:
  *   keys       [P][4 segments][G][2 words], position-major: element d of a key
  *              is in segment (d % 64) / 16, group d / 64, word (d % 16) / 8,

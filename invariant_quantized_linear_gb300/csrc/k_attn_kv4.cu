@@ -82,6 +82,8 @@ constexpr int kCluster = kChunkBlocks;              // CTAs that share a span
 constexpr int kMinExp = -100;                       // least exponent that value scales are normalised to
 constexpr int kMaxExp = 118;                        // largest that is undone again within fp32
 constexpr float kMinScale = 0x1p-110f;              // groups of smaller scale count as zeros
+constexpr uint32_t kInfBits = 0x7F800000u;          // scales from here on are infinite or NaN
+constexpr float kMaxRatio = 65504.0f;               // largest z / s that f16 holds (of a valid group: 4096)
 constexpr int kCounters = 16384;                    // row blocks whose spans are counted in the workspace
 constexpr int kJoinSpans = 16;                      // spans that a CTA joins itself at most, and a run of the second launch
 constexpr size_t kStatusBytes = 256;                // the status word, then the counters, then the spans' results
@@ -350,6 +352,39 @@ struct SpanArgs {
     int pdl;
 };
 
+// A block's value groups that are not finite (sv, r: scales and z / s of positions 2 lane and 2 lane + 1).  A weight of
+// zero does not keep them from a row, so they are set to nothing for the products, and the minima's term (z, of the
+// lane's columns) of the rows that see them, which joins the values of their group alone, becomes NaN.  Returns the bits
+// of the largest other scale.  Rows see seen[] positions, the block's begin at pb.
+template <int NB, int G>
+__device__ __forceinline__ uint32_t set_aside(const int *seen, int pb, float (&sv)[2][G], float (&r)[2][G], f2 (&z)[NB][G])
+{
+    const int t = threadIdx.x & 3;
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < G; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool bad = __float_as_uint(sv[i][k]) >= kInfBits || !(fabsf(r[i][k]) <= kMaxRatio);
+            const unsigned at = __ballot_sync(0xffffffffu, bad);
+            if (bad) sv[i][k] = r[i][k] = 0.0f;
+            top = max(top, __float_as_uint(sv[i][k]));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                // of the positions 2 l + i the row sees those of the first n lanes
+                auto sees = [&](int row) {
+                    const int n = max(0, min(32, (seen[row] - pb - i + 1) >> 1));
+                    return (at & static_cast<unsigned>((1ull << n) - 1)) != 0;
+                };
+                float2 v = upk(z[nb][k]);
+                if (sees(8 * nb + 2 * t)) v.x = __int_as_float(0x7FC00000);
+                if (sees(8 * nb + 2 * t + 1)) v.y = __int_as_float(0x7FC00000);
+                z[nb][k] = pk(v.x, v.y);
+            }
+        }
+    return __reduce_max_sync(0xffffffffu, top);
+}
+
 // What a CTA finds before it knows how many rows it has.
 struct Task {
     int rank, hk, rb, b, span;
@@ -484,7 +519,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         const unsigned char *par = mine + 2 * P::kCodes;
 
         // ---- the values' scales and z / s of positions 2 lane and 2 lane + 1; nothing for positions that no row sees
-        uint32_t top_scale = 0;
+        uint32_t top_scale = 0;                            // bits of the block's largest
         {
             uint32_t w[2][G];
 #pragma unroll
@@ -502,23 +537,28 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
                         for (int k = 0; k < G; ++k) w[i][k] = 0;
                     }
             }
-            // position y of tile y / 16 is element 2 t + (i & 1) + 8 (i / 2) of its rows, kept as 4 t + i
-            unsigned char *at = ratio + (lane >> 3) * (G * 64) + (lane & 3) * 8 + (lane & 4);
-            float sv[2][G];
+            float sv[2][G], r[2][G];
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                float r[2];
+            for (int k = 0; k < G; ++k)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float sc = bf16_lo(w[i][k]), zv = bf16_hi(w[i][k]), v = sc != 0.0f ? sc : 0.125f * fabsf(zv);
-                    const bool some = v >= kMinScale;
+                    const bool some = !(v < kMinScale);    // a scale that is NaN too
                     sv[i][k] = some ? v : 0.0f;
-                    r[i] = some ? __fdividef(zv, v) : 0.0f;
+                    r[i][k] = some ? __fdividef(zv, v) : 0.0f;
                     top_scale = max(top_scale, __float_as_uint(sv[i][k]));
+                    if (!full && !(fabsf(r[i][k]) <= kMaxRatio)) top_scale = ~0u;
                 }
-                const __half2 hi = __floats2half2_rn(r[0], r[1]);
+            top_scale = __reduce_max_sync(0xffffffffu, top_scale);
+            if (top_scale >= kInfBits)
+                top_scale = set_aside<NB, G>(reinterpret_cast<const int *>(smem + P::kN), pb, sv, r, z);
+            // position y of tile y / 16 is element 2 t + (i & 1) + 8 (i / 2) of its rows, kept as 4 t + i
+            unsigned char *at = ratio + (lane >> 3) * (G * 64) + (lane & 3) * 8 + (lane & 4);
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                const __half2 hi = __floats2half2_rn(r[0][k], r[1][k]);
                 const float2 back = __half22float2(hi);
-                const __half2 lo = __floats2half2_rn(r[0] - back.x, r[1] - back.y);
+                const __half2 lo = __floats2half2_rn(r[0][k] - back.x, r[1][k] - back.y);
                 *reinterpret_cast<__half2 *>(at + k * 64) = hi;
                 *reinterpret_cast<__half2 *>(at + k * 64 + 32) = lo;
             }
@@ -621,7 +661,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         int es[NB][2];
         if (full) {
             // s < 2^e
-            const int e_all = max(kMinExp, static_cast<int>(__reduce_max_sync(0xffffffffu, top_scale) >> 23) - 126);
+            const int e_all = max(kMinExp, static_cast<int>(top_scale >> 23) - 126);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) es[nb][0] = es[nb][1] = e_all;
         } else {

@@ -84,3 +84,75 @@ def test_queries_of_many_binades_in_every_form(bi, D):
                               ("8 rows, clusters", 8, 60)):
         bad = differ(s.attend(q[:, :heads], each), want[:, :heads].contiguous())
         assert bad == 0, "%s: %d elements of %d differ" % (what, bad, want[:, :heads].numel())
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+def verify_pass(bi, seqs, Hkv, D, P, copies=1, seed=5):
+    """A batch of `copies` times the sequences, each on pages of its own, filled by the append."""
+    rng = np.random.default_rng(seed)
+    b = step.Batch(bi, [(n, n) for _, n in seqs] * copies, Hkv, D, P, seed=seed)
+    b.pool[:] = 0
+    b.to_device()
+    x = torch.from_numpy(rng.normal(size=(2, b.T, Hkv, D)).astype(np.float32)).to(DEV).bfloat16()
+    append(bi, b, *x)
+    b.seqs = seqs * copies
+    b.kv_x, b.first = x, b.cu
+    b.cu = np.concatenate([[0], np.cumsum([q for q, _ in b.seqs])]).astype(np.int32)
+    b.T = int(b.cu[-1])
+    b.d[0] = torch.from_numpy(b.cu).to(DEV)
+    b.batch = bi.kv4_batch(*b.d, b.T, max(q for q, _ in seqs), b.max_kv)
+    return b
+
+
+def append(bi, b, k, v):
+    """k and v, not rotated, to the cache at the batch's positions."""
+    none = torch.zeros((b.T, 1, b.D), dtype=torch.bfloat16, device=DEV)
+    bi.bi_rope_append_kv4(none, k, v, torch.zeros((b.max_kv, 1, 2), device=DEV), 0, bi.BI_ROPE_HALF, torch.empty_like(none),
+                          b.cache, b.batch)
+
+
+@pytest.mark.parametrize("copies", [1, 40])
+@pytest.mark.parametrize("D,P", [(64, 16), (64, 128), (128, 32), (128, 64)])
+@pytest.mark.parametrize("kind", ["inf", "-inf", "nan scale", "inf minimum", "key"])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(bi, kind, D, P, copies):
+    """A drafted token whose value (or key) has an element that is not finite: tokens before it have the bits that they have
+    without it, those that see it NaN in the elements of its group and finite ones elsewhere."""
+    Hq, Hkv = 4, 2
+    seqs = [(5, 70), (3, 64), (4, 130), (9, 9)]
+    at = [2, 1, 0, 7]                                          # the token that has it
+    b = verify_pass(bi, seqs, Hkv, D, P, copies)
+    rng = np.random.default_rng(1)
+    q = torch.from_numpy(np.tile(rng.normal(size=(sum(n for n, _ in seqs), Hq, D)), (copies, 1, 1)).astype(np.float32)).to(DEV).bfloat16()
+    clean = step.attend(bi, b, q, D ** -0.5)
+    x = b.kv_x.clone()
+    table, G = b.pages, D // 64
+    for s, ((n_q, n), i) in enumerate(zip(b.seqs, at * copies)):
+        pos = n - n_q + i
+        if kind in ("inf", "-inf", "key"):
+            x[0 if kind == "key" else 1, b.first[s] + pos, 1, 3] = float("-inf" if kind == "-inf" else "inf")
+        else:                                                  # parameters of the first group of kv head 1's value
+            words = b.d_pool[table[s, pos // P], 0, 1, P * D:].view(torch.int16).view(P, 2, G, 2)
+            if kind == "nan scale":
+                words[pos % P, 1, 0, 0] = 0x7FC0
+            else:
+                words[pos % P, 1, 0, 1] = 0x7F80
+    if kind in ("inf", "-inf", "key"):
+        whole, now = b.batch, b.T
+        b.T = x.shape[1]
+        cu = torch.from_numpy(b.first).to(DEV)
+        b.batch = bi.kv4_batch(cu, b.d[1], b.d[2], b.T, max(n for _, n in seqs), b.max_kv)
+        append(bi, b, *x)
+        b.batch, b.T = whole, now
+    o = step.attend(bi, b, q, D ** -0.5)
+    value = lambda t: t.view(torch.bfloat16).float()
+    for s, ((n_q, n), i) in enumerate(zip(b.seqs, at * copies)):
+        a = b.cu[s]
+        assert torch.equal(o[a:a + i], clean[a:a + i]), "sequence %d: a row before token %d" % (s, i)
+        assert torch.equal(o[a:a + n_q, :2], clean[a:a + n_q, :2]), "sequence %d: the other kv head" % s
+        if kind != "key":
+            after = value(o[a + i:a + n_q, 2:])
+            assert after[..., :64].isnan().all(), "sequence %d" % s
+            # the other group: both results rounded to bf16, and their weights to f16, both ways; |v| < 6
+            was = value(clean[a + i:a + n_q, 2:])[..., 64:]
+            assert ((after[..., 64:] - was).abs() <= 2 * (was.abs() * 2.0 ** -8 + 6 * 2.0 ** -10)).all(), "sequence %d" % s
