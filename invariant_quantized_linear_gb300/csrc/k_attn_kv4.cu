@@ -155,8 +155,10 @@ struct Plan {
     static constexpr int kN = kF + R * 4;                  // positions that a row sees
     static constexpr int kM = kN + R * 4;                  // maxima [warp][row]
     static constexpr int kL = kM + kChunks * R * 4;        // sums [chunk][row]
-    // in a cluster: the chunks' maxima [chunk][row] and values of the CTA's rows [chunk][item]
-    static constexpr int kC = kL + kChunks * R * 4;
+    // in a cluster: exponents of value scales [warp][row], the chunks' maxima [chunk][row] and values of the CTA's rows
+    // [chunk][item]
+    static constexpr int kE = kL + kChunks * R * 4;
+    static constexpr int kC = kE + (SPLIT ? kChunks * R * 4 : 0);
     static constexpr int kV = kC + (SPLIT ? kChunks * R * 4 : 0);
     static constexpr int kFlag = kV + (SPLIT ? kO / 8 * kChunks : 0);
     static constexpr int kBar = kFlag + 16;                // two barriers a warp: keys and parameters, values
@@ -315,14 +317,24 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The fold of a block's result into a chunk's: weights of the two sides.
-__device__ __forceinline__ float fold_weights(float m, float mb, float &wa, float &wb)
+// The fold of a block's result into a chunk's: weights of the two sides, the block's with its power of two undone,
+// 2^(es - 15) but for 2^5.  The product may be subnormal, so both forms of the kernel fold with it as it is.
+__device__ __forceinline__ float fold_weights(float m, float mb, int es, float &wa, float &wb)
 {
     const float top = fmaxf(m, mb), ref = top == -INFINITY ? 0.0f : top;
     wa = ex2(m - ref);
-    wb = ex2(mb - ref);
+    wb = ex2(mb - ref) * pow2_int(min(es, kMaxExp) - 20);
     return top;
 }
+
+constexpr float kFoldSum = 32.0f;                   // what is left of the power of two in sums of weights (exact products),
+constexpr float kFoldEven = 0x1p29f;                // in products with codes, which carry 2^-24,
+constexpr float kFoldOdd = 0x1p25f;                 // and 2^-20 in odd elements
+
+__device__ __forceinline__ f2 times2(f2 v, float f) { return mul2(v, pk(f, f)); }
+
+// a + the block's b
+__device__ __forceinline__ f2 fold2(f2 a, f2 wa, f2 b, f2 wb) { return fma2(b, wb, mul2(a, wa)); }
 
 // out[row] from the joined value v (4 elements at d) and sum.
 template <int D>
@@ -484,6 +496,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
     stage_queries<D, NB, SPLIT>(a, smem, rows);
     unsigned char *scale = mine + 2 * P::kCodes + P::kPar, *ratio = scale + P::kScale;
     if (lane < 8) *reinterpret_cast<uint32_t *>(ratio + P::kRatio + 4 * lane) = 0;
+    if (SPLIT && lane < P::R) *reinterpret_cast<int *>(smem + P::kE + (warp * P::R + lane) * 4) = 0;   // a warp may have no block
     // this lane's part of z / s as rows of V^T: row 0 the first parts, row 1 the second, no others
     const unsigned char *my_ratio = g < 2 ? ratio + g * 32 + t * 8 : ratio + P::kRatio + t * 8;
     const int ratio_step = g < 2 ? 64 : 0;
@@ -739,24 +752,32 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
             }
         }
 
-        // ---- weights of the fold: the chunk's side, and the block's with its power of two undone
+        // ---- the fold of sums and maxima; in a cluster, blocks are folded where all of them meet
         f2 wa[NB], wo[NB], wq[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            float u[2], v[2];
+            if constexpr (SPLIT) {
+                m[nb][0] = mb[nb][0], m[nb][1] = mb[nb][1];
+                if (g == 0)
+                    *reinterpret_cast<int2 *>(smem + P::kE + (warp * P::R + 8 * nb + 2 * t) * 4) =
+                        make_int2(es[nb][0], es[nb][1]);
+                l[nb] = times2(lb[nb], kFoldSum);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                m[nb][i] = fold_weights(m[nb][i], mb[nb][i], u[i], v[i]);
-                v[i] *= pow2_int(min(es[nb][i], kMaxExp) - 20);   // 2^(es - 15), its 2^5 left out
+                for (int k = 0; k < G; ++k)
+                    z[nb][k] = fma2(pk(zb[k][nb][0], zb[k][nb][1]), pk(kFoldSum, kFoldSum), z[nb][k]);   // on 0 or NaN
+            } else {
+                float u[2], v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) m[nb][i] = fold_weights(m[nb][i], mb[nb][i], es[nb][i], u[i], v[i]);
+                wa[nb] = pk(u[0], u[1]);
+                const f2 wb = pk(v[0], v[1]);
+                l[nb] = fold2(l[nb], wa[nb], times2(lb[nb], kFoldSum), wb);
+#pragma unroll
+                for (int k = 0; k < G; ++k)
+                    z[nb][k] = fold2(z[nb][k], wa[nb], times2(pk(zb[k][nb][0], zb[k][nb][1]), kFoldSum), wb);
+                wo[nb] = times2(wb, kFoldEven);
+                wq[nb] = times2(wb, kFoldOdd);
             }
-            wa[nb] = pk(u[0], u[1]);
-            const f2 wb = pk(v[0], v[1]);
-            l[nb] = fma2(mul2(lb[nb], pk(32.0f, 32.0f)), wb, mul2(l[nb], wa[nb]));
-#pragma unroll
-            for (int k = 0; k < G; ++k)
-                z[nb][k] = fma2(mul2(pk(zb[k][nb][0], zb[k][nb][1]), pk(32.0f, 32.0f)), wb, mul2(z[nb][k], wa[nb]));
-            wo[nb] = mul2(wb, pk(0x1p29f, 0x1p29f));        // and products carry 2^-24, odd elements 2^-20
-            wq[nb] = mul2(wb, pk(0x1p25f, 0x1p25f));
         }
 
         // ---- weighted values
@@ -794,8 +815,8 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
                             f2 *u = o[k][2 * j + h][nb];   // elements 2 h and 2 h + 1 of the word, two rows each
                             const f2 odd = pk(acc[h][nb][2], acc[h][nb][3]),
                                      even = fma2(odd, pk(-1.0f, -1.0f), pk(acc[h][nb][0], acc[h][nb][1]));
-                            u[0] = fma2(even, wo[nb], mul2(u[0], wa[nb]));
-                            u[1] = fma2(odd, wq[nb], mul2(u[1], wa[nb]));
+                            u[0] = SPLIT ? times2(even, kFoldEven) : fold2(u[0], wa[nb], even, wo[nb]);
+                            u[1] = SPLIT ? times2(odd, kFoldOdd) : fold2(u[1], wa[nb], odd, wq[nb]);
                         }
                 }
         }
@@ -858,12 +879,13 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         const int nbr = NB == 2 ? rank / 4 : 0, tr = NB == 2 ? rank % 4 : rank / 2;
         float *chunk_max = reinterpret_cast<float *>(smem + P::kC);
         uint32_t cta[kCluster];
-        f2 mj[kChunkBlocks], lj[kChunkBlocks], zj[kChunkBlocks][G], ll = 0, zz[G];
+        f2 mj[kChunkBlocks], ej[kChunkBlocks], lj[kChunkBlocks], zj[kChunkBlocks][G], ll = 0, zz[G];
 #pragma unroll
         for (int j = 0; j < kChunkBlocks; ++j) {
             cta[j] = cluster_map(smem_u32(smem), j);
             const uint32_t lz = cta[j] + warp * P::kWarp + P::kO;
             mj[j] = ld_cluster_b64(cta[j] + P::kM + (warp * P::R + 8 * nbr + 2 * tr) * 4);
+            ej[j] = ld_cluster_b64(cta[j] + P::kE + (warp * P::R + 8 * nbr + 2 * tr) * 4);
             lj[j] = ld_cluster_b64(lz + (nbr * 32 + 4 * g + tr) * 8);
 #pragma unroll
             for (int k = 0; k < G; ++k)
@@ -877,13 +899,13 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         for (int j = 0; j < kChunkBlocks; ++j) {
             const float2 x = upk(mj[j]);
             float u[2], v[2];
-            mm[0] = fold_weights(mm[0], x.x, u[0], v[0]);
-            mm[1] = fold_weights(mm[1], x.y, u[1], v[1]);
+            mm[0] = fold_weights(mm[0], x.x, static_cast<int>(ej[j]), u[0], v[0]);
+            mm[1] = fold_weights(mm[1], x.y, static_cast<int>(ej[j] >> 32), u[1], v[1]);
             fa[j] = pk(u[0], u[1]);
             fb[j] = pk(v[0], v[1]);
-            ll = fma2(lj[j], fb[j], mul2(ll, fa[j]));
+            ll = fold2(ll, fa[j], lj[j], fb[j]);
 #pragma unroll
-            for (int k = 0; k < G; ++k) zz[k] = fma2(zj[j][k], fb[j], mul2(zz[k], fa[j]));
+            for (int k = 0; k < G; ++k) zz[k] = fold2(zz[k], fa[j], zj[j][k], fb[j]);
         }
         const f2 sum = over_lanes(ll);
         if (lane == 0) {

@@ -156,3 +156,25 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(bi, kind, D
             # the other group: both results rounded to bf16, and their weights to f16, both ways; |v| < 6
             was = value(clean[a + i:a + n_q, 2:])[..., 64:]
             assert ((after[..., 64:] - was).abs() <= 2 * (was.abs() * 2.0 ** -8 + 6 * 2.0 ** -10)).all(), "sequence %d" % s
+
+
+# ------------------------------------------------------------------ values that are zero, or nearly
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sigma", [0.0, 1e-27])
+def test_blocks_of_small_values_far_below_the_maximum(bi, D, sigma):
+    """Blocks whose values are zero or tiny and whose scores lie 11 to 20 binades below the row's largest: their part of
+    the softmax sum is the same with a span a CTA as with a span a cluster."""
+    rng = np.random.default_rng(7)
+    n, N, H = 2048, 2000, 8
+    k, v = np.zeros((n, D), np.float32), (rng.normal(size=(n, D)) * sigma).astype(np.float32)
+    for p in (0, 64, 128, 192):                                # the first block of every chunk has one position that counts
+        k[p, :4], v[p] = (15 / 15, 1 / 15, 2 / 15, 4 / 15), rng.normal(size=D)
+    s = Shared(bi, k, v)
+    q = rng.normal(size=(N, H, D)).astype(np.float32)
+    q[..., 0] = rng.uniform(8, 14, (N, H)) / 0.125
+    q[..., 1:4] *= 4                                           # scores of many different fractions
+    q = torch.from_numpy(q).to(DEV).bfloat16()
+    want = s.attend(q, N)
+    bad = differ(s.attend(q, 100), want)
+    assert bad == 0, "%d elements of %d differ" % (bad, want.numel())
