@@ -409,11 +409,13 @@ typedef struct {
  * sequence b is kept in page pages[b * ld_pages + p / page_size] of the pool,
  * at p % page_size.  The arrays are read on the device, so a captured graph
  * can be replayed with other lengths and pages; T, max_q and max_kv are bounds
- * that the host knows.  Rows from T on, tokens of a sequence past max_q and
- * positions past max_kv are left out, like positions whose page index lies
- * outside the table or whose page is not in 0 .. num_pages - 1: they are not
- * written, not attended to, and gathered as zeros; a token so left out has
- * zeros for its outputs.  Token rows from cu_q[B] on belong to no sequence:
+ * that the host knows.  Rows from T on are not touched.  Tokens of a sequence
+ * past max_q, or at a position from max_kv on, are left out: their key and value
+ * are not written, their q, attention and gathered values are zeros.  Positions
+ * whose page index lies outside the table, or whose page is not in 0 ..
+ * num_pages - 1, are not written, not attended to, and gathered as zeros; the
+ * q of a token at such a position is rotated, and its attention goes over the
+ * positions that have pages.  Token rows from cu_q[B] on belong to no sequence:
  * their outputs are not touched.
  */
 typedef struct {
@@ -451,8 +453,8 @@ BI_API bi_status bi_rope_table(const double *inv_freq, int n_freq, float amp, in
  *        becomes (a c - b s, b c + a s); pair i is (i, i + rot / 2) with
  *        BI_ROPE_HALF and (2 i, 2 i + 1) with BI_ROPE_INTERLEAVED;
  *   bf16_rne; k and v (v as given) are then quantised as bi_kv4_cache says.
- * A token at a negative position or one past n_pos has q_out 0 and is not
- * appended.
+ * A token at a negative position, or at one from n_pos on, has q_out 0 and is
+ * not appended either.
  *   q  bf16, row t and head h at q + t ldq + h D, Hq heads (read only)
  *   k, v  bf16, rows of Hkv heads with strides ldk, ldv
  *        (the three may be parts of one packed projection output)

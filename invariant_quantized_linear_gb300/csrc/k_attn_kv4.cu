@@ -212,11 +212,8 @@ struct Rows {
     __device__ __forceinline__ int token(int r) const { return static_cast<int>((r * magic) >> 32); }
 };
 
-// Positions that row r sees.
-__device__ __forceinline__ int row_positions(const AttnKv4Args &a, const Rows &w, int r)
-{
-    return min(a.c.max_kv, w.first + w.token(r) + 1);
-}
+// Positions that row r sees: at most max_kv, or the row would have been left out.
+__device__ __forceinline__ int row_positions(const Rows &w, int r) { return w.first + w.token(r) + 1; }
 
 // Query rows to shared memory: f16 elements scaled by a power of two, odd
 // element pairs divided by 16; the sums and the factor that turn products with
@@ -291,7 +288,7 @@ __device__ __forceinline__ void stage_queries(const AttnKv4Args &a, unsigned cha
             // scores = factor * (products with 2^-24 c and up q)
             *reinterpret_cast<float *>(smem + P::kF + rl * 4) =
                 fmaxf(fminf(a.scale * 1.4426950408889634f * 0x1p10f * pow2_int(ex), 0x1p126f), 0x1p-126f);
-            *reinterpret_cast<int *>(smem + P::kN + rl * 4) = min(a.c.max_kv, rows.first + tok + 1);
+            *reinterpret_cast<int *>(smem + P::kN + rl * 4) = rows.first + tok + 1;
         }
     }
 }
@@ -402,6 +399,11 @@ struct Task {
     int rank, hk, rb, b, span;
     int my_pos, page;                            // the lane's 16 positions and their page
     int cu0, cu1, len;
+
+    __device__ __forceinline__ int first() const { return len - (cu1 - cu0); }       // position of the first new token
+    __device__ __forceinline__ int tokens(const Kv4View &c) const { return min(c.T, max(0, cu1)) - max(0, cu0); }
+    // tokens that are not left out: those before max_q, at positions before max_kv
+    __device__ __forceinline__ int live(const Kv4View &c) const { return min(min(tokens(c), c.max_q), c.max_kv - first()); }
 };
 
 // One span (SPLIT: the CTA's eighth of it) for rows block_rows rb .. of a kv head, at most 8 NB.
@@ -423,10 +425,10 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
     rows.hk = task.hk;
     rows.magic = p.magic;
     rows.r0 = rb * block_rows;
-    rows.first = task.len - (task.cu1 - task.cu0);                       // position of the first new token
-    const int tokens = min(c.T, max(0, task.cu1)) - rows.t0, n_rows = min(tokens, c.max_q) * rows.GH;
-    if (rb == 0 && span == 0 && rank == 0)                // tokens past max_q are left out: zeros
-        for (int64_t i = static_cast<int64_t>(c.max_q) * rows.GH * (D / 4) + threadIdx.x;
+    rows.first = task.first();
+    const int tokens = task.tokens(c), live = task.live(c), n_rows = live * rows.GH;
+    if (rb == 0 && span == 0 && rank == 0)                // the other tokens have zeros
+        for (int64_t i = static_cast<int64_t>(max(0, live)) * rows.GH * (D / 4) + threadIdx.x;
              i < static_cast<int64_t>(tokens) * rows.GH * (D / 4); i += kThreads) {
             const int64_t r = i / (D / 4), tok = r / rows.GH;
             write_out<D>(a, (rows.t0 + tok) * a.Hq + rows.hk * rows.GH + r - tok * rows.GH, static_cast<int>(i % (D / 4)) * 4,
@@ -434,7 +436,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         }
     if (rows.r0 >= n_rows) return;
     rows.r_last = min(n_rows, rows.r0 + P::R) - 1;
-    const int n_most = row_positions(a, rows, rows.r_last), n_least = row_positions(a, rows, rows.r0);
+    const int n_most = row_positions(rows, rows.r_last), n_least = row_positions(rows, rows.r0);
     if (p0 >= n_most && (span > 0 || n_most > 0)) return;
     if (my_pos >= n_most) page = -1;
     const unsigned pages = __ballot_sync(0xffffffffu, page >= 0);
@@ -945,7 +947,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
     for (int i = threadIdx.x; i < kItems; i += kThreads) {
         const int e = rank * kItems + i, rl = e / (D / 4), d = e % (D / 4) * 4, r = rows.r0 + rl;
         if (r > rows.r_last) break;
-        const int tok = rows.token(r), n = min(c.max_kv, rows.first + tok + 1);
+        const int tok = rows.token(r), n = rows.first + tok + 1;
         if (p0 >= n && (span > 0 || n > 0)) continue;
         float mc[kChunks], top = -INFINITY, sum = 0.0f;
         float4 vc[kChunks];
@@ -999,7 +1001,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
     for (int i = threadIdx.x; i < kItems; i += kThreads) {
         const int e = rank * kItems + i, rl = e / (D / 4), d = e % (D / 4) * 4, r = rows.r0 + rl;
         if (r > rows.r_last) break;
-        const int tok = rows.token(r), n = min(c.max_kv, rows.first + tok + 1);
+        const int tok = rows.token(r), n = rows.first + tok + 1;
         if (n <= kSpan) continue;
         const int64_t at = static_cast<int64_t>(rows.t0 + tok) * a.Hq + rows.hk * rows.GH + r - tok * rows.GH;
         const float *part =
@@ -1064,8 +1066,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NB, SPLIT>) attn_kv4_s
     task.len = __ldg(c.kv_len + task.b);
     if constexpr (NB == 2) {
         // a last block of at most 8 rows does not pay for 16
-        const int n_rows = min(min(c.T, max(0, task.cu1)) - max(0, task.cu0), c.max_q) * (p.a.Hq / c.Hkv);
-        if (n_rows - task.rb * 16 <= 8) return span_task<D, 1, SPLIT>(p, task, 16, smem);
+        if (task.live(c) * (p.a.Hq / c.Hkv) - task.rb * 16 <= 8) return span_task<D, 1, SPLIT>(p, task, 16, smem);
     }
     span_task<D, NB, SPLIT>(p, task, 8 * NB, smem);
 }
@@ -1087,8 +1088,8 @@ __global__ void __launch_bounds__(2 * D) attn_kv4_join_kernel(AttnKv4Args a, int
     const int b = kv4_sequence(a.c, t);
     if (b < 0) return;
     const int begin = __ldg(a.c.cu_q + b), end = __ldg(a.c.cu_q + b + 1);
-    const int n = min(a.c.max_kv, __ldg(a.c.kv_len + b) - (end - t) + 1);
-    if (t - begin >= a.c.max_q || n <= kSpan) return;
+    const int n = __ldg(a.c.kv_len + b) - (end - t) + 1;
+    if (t - begin >= a.c.max_q || n > a.c.max_kv || n <= kSpan) return;
     const int C = (n + kSpan - 1) / kSpan;
     const float *part = reinterpret_cast<const float *>(static_cast<char *>(a.ws) + kCounterBytes) +
                         static_cast<int64_t>(blockIdx.x) * spans * (D + 4);

@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas) rope_append_ke
     const Kv4Token tok = kv4_token(a.c, t);
     if (tok.b < 0) return;
     uint16_t *const qo = a.q_out + (static_cast<int64_t>(t) * a.Hq + hl) * D + d;
-    if (tok.pos < 0 || tok.pos >= a.n_pos) {
+    if (tok.pos < 0 || tok.pos >= min(a.n_pos, a.c.max_kv)) {
         for (int step = first; step < min(last, q_steps); ++step)
             if (step * HEADS + hl < a.Hq) *reinterpret_cast<uint4 *>(qo + step * (HEADS * D)) = make_uint4(0u, 0u, 0u, 0u);
         return;

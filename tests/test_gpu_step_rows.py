@@ -158,6 +158,69 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(bi, kind, D
             assert ((after[..., 64:] - was).abs() <= 2 * (was.abs() * 2.0 ** -8 + 6 * 2.0 ** -10)).all(), "sequence %d" % s
 
 
+# ------------------------------------------------------------------ bounds of the batch
+
+def test_positions_past_the_bound(bi):
+    """Tokens at positions from max_kv on: zeros for q, not appended, gathered as zeros; the others as with a larger bound."""
+    Hq, Hkv, D, P, bound = 2, 1, 64, 16, 37
+    seqs = [(5, 40), (3, 20), (2, 31), (4, 60), (1, 37), (1, 38)]
+    for rot, layout in ((64, "HALF"), (16, "HALF"), (32, "INTERLEAVED")):
+        b = step.Batch(bi, seqs, Hkv, D, P, max_kv=bound)
+        rng = np.random.default_rng(0)
+        qkv = step.bits(rng, (b.T, Hq + 2 * Hkv, D))
+        pos = np.concatenate([np.arange(n - q, n) for q, n in seqs])
+        seq = np.repeat(np.arange(len(seqs)), [q for q, _ in seqs])
+        rope = np.stack((np.ones((60, rot // 2)), np.zeros((60, rot // 2))), -1).astype(np.float32)
+        x, want = ref.f32(qkv), b.pool.copy()
+        for t in range(b.T):
+            if pos[t] < bound:
+                ref.write_position(want[b.pages[seq[t], pos[t] // P], 0, 0], P, D, pos[t] % P, x[t, Hq], x[t, Hq + 1])
+        b.to_device()
+        q_out = torch.full((b.T, Hq, D), 7, dtype=torch.int16, device=DEV)
+        d = step.dev(qkv)
+        bi.bi_rope_append_kv4(d[:, :2], d[:, 2:3], d[:, 3:], step.dev(rope), rot, getattr(bi, "BI_ROPE_" + layout), q_out,
+                              b.cache, b.batch)
+        step.same(step.host(b.d_pool), want, "cache")
+        q_want = np.where((pos < bound)[:, None, None], qkv[:, :Hq], np.uint16(0))
+        step.same(step.host(q_out), q_want, "q")
+        k = torch.full((b.T, Hkv, D), 7, dtype=torch.int16, device=DEV)
+        v = k.clone()
+        bi.bi_kv4_gather(b.cache, b.batch, k, v)
+        past = torch.from_numpy(pos >= bound).to(DEV)
+        assert not k[past].any() and not v[past].any()
+        b.batch = bi.kv4_batch(*b.d, b.T, b.max_q, 60)
+        k2, v2 = torch.empty_like(k), torch.empty_like(v)
+        bi.bi_kv4_gather(b.cache, b.batch, k2, v2)
+        assert torch.equal(k[~past], k2[~past]) and torch.equal(v[~past], v2[~past])
+
+
+BOUNDS = [
+    # sequences (new, total), copies, Hq, Hkv, D, page, bound
+    ([(5, 40), (3, 20), (2, 31), (4, 60), (1, 37), (1, 38)], 1, 4, 2, 64, 16, 37),
+    ([(5, 40), (3, 20), (2, 31), (4, 60), (1, 37), (1, 38)], 40, 8, 2, 128, 32, 37),
+    ([(20, 75), (20, 64)], 1, 4, 4, 128, 64, 64),
+    ([(6, 4100), (2, 4099), (3, 2050)], 1, 8, 1, 64, 128, 4098),         # joined in the kernel
+    ([(5, 32772), (2, 100)], 1, 2, 1, 64, 128, 32770),                   # and by a launch of its own
+]
+
+
+@pytest.mark.parametrize("seqs,copies,Hq,Hkv,D,P,bound", BOUNDS)
+def test_attention_of_positions_past_the_bound(bi, seqs, copies, Hq, Hkv, D, P, bound):
+    """Tokens at positions from max_kv on have zeros, the others what they have with a larger bound."""
+    b = verify_pass(bi, seqs, Hkv, D, P, copies)
+    gen = torch.Generator(device=DEV).manual_seed(bound)
+    q = torch.randn((b.T, Hq, D), device=DEV, generator=gen).bfloat16()
+    whole = step.attend(bi, b, q, D ** -0.5)
+    most = max(n for n, _ in seqs)
+    b.batch = bi.kv4_batch(*b.d, b.T, most, bound)
+    o = step.attend(bi, b, q, D ** -0.5)
+    pos = np.concatenate([np.arange(n - n_q, n) for n_q, n in b.seqs])
+    past = torch.from_numpy(pos >= bound).to(DEV)
+    assert past.any() and not past.all()
+    assert not o[past].any(), "a token past the bound"
+    assert torch.equal(o[~past], whole[~past]), "a token before the bound"
+
+
 # ------------------------------------------------------------------ values that are zero, or nearly
 
 @pytest.mark.parametrize("D", [64, 128])
