@@ -485,11 +485,17 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         }
     };
     int *status = static_cast<int *>(a.ws);
-    auto wait = [&](int which, int blk) {
+    // Waits for block blk's keys (0) or values (1).  If they do not come within the limit the call's result is lost: the
+    // status says so, the copies in flight on the barriers (next: the next block's keys too) get one more limit to land,
+    // and if these do not either the warp issues no others and goes on, after this block, to the barriers that the other
+    // warps wait at: nothing then keeps a later copy from landing in shared memory that the CTA uses again or has left.
+    bool lost = false;
+    auto wait = [&](int which, int blk, bool next) {
         if (!mbar_wait_bounded(bars + which, blk & 1, status)) {
             *status = DEV_TIMEOUT;
-            volatile int never = 0;                        // the copies may not land after the CTA has gone
-            mbar_wait_bounded(bars + which, blk & 1, &never);
+            volatile int never = 0;
+            lost = !mbar_wait_bounded(bars + which, blk & 1, &never);
+            if (next) mbar_wait_bounded(bars, (blk + 1) & 1, &never);
         }
         __syncwarp();
     };
@@ -525,12 +531,12 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
 #pragma unroll 1
     for (int blk = 0; blk < BLOCKS; ++blk) {
         const int pb = pw + blk * kStep;
-        if (pb >= n_most) break;
+        if (pb >= n_most || __any_sync(0xffffffffu, lost)) break;
         const bool more = blk + 1 < BLOCKS && pb + kStep < n_most;
         // bit i: positions 16 i .. of the block are on a page; full: and every row sees the whole block
         const unsigned there = (pages >> (4 * blk)) & 15u;
         const bool full = there == 15u && pb + kBlock <= n_least;
-        wait(0, blk);
+        wait(0, blk, false);
         const unsigned char *par = mine + 2 * P::kCodes;
 
         // ---- the values' scales and z / s of positions 2 lane and 2 lane + 1; nothing for positions that no row sees
@@ -668,7 +674,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         }
         // keys and parameters are read: the next block's may come
         __syncwarp();
-        if (more) copy_keys(blk + 1);
+        if (more && !lost) copy_keys(blk + 1);
 
 
         // ---- the block's maxima of scores and of value scales' exponents, per row
@@ -783,7 +789,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
         }
 
         // ---- weighted values
-        wait(1, blk);
+        wait(1, blk, more && !lost);
         {
             uint32_t vw[2 * kTiles][W];
 #pragma unroll
@@ -823,7 +829,7 @@ __device__ __forceinline__ void span_task(const SpanArgs &p, const Task &task, i
                 }
         }
         __syncwarp();
-        if (more) copy_values(blk + 1);
+        if (more && !lost) copy_values(blk + 1);
     }
     __syncwarp();                                          // the warp's codes are read; its results take their place
 
