@@ -90,6 +90,12 @@ class bi_logits_rules(ctypes.Structure):
                 ("frequency", _vp), ("bias_ids", _vp), ("bias", _vp), ("n_bias", _ci), ("mask", _vp), ("ld_mask", _i64)]
 
 
+def _holding(s, *tensors):
+    """A structure of addresses that keeps the tensors behind them alive as long as it lives."""
+    s.tensors = tensors
+    return s
+
+
 _cache_p, _batch_p = ctypes.POINTER(bi_kv4_cache), ctypes.POINTER(bi_kv4_batch)
 lib.bi_rmsnorm_quantize.argtypes = [_vp, _i64, _vp, _i64, _vp, ctypes.c_float, _ci, _ci, _vp, _i64, _vp, _vp, _cu, _vp]
 lib.bi_rmsnorm_quantize.restype = _ci
@@ -309,11 +315,11 @@ def bi_kv4_block_bytes(page_size: int, D: int) -> int:
 
 def kv4_cache(pool: torch.Tensor, page_size: int, D: int) -> bi_kv4_cache:
     """A cache over `pool`, uint8 [num_pages, Hkv, bi_kv4_block_bytes(page_size, D)] with any page stride (for
-    instance one layer of a pool of all layers).  The caller keeps the tensor alive."""
+    instance one layer of a pool of all layers).  The cache holds the tensor."""
     n, Hkv, block = pool.shape
     assert pool.dtype == torch.uint8 and block == bi_kv4_block_bytes(page_size, D)
     assert pool.stride(2) == 1 and pool.stride(1) == block
-    return bi_kv4_cache(pool.data_ptr(), pool.stride(0) if n > 1 else Hkv * block, n, page_size, Hkv, D)
+    return _holding(bi_kv4_cache(pool.data_ptr(), pool.stride(0) if n > 1 else Hkv * block, n, page_size, Hkv, D), pool)
 
 
 def new_kv4_pool(num_pages: int, Hkv: int, page_size: int, D: int, device="cuda") -> torch.Tensor:
@@ -324,12 +330,13 @@ def new_kv4_pool(num_pages: int, Hkv: int, page_size: int, D: int, device="cuda"
 def kv4_batch(cu_q: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, T: int, max_q: int,
               max_kv: int) -> bi_kv4_batch:
     """cu_q int32 [B + 1], kv_len int32 [B], pages int32 [B, n]; T, max_q, max_kv: bounds
-    known to the host.  The caller keeps the tensors alive."""
+    known to the host.  The batch holds the tensors."""
     B = kv_len.shape[0]
     assert cu_q.dtype == kv_len.dtype == pages.dtype == torch.int32
     assert cu_q.shape[0] == B + 1 and cu_q.is_contiguous() and kv_len.is_contiguous()
     assert pages.shape[0] == B and pages.is_contiguous()
-    return bi_kv4_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, T, max_q, max_kv)
+    return _holding(bi_kv4_batch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.shape[1], B, T, max_q, max_kv),
+                    cu_q, kv_len, pages)
 
 
 def _heads(t: torch.Tensor, T: int, H: int, D: int) -> int:
@@ -395,7 +402,7 @@ def logits_rules(ids: torch.Tensor | None = None, begin: torch.Tensor | None = N
                  bias_ids: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                  mask: torch.Tensor | None = None) -> bi_logits_rules:
     """ids int32; begin, mid, end int32 [M]; repetition, presence, frequency fp32 [M]; bias_ids int32 [M, n] and bias
-    fp32 [M, n]; mask int32 words [M, >= ceil(V / 32)].  The caller keeps the tensors alive."""
+    fp32 [M, n]; mask int32 words [M, >= ceil(V / 32)].  The rules hold the tensors."""
     for t in (ids, begin, mid, end, bias_ids, mask):
         assert t is None or t.dtype == torch.int32
     for t in (repetition, presence, frequency, bias):
@@ -404,9 +411,10 @@ def logits_rules(ids: torch.Tensor | None = None, begin: torch.Tensor | None = N
         assert t is None or t.is_contiguous()
     assert mask is None or mask.stride(1) == 1 or mask.shape[1] == 1
     n = 0 if bias_ids is None else bias_ids.shape[1]
-    return bi_logits_rules(_ptr(ids), _ptr(begin), _ptr(mid), _ptr(end), _ptr(repetition), _ptr(presence),
-                           _ptr(frequency), _ptr(bias_ids), _ptr(bias), n, _ptr(mask),
-                           0 if mask is None else mask.stride(0) if mask.shape[0] > 1 else mask.shape[1])
+    r = bi_logits_rules(_ptr(ids), _ptr(begin), _ptr(mid), _ptr(end), _ptr(repetition), _ptr(presence),
+                        _ptr(frequency), _ptr(bias_ids), _ptr(bias), n, _ptr(mask),
+                        0 if mask is None else mask.stride(0) if mask.shape[0] > 1 else mask.shape[1])
+    return _holding(r, ids, begin, mid, end, repetition, presence, frequency, bias_ids, bias, mask)
 
 
 def bi_logits_workspace_size(M: int) -> int:
