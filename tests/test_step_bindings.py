@@ -21,18 +21,15 @@ def ints(*shape):
 def test_structures_hold_their_tensors(bi):
     """Cache, batch and rules are addresses: the tensors behind them live as long as they do."""
     def lives(make, *tensors):
-        refs = [weakref.ref(t) for t in tensors]
-        s = make(*tensors)
-        del tensors
-        return refs, s
-    pool = torch.zeros((2, 1, bi.bi_kv4_block_bytes(16, 64)), dtype=torch.uint8)
-    for refs, s in (lives(lambda p: bi.kv4_cache(p, 16, 64), pool),
-                    lives(lambda c, n, p: bi.kv4_batch(c, n, p, 3, 3, 40), ints(3), ints(2), ints(2, 4)),
-                    lives(lambda i, b, m, e, k: bi.logits_rules(ids=i, begin=b, mid=m, end=e, mask=k), ints(9), ints(2), ints(2),
-                          ints(2), ints(2, 32)),
-                    lives(lambda r, p, f, i, b: bi.logits_rules(repetition=r, presence=p, frequency=f, bias_ids=i, bias=b),
-                          torch.ones(2), torch.ones(2), torch.ones(2), ints(2, 5), torch.ones(2, 5))):
-        pool = None
+        return [weakref.ref(t) for t in tensors], make(*tensors)
+    for make in (lambda: lives(lambda p: bi.kv4_cache(p, 16, 64),
+                               torch.zeros((2, 1, bi.bi_kv4_block_bytes(16, 64)), dtype=torch.uint8)),
+                 lambda: lives(lambda c, n, p: bi.kv4_batch(c, n, p, 3, 3, 40), ints(3), ints(2), ints(2, 4)),
+                 lambda: lives(lambda i, b, m, e, k: bi.logits_rules(ids=i, begin=b, mid=m, end=e, mask=k), ints(9), ints(2),
+                               ints(2), ints(2), ints(2, 32)),
+                 lambda: lives(lambda r, p, f, i, b: bi.logits_rules(repetition=r, presence=p, frequency=f, bias_ids=i, bias=b),
+                               torch.ones(2), torch.ones(2), torch.ones(2), ints(2, 5), torch.ones(2, 5))):
+        refs, s = make()
         gc.collect()
         assert all(r() is not None for r in refs)
         del s
