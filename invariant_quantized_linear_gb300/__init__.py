@@ -348,6 +348,12 @@ def _heads(t: torch.Tensor, T: int, H: int, D: int) -> int:
     return ld if n > 1 else H * D
 
 
+def _vector(t: torch.Tensor, n: int, size: int) -> int:
+    """The address of n elements of `size` bytes side by side."""
+    assert t.shape == (n,) and (t.stride(0) == 1 or n == 1) and t.element_size() == size
+    return t.data_ptr()
+
+
 def bi_rope_table(inv_freq: torch.Tensor, rope: torch.Tensor, amp: float = 1.0, stream=None) -> None:
     """inv_freq: fp64 [n]; rope: fp32 [positions, n, 2] out."""
     assert inv_freq.dtype == torch.float64 and rope.dtype == torch.float32 and rope.is_contiguous()
@@ -360,13 +366,15 @@ def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: 
                        q_out: torch.Tensor, cache: bi_kv4_cache, batch: bi_kv4_batch, q_norm: torch.Tensor | None = None,
                        k_norm: torch.Tensor | None = None, eps: float = 0.0, flags: int = 0, stream=None) -> None:
     """q: bf16 [T, Hq, D], k, v: bf16 [T, Hkv, D] (row strides stride(0); parts of one packed tensor will do);
-    rope: fp32 [positions, rot / 2, 2]; q_norm, k_norm: bf16 [D] or None; q_out: bf16 [T, Hq, D]."""
+    rope: fp32 [positions, rot / 2, 2] (any width with rot 0); q_norm, k_norm: bf16 [D] or None; q_out: bf16 [T, Hq, D]."""
     T, D, Hq, Hkv = batch.T, cache.D, q.shape[1], cache.Hkv
     ldq, ldk, ldv = _heads(q, T, Hq, D), _heads(k, T, Hkv, D), _heads(v, T, Hkv, D)
-    assert _heads(q_out, T, Hq, D) == Hq * D and rope.is_contiguous()
-    _check(lib.bi_rope_append_kv4(q.data_ptr(), ldq, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(q_norm),
-                                  _ptr(k_norm), eps, rope.data_ptr(), rope.shape[0], rot, layout, q_out.data_ptr(),
-                                  cache, batch, flags, _stream(stream)), "bi_rope_append_kv4")
+    assert _heads(q_out, T, Hq, D) == Hq * D and rope.is_contiguous() and rope.dtype == torch.float32
+    assert rot == 0 or rope.shape[1:] == (rot // 2, 2)
+    qn, kn = (None if t is None else _vector(t, D, 2) for t in (q_norm, k_norm))
+    _check(lib.bi_rope_append_kv4(q.data_ptr(), ldq, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, qn, kn, eps,
+                                  rope.data_ptr(), rope.shape[0], rot, layout, q_out.data_ptr(), cache, batch, flags,
+                                  _stream(stream)), "bi_rope_append_kv4")
 
 
 def bi_kv4_gather(cache: bi_kv4_cache, batch: bi_kv4_batch, k_out: torch.Tensor, v_out: torch.Tensor,

@@ -35,3 +35,26 @@ def test_structures_hold_their_tensors(bi):
         del s
         gc.collect()
         assert all(r() is None for r in refs)
+
+
+def test_append_checks_the_table_and_the_norms(bi):
+    """A table narrower than rot / 2 or of another type, and norms of another length, are not read past their end."""
+    T, Hq, Hkv, D = 6, 4, 2, 64
+    pool = torch.zeros((2, Hkv, bi.bi_kv4_block_bytes(16, D)), dtype=torch.uint8)
+    cache, batch = bi.kv4_cache(pool, 16, D), bi.kv4_batch(ints(3), ints(2), ints(2, 4), T, 3, 40)
+    half = dict(dtype=torch.bfloat16)
+    q, k, v, out = (torch.zeros((T, h, D), **half) for h in (Hq, Hkv, Hkv, Hq))
+    norm = torch.ones(D, **half)
+
+    def call(rope=torch.zeros((40, 16, 2)), rot=32, q_norm=norm, k_norm=norm, q_out=out):
+        bi.bi_rope_append_kv4(q, k, v, rope, rot, bi.BI_ROPE_HALF, q_out, cache, batch, q_norm=q_norm, k_norm=k_norm, stream=0)
+    for bad in (dict(rope=torch.zeros((40, 15, 2))), dict(rope=torch.zeros((40, 32, 2))), dict(rope=torch.zeros((40, 16, 1))),
+                dict(rope=torch.zeros((40, 32))), dict(rope=torch.zeros((40, 16, 2), dtype=torch.float64)),
+                dict(rope=torch.zeros((40, 2, 16)).transpose(1, 2)), dict(rope=torch.zeros((40, 16, 2)).bfloat16()),
+                dict(q_norm=norm[:32]), dict(k_norm=norm[:63]), dict(q_norm=norm.float()), dict(k_norm=torch.ones(2 * D, **half)[::2]),
+                dict(k_norm=torch.ones((1, D), **half)), dict(q_out=out[:5])):
+        with pytest.raises(AssertionError):
+            call(**bad)
+    # the shapes that are right reach the library, which finds no device (or unaligned memory) here
+    with pytest.raises(bi.BiError):
+        call(rot=36, rope=torch.zeros((40, 18, 2)))            # half layout: a multiple of 8
