@@ -294,19 +294,33 @@ def bi_attention_verify(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, T0: i
                                    nbytes, _stream(stream)), "bi_attention_verify")
 
 
+def _rows(t: torch.Tensor, M: int, K: int, size: int) -> int:
+    """The row stride of elements of `size` bytes [>= M, >= K]; of a single row, whose stride may be anything, K."""
+    assert t.dim() == 2
+    m, k = t.shape
+    ld, s = t.stride()
+    assert m >= M and k >= K and (s == 1 or K == 1) and t.element_size() == size
+    return ld if M > 1 else K
+
+
+def _vector(t: torch.Tensor, n: int, size: int) -> int:
+    """The address of at least n elements of `size` bytes side by side."""
+    assert t.is_contiguous() and t.numel() >= n and t.element_size() == size
+    return t.data_ptr()
+
+
 def bi_rmsnorm_quantize(h: torch.Tensor, y: torch.Tensor | None, w: torch.Tensor, eps: float,
                         h_out: torch.Tensor | None, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0,
                         stream=None) -> None:
     """h, y: bf16 [M, >= K] (row strides h.stride(0), y.stride(0)); w: bf16 [K]; h_out: bf16 [M, >= K], given with y
     (it may be h); q: int8 [M, K]; s_a: fp32 [M]."""
     M, K = q.shape
-    ldh = ldy = ldo = K                                    # a single row's stride may be anything
-    if M > 1:
-        ldh = h.stride(0)
-        if y is not None:
-            ldy, ldo = y.stride(0), h_out.stride(0)
-    _check(lib.bi_rmsnorm_quantize(h.data_ptr(), ldh, _ptr(y), ldy, w.data_ptr(), eps, M, K, _ptr(h_out), ldo,
-                                   q.data_ptr(), s_a.data_ptr(), flags, _stream(stream)), "bi_rmsnorm_quantize")
+    assert q.element_size() == 1 and q.is_contiguous()
+    ldh = _rows(h, M, K, 2)
+    ldy = K if y is None else _rows(y, M, K, 2)
+    ldo = K if h_out is None else _rows(h_out, M, K, 2)
+    _check(lib.bi_rmsnorm_quantize(h.data_ptr(), ldh, _ptr(y), ldy, _vector(w, K, 2), eps, M, K, _ptr(h_out), ldo,
+                                   q.data_ptr(), _vector(s_a, M, 4), flags, _stream(stream)), "bi_rmsnorm_quantize")
 
 
 def bi_kv4_block_bytes(page_size: int, D: int) -> int:
@@ -346,12 +360,6 @@ def _heads(t: torch.Tensor, T: int, H: int, D: int) -> int:
     ld, sh, sd = t.stride()
     assert n >= T and h == H and d == D and sd == 1 and (sh == D or h == 1) and t.element_size() == 2
     return ld if n > 1 else H * D
-
-
-def _vector(t: torch.Tensor, n: int, size: int) -> int:
-    """The address of n elements of `size` bytes side by side."""
-    assert t.shape == (n,) and (t.stride(0) == 1 or n == 1) and t.element_size() == size
-    return t.data_ptr()
 
 
 def bi_rope_table(inv_freq: torch.Tensor, rope: torch.Tensor, amp: float = 1.0, stream=None) -> None:

@@ -52,9 +52,32 @@ def test_append_checks_the_table_and_the_norms(bi):
                 dict(rope=torch.zeros((40, 32))), dict(rope=torch.zeros((40, 16, 2), dtype=torch.float64)),
                 dict(rope=torch.zeros((40, 2, 16)).transpose(1, 2)), dict(rope=torch.zeros((40, 16, 2)).bfloat16()),
                 dict(q_norm=norm[:32]), dict(k_norm=norm[:63]), dict(q_norm=norm.float()), dict(k_norm=torch.ones(2 * D, **half)[::2]),
-                dict(k_norm=torch.ones((1, D), **half)), dict(q_out=out[:5])):
+                dict(q_out=out[:5])):
         with pytest.raises(AssertionError):
             call(**bad)
     # the shapes that are right reach the library, which finds no device (or unaligned memory) here
     with pytest.raises(bi.BiError):
         call(rot=36, rope=torch.zeros((40, 18, 2)))            # half layout: a multiple of 8
+
+
+def test_norm_checks_shapes_and_types(bi):
+    M, K = 3, 64
+    half = dict(dtype=torch.bfloat16)
+    good = dict(h=torch.zeros((M, K), **half), y=torch.zeros((M, K), **half), w=torch.zeros(K, **half), eps=1e-6,
+                h_out=torch.zeros((M, K), **half), q=torch.zeros((M, K), dtype=torch.int8), s_a=torch.zeros(M))
+
+    def call(**o):
+        a = {**good, **o}
+        bi.bi_rmsnorm_quantize(a["h"], a["y"], a["w"], a["eps"], a["h_out"], a["q"], a["s_a"], stream=0)
+    wide = torch.zeros((M, 2 * K), **half)
+    for bad in (dict(h=wide[:2]), dict(h=wide[:, :K - 8]), dict(h=wide[:, ::2]), dict(h=torch.zeros((M, K))), dict(h=wide[0]),
+                dict(y=wide[:2]), dict(y=wide[:, :K - 1]), dict(y=torch.zeros((M, K))), dict(w=wide[0, :K - 1]),
+                dict(w=torch.zeros(K)), dict(w=wide[0, ::2]), dict(h_out=wide[:2]), dict(h_out=wide[:, :8]),
+                dict(h_out=torch.zeros((M, K))), dict(q=torch.zeros((M, 2 * K), dtype=torch.int8)[:, :K]),
+                dict(q=torch.zeros((M, K), dtype=torch.int16)), dict(s_a=torch.zeros(M - 1)),
+                dict(s_a=torch.zeros(M, dtype=torch.float64)), dict(s_a=torch.zeros(2 * M)[::2])):
+        with pytest.raises(AssertionError):
+            call(**bad)
+    for refused in (dict(y=None), dict(h_out=None), dict(eps=-1.0)):
+        with pytest.raises(bi.BiError):
+            call(**refused)
