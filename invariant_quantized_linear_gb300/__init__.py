@@ -299,7 +299,7 @@ def _rows(t: torch.Tensor, M: int, K: int, size: int) -> int:
     assert t.dim() == 2
     m, k = t.shape
     ld, s = t.stride()
-    assert m >= M and k >= K and (s == 1 or K == 1) and t.element_size() == size
+    assert m >= M and k >= K and (s == 1 or k == 1) and t.element_size() == size
     return ld if M > 1 else K
 
 
@@ -426,10 +426,15 @@ def logits_rules(ids: torch.Tensor | None = None, begin: torch.Tensor | None = N
     for t in (ids, begin, mid, end, repetition, presence, frequency, bias_ids, bias):
         assert t is None or t.is_contiguous()
     assert mask is None or mask.stride(1) == 1 or mask.shape[1] == 1
+    assert bias_ids is None or bias is None or bias.shape == bias_ids.shape
     n = 0 if bias_ids is None else bias_ids.shape[1]
     r = bi_logits_rules(_ptr(ids), _ptr(begin), _ptr(mid), _ptr(end), _ptr(repetition), _ptr(presence),
                         _ptr(frequency), _ptr(bias_ids), _ptr(bias), n, _ptr(mask),
                         0 if mask is None else mask.stride(0) if mask.shape[0] > 1 else mask.shape[1])
+    # rows that there are rules for, and elements of a row that the mask reaches
+    r.rows = min((t.shape[0] for t in (begin, mid, end, repetition, presence, frequency, bias_ids, bias, mask) if t is not None),
+                 default=None)
+    r.reach = None if mask is None else 32 * mask.shape[1]
     return _holding(r, ids, begin, mid, end, repetition, presence, frequency, bias_ids, bias, mask)
 
 
@@ -444,18 +449,20 @@ def new_logits_workspace(M: int, device="cuda") -> torch.Tensor:
 
 def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.Tensor | None,
                       argmax: torch.Tensor | None, ws: torch.Tensor, flags: int = 0, stream=None) -> None:
-    """logits: bf16 [M, V] (row stride logits.stride(0)); out: fp32 [M, V] or None; argmax: int32 [M] or None."""
+    """logits: bf16 [M, V] (row stride logits.stride(0)); rules: for at least M rows; out: fp32 [M, V] or None; argmax:
+    int32 [M] or None."""
     M, V = logits.shape
-    ldl, sl = logits.stride()
-    assert (sl == 1 or V == 1) and logits.element_size() == 2
-    ldo = V
+    ldl, ldo = _rows(logits, M, V, 2), V
     if out is not None:
-        ldo, so = out.stride()
-        assert (so == 1 or V == 1) and out.dtype == torch.float32
-    if M == 1:                                             # a single row's stride may be anything
-        ldl = ldo = V
-    _check(lib.bi_logits_process(logits.data_ptr(), ldl, M, V, rules, _ptr(out), ldo, _ptr(argmax), ws.data_ptr(),
-                                 ws.nbytes, flags, _stream(stream)), "bi_logits_process")
+        assert out.dtype == torch.float32
+        ldo = _rows(out, M, V, 4)
+    assert argmax is None or argmax.dtype == torch.int32
+    # a structure that logits_rules did not make has no rows and no reach to look at
+    rows, reach = getattr(rules, "rows", None), getattr(rules, "reach", None)
+    assert (rows is None or rows >= M) and (reach is None or reach >= V)
+    _check(lib.bi_logits_process(logits.data_ptr(), ldl, M, V, rules, _ptr(out), ldo,
+                                 None if argmax is None else _vector(argmax, M, 4), ws.data_ptr(), ws.nbytes, flags,
+                                 _stream(stream)), "bi_logits_process")
 
 
 def bi_probe_read(buf: torch.Tensor, out: torch.Tensor, stream=None) -> None:

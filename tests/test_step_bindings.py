@@ -81,3 +81,29 @@ def test_norm_checks_shapes_and_types(bi):
     for refused in (dict(y=None), dict(h_out=None), dict(eps=-1.0)):
         with pytest.raises(bi.BiError):
             call(**refused)
+
+
+def test_logits_checks_rows_and_results(bi):
+    M, V = 3, 100
+    x, out, ws = torch.zeros((M, V), dtype=torch.bfloat16), torch.zeros((M, V)), torch.zeros(1, dtype=torch.uint8)
+
+    def call(rules, out=out, argmax=ints(M)):
+        bi.bi_logits_process(x, rules, out, argmax, ws, stream=0)
+    none = bi.logits_rules()
+    ids = dict(ids=ints(9), begin=ints(M), mid=ints(M), end=ints(M))
+    for bad in (bi.logits_rules(**{**ids, "begin": ints(M - 1)}), bi.logits_rules(**{**ids, "end": ints(1)}),
+                bi.logits_rules(**ids, repetition=torch.ones(M - 1)), bi.logits_rules(presence=torch.ones(1)),
+                bi.logits_rules(frequency=torch.ones(2)), bi.logits_rules(bias_ids=ints(2, 4), bias=torch.ones(2, 4)),
+                bi.logits_rules(mask=ints(M - 1, 4)), bi.logits_rules(mask=ints(M, 3)), bi.logits_rules(mask=ints(M, 9)[:, :3])):
+        with pytest.raises(AssertionError):
+            call(bad)
+    with pytest.raises(AssertionError):
+        bi.logits_rules(bias_ids=ints(M, 4), bias=torch.ones(M, 3))
+    for o in (out[:2], out[:, :99], torch.zeros((M, V), dtype=torch.bfloat16), out.double(), out.t().contiguous().t()):
+        with pytest.raises(AssertionError):
+            call(none, out=o)
+    for a in (ints(M - 1), ints(2 * M)[::2], ints(M).long(), torch.zeros(M)):
+        with pytest.raises(AssertionError):
+            call(none, argmax=a)
+    with pytest.raises(bi.BiError):                             # more rows than the logits will do; the workspace will not
+        call(bi.logits_rules(**{k: v if k == "ids" else ints(M + 2) for k, v in ids.items()}, mask=ints(M + 1, 4)))
