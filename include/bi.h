@@ -493,7 +493,7 @@ BI_API bi_status bi_kv4_gather(const bi_kv4_cache *cache, const bi_kv4_batch *ba
  *       16-byte aligned, zero-filled before its first use; every call that
  *       completes leaves it ready for the next.  Its layout depends on no
  *       argument, so one workspace of the largest size serves calls of any
- *       shape on one stream.  A copy that does not arrive within the wait limit
+ *       shape on one stream.  It overlaps neither q nor o.  A copy that does not arrive within the wait limit
  *       is reported by bi_workspace_status as BI_ERR_TIMEOUT.
  * Scores, softmax sums and outputs are fp32; the products run on the tensor
  * cores with the codes exact and q exact but for elements 2^-24 below its
@@ -540,6 +540,7 @@ typedef struct {
  *   ws      workspace of at least bi_logits_workspace_size(M) bytes, 16-byte
  *           aligned, zero-filled before its first use; every call that completes
  *           leaves it zero-filled
+ * out, argmax and ws overlap neither one another nor anything that is read.
  * 1 <= M <= 65535, 1 <= V <= 2^24.  Logits rows may start anywhere on 2 bytes,
  * out rows on 4; rows on 16 bytes are faster.
  */

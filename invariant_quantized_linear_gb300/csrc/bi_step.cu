@@ -84,6 +84,13 @@ size_t rows_bytes(int64_t rows, int64_t ld, int64_t width, size_t esz)
     return static_cast<size_t>((rows - 1) * ld + width) * esz;
 }
 
+// Bytes from p on; none where p is null or n is 0.
+struct Span {
+    const void *p;
+    size_t n;
+    bool meets(const Span &o) const { return p && o.p && n && o.n && overlaps(p, n, o.p, o.n); }
+};
+
 bool finite_at_least(float x, float least) { return x >= least && x <= 3.402823466e38f; }
 
 }  // namespace
@@ -239,6 +246,8 @@ bi_status bi_attention_kv4(const uint16_t *q, int64_t ldq, int Hq, const bi_kv4_
     const size_t need = bi_attention_kv4_workspace_size(Hq, cache, batch);
     if (need == 0) return BI_ERR_INVALID_ARG;
     if (!ws || ws_bytes < need || !aligned16(ws)) return BI_ERR_WORKSPACE;
+    if (overlaps(ws, need, q, rows_bytes(batch->T, ldq, wq, 2)) || overlaps(ws, need, o, static_cast<size_t>(batch->T) * wq * 2))
+        return BI_ERR_INVALID_ARG;
     bi::AttnKv4Args a;
     st = device_info(&a.sms);
     if (st != BI_OK) return st;
@@ -268,8 +277,26 @@ bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, int V, c
         !aligned4(r.mid) || !aligned4(r.end) || !aligned4(r.repetition) || !aligned4(r.presence) ||
         !aligned4(r.frequency) || !aligned4(r.bias_ids) || !aligned4(r.bias) || !aligned4(r.mask))
         return BI_ERR_ALIGNMENT;
-    if (out && overlaps(out, rows_bytes(M, ldo, V, 4), logits, rows_bytes(M, ldl, V, 2))) return BI_ERR_INVALID_ARG;
     if (!ws || ws_bytes < bi::logits_workspace(M) || !aligned16(ws)) return BI_ERR_WORKSPACE;
+    // what is written overlaps nothing; the extent of ids is the device's to know
+    const size_t per_row = 4 * static_cast<size_t>(M), per_bias = per_row * static_cast<size_t>(r.n_bias);
+    const Span written[] = {{out, out ? rows_bytes(M, ldo, V, 4) : 0}, {argmax, per_row}, {ws, bi::logits_workspace(M)}};
+    const Span read[] = {{logits, rows_bytes(M, ldl, V, 2)},
+                         {r.ids ? r.begin : nullptr, per_row},
+                         {r.ids ? r.mid : nullptr, per_row},
+                         {r.ids ? r.end : nullptr, per_row},
+                         {r.repetition, per_row},
+                         {r.presence, per_row},
+                         {r.frequency, per_row},
+                         {r.bias_ids, per_bias},
+                         {r.n_bias > 0 ? r.bias : nullptr, per_bias},
+                         {r.mask, r.mask ? rows_bytes(M, r.ld_mask, (V + 31) / 32, 4) : 0}};
+    for (const Span &w : written) {
+        for (const Span &x : read)
+            if (w.meets(x)) return BI_ERR_INVALID_ARG;
+        for (const Span &x : written)
+            if (&w < &x && w.meets(x)) return BI_ERR_INVALID_ARG;
+    }
     int sms = 0;
     const bi_status st = device_info(&sms);
     if (st != BI_OK) return st;
