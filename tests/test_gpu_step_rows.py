@@ -241,3 +241,19 @@ def test_blocks_of_small_values_far_below_the_maximum(bi, D, sigma):
     want = s.attend(q, N)
     bad = differ(s.attend(q, 100), want)
     assert bad == 0, "%d elements of %d differ" % (bad, want.numel())
+
+
+# ------------------------------------------------------------------ append, several steps a warp
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,P,rot,inter,norm", [
+    ([(1600, 1600)], 9, 5, 64, 16, 16, False, True),          # a warp a token: q, k and v heads one after the other
+    ([(1600, 1700)], 9, 5, 64, 32, 64, True, False),
+    ([(1700, 1700)], 7, 3, 128, 64, 32, False, True),
+    ([(1600, 1600)], 7, 3, 128, 16, 64, True, True),
+    ([(1600, 1650)], 13, 1, 128, 128, 64, False, False),      # more q heads than are in flight
+    ([(700, 700), (300, 900)], 12, 4, 128, 64, 48, True, True),   # three warps a token: runs that end inside a kind
+    ([(1000, 1000)], 12, 4, 128, 64, 64, False, True),
+])
+def test_append_of_prompts_in_every_layout(bi, seqs, Hq, Hkv, D, P, rot, inter, norm):
+    """Heads rotated in part, or in pairs, in calls whose warps have several steps."""
+    step.test_append_and_gather(bi, seqs, Hq, Hkv, D, P, rot, inter, norm)
