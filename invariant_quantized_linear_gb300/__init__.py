@@ -366,7 +366,7 @@ def bi_rope_table(inv_freq: torch.Tensor, rope: torch.Tensor, amp: float = 1.0, 
     """inv_freq: fp64 [n]; rope: fp32 [positions, n, 2] out."""
     assert inv_freq.dtype == torch.float64 and rope.dtype == torch.float32 and rope.is_contiguous()
     assert rope.shape[1:] == (inv_freq.shape[0], 2)
-    _check(lib.bi_rope_table(_ptr(inv_freq), inv_freq.shape[0], amp, rope.shape[0], _ptr(rope), _stream(stream)),
+    _check(lib.bi_rope_table(_vector(inv_freq, inv_freq.shape[0], 8), inv_freq.shape[0], amp, rope.shape[0], _ptr(rope), _stream(stream)),
            "bi_rope_table")
 
 

@@ -107,3 +107,15 @@ def test_logits_checks_rows_and_results(bi):
             call(none, argmax=a)
     with pytest.raises(bi.BiError):                             # more rows than the logits will do; the workspace will not
         call(bi.logits_rules(**{k: v if k == "ids" else ints(M + 2) for k, v in ids.items()}, mask=ints(M + 1, 4)))
+
+
+def test_rope_table_checks_its_frequencies(bi):
+    """Frequencies that are not side by side are not read as if they were."""
+    f, rope = torch.ones(16, dtype=torch.float64), torch.zeros((5, 8, 2))
+    for bad in (dict(inv_freq=f[::2]), dict(inv_freq=f[:8].float()), dict(inv_freq=f[:7]), dict(rope=torch.zeros((5, 9, 2))),
+                dict(rope=rope.double()), dict(rope=torch.zeros((5, 2, 8)).transpose(1, 2))):
+        a = {**dict(inv_freq=f[:8], rope=rope), **bad}
+        with pytest.raises(AssertionError):
+            bi.bi_rope_table(a["inv_freq"], a["rope"], stream=0)
+    with pytest.raises(bi.BiError):
+        bi.bi_rope_table(f[:8], rope, float("nan"), stream=0)
