@@ -1,6 +1,7 @@
 """Batch-invariant verify pass for GB300 (sm_103a): Python binding of the W8A8
-linear and LM head, the verify-pass executor, the block-scaled variant and the
-split-KV verify attention.
+linear and LM head, the verify-pass executor, the block-scaled variant, the
+split-KV verify attention and the decoder-step operators (norm, rotation with the
+4-bit paged cache, attention over it, logit rules).
 
 A thin ctypes layer over ``libbi.so`` (C ABI declared in ``include/bi.h``).
 Each function has the name of the C entry point it calls and only marshals
@@ -88,6 +89,8 @@ class bi_logits_rules(ctypes.Structure):
     """Rules applied to logits (struct bi_logits_rules of include/bi.h)."""
     _fields_ = [("ids", _vp), ("begin", _vp), ("mid", _vp), ("end", _vp), ("repetition", _vp), ("presence", _vp),
                 ("frequency", _vp), ("bias_ids", _vp), ("bias", _vp), ("n_bias", _ci), ("mask", _vp), ("ld_mask", _i64)]
+    # rows that there are rules for, and elements of a row that the mask reaches, as far as logits_rules knows
+    rows = reach = 1 << 62
 
 
 def _holding(s, *tensors):
@@ -366,8 +369,8 @@ def bi_rope_table(inv_freq: torch.Tensor, rope: torch.Tensor, amp: float = 1.0, 
     """inv_freq: fp64 [n]; rope: fp32 [positions, n, 2] out."""
     assert inv_freq.dtype == torch.float64 and rope.dtype == torch.float32 and rope.is_contiguous()
     assert rope.shape[1:] == (inv_freq.shape[0], 2)
-    _check(lib.bi_rope_table(_vector(inv_freq, inv_freq.shape[0], 8), inv_freq.shape[0], amp, rope.shape[0], _ptr(rope), _stream(stream)),
-           "bi_rope_table")
+    n = inv_freq.shape[0]
+    _check(lib.bi_rope_table(_vector(inv_freq, n, 8), n, amp, rope.shape[0], _ptr(rope), _stream(stream)), "bi_rope_table")
 
 
 def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor, rot: int, layout: int,
@@ -377,11 +380,13 @@ def bi_rope_append_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: 
     rope: fp32 [positions, rot / 2, 2] (any width with rot 0); q_norm, k_norm: bf16 [D] or None; q_out: bf16 [T, Hq, D]."""
     T, D, Hq, Hkv = batch.T, cache.D, q.shape[1], cache.Hkv
     ldq, ldk, ldv = _heads(q, T, Hq, D), _heads(k, T, Hkv, D), _heads(v, T, Hkv, D)
+    table = rope.shape
     assert _heads(q_out, T, Hq, D) == Hq * D and rope.is_contiguous() and rope.dtype == torch.float32
-    assert rot == 0 or rope.shape[1:] == (rot // 2, 2)
-    qn, kn = (None if t is None else _vector(t, D, 2) for t in (q_norm, k_norm))
+    assert rot == 0 or table == (table[0], rot // 2, 2)
+    qn = None if q_norm is None else _vector(q_norm, D, 2)
+    kn = None if k_norm is None else _vector(k_norm, D, 2)
     _check(lib.bi_rope_append_kv4(q.data_ptr(), ldq, Hq, k.data_ptr(), ldk, v.data_ptr(), ldv, qn, kn, eps,
-                                  rope.data_ptr(), rope.shape[0], rot, layout, q_out.data_ptr(), cache, batch, flags,
+                                  rope.data_ptr(), table[0], rot, layout, q_out.data_ptr(), cache, batch, flags,
                                   _stream(stream)), "bi_rope_append_kv4")
 
 
@@ -431,10 +436,10 @@ def logits_rules(ids: torch.Tensor | None = None, begin: torch.Tensor | None = N
     r = bi_logits_rules(_ptr(ids), _ptr(begin), _ptr(mid), _ptr(end), _ptr(repetition), _ptr(presence),
                         _ptr(frequency), _ptr(bias_ids), _ptr(bias), n, _ptr(mask),
                         0 if mask is None else mask.stride(0) if mask.shape[0] > 1 else mask.shape[1])
-    # rows that there are rules for, and elements of a row that the mask reaches
     r.rows = min((t.shape[0] for t in (begin, mid, end, repetition, presence, frequency, bias_ids, bias, mask) if t is not None),
-                 default=None)
-    r.reach = None if mask is None else 32 * mask.shape[1]
+                 default=r.rows)
+    if mask is not None:
+        r.reach = 32 * mask.shape[1]
     return _holding(r, ids, begin, mid, end, repetition, presence, frequency, bias_ids, bias, mask)
 
 
@@ -457,9 +462,7 @@ def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.T
         assert out.dtype == torch.float32
         ldo = _rows(out, M, V, 4)
     assert argmax is None or argmax.dtype == torch.int32
-    # a structure that logits_rules did not make has no rows and no reach to look at
-    rows, reach = getattr(rules, "rows", None), getattr(rules, "reach", None)
-    assert (rows is None or rows >= M) and (reach is None or reach >= V)
+    assert rules.rows >= M and rules.reach >= V
     _check(lib.bi_logits_process(logits.data_ptr(), ldl, M, V, rules, _ptr(out), ldo,
                                  None if argmax is None else _vector(argmax, M, 4), ws.data_ptr(), ws.nbytes, flags,
                                  _stream(stream)), "bi_logits_process")
