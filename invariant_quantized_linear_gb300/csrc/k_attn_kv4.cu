@@ -1187,13 +1187,15 @@ cudaError_t launch_attention_kv4(const AttnKv4Args &a, int D, bool pdl, cudaStre
     p.spans = spans_of(a.c.max_kv);
     p.pdl = pdl ? 1 : 0;
     // 16 rows a CTA where there are as many, 8 while their clusters leave an SM at most two CTAs (b 1, 8 tokens, 2000
-    // positions: 8.7 us, with 16 rows 9.8; b 1, 4 tokens, 4104, above that: 12.3, with 16 11.7).  A span a cluster while the
-    // spans alone leave SMs idle: it takes 5.5 us and 0.13 us more for each span of 8 rows (152 SMs), a span a CTA 18.8 us
-    // up to a span a SM; they meet at 105 spans.
+    // positions: 8.9 us, with 16 rows 10.2; b 1, 4 tokens, 4104, above that: 12.6, with 16 12.1).  A span a cluster while
+    // all the clusters fit at once, by the CTAs a SM that the registers leave them, a span a CTA after that.  Clusters and
+    // CTAs on 152 SMs, spans of 2048: 8 rows of head size 128, 64, 72, 80 and 96 spans: 12.3, 12.7, 15.5, 18.4 and 15.5 us;
+    // head size 64, 72 and 80: 9.4, 13.3 and 12.3; with 16 rows, 72 and 80: 11.5, 15.3 and 14.2; 16 rows of head size 128,
+    // 40, 48 and 56 spans: 13.6, 14.2, 20.7 and 19.4.
     const int64_t heads = static_cast<int64_t>(a.c.B) * a.c.Hkv;
     const bool two = rows > 8 && kCluster * heads * ((rows + 7) / 8) * p.spans > 2 * a.sms;
     p.row_blocks = two ? (rows + 15) / 16 : (rows + 7) / 8;
-    const bool split = 3 * heads * p.row_blocks * p.spans <= 2 * a.sms;
+    const bool split = (D == 128 && two ? 3 : 2) * heads * p.row_blocks * p.spans <= a.sms;
     p.count = heads * p.row_blocks * (split ? kCluster : 1) <= kCounters && p.spans <= kJoinSpans;
     cudaError_t e;
     if (D == 64)
