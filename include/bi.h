@@ -493,11 +493,17 @@ BI_API bi_status bi_kv4_gather(const bi_kv4_cache *cache, const bi_kv4_batch *ba
  *       16-byte aligned, zero-filled before its first use; every call that
  *       completes leaves it ready for the next.  Its layout depends on no
  *       argument, so one workspace of the largest size serves calls of any
- *       shape on one stream.  It overlaps neither q nor o.  A copy that does not arrive within the wait limit
+ *       shape on one stream.  It overlaps neither q nor o.  Its size is the
+ *       counters' (about 2 MB) and, where max_kv is above 2048, 4 (D + 4) bytes for
+ *       each of T Hq ceil(max_kv / 2048) results: 0.55 GB for 8192 tokens of 32
+ *       heads of 128 at 8192 positions, 8.9 GB at 131072; long prompts go in
+ *       parts of fewer tokens.  A copy that does not arrive within the wait limit
  *       is reported by bi_workspace_status as BI_ERR_TIMEOUT.
  * Scores, softmax sums and outputs are fp32; the products run on the tensor
  * cores with the codes exact and q exact but for elements 2^-24 below its
- * head's largest, and the weights in f16 with 11 bits.  A query's result
+ * head's largest (scale times that one below 2^115), and the weights in f16 with
+ * 11 bits, always: outputs differ from fp32 weights' by up to 2^-10 of the mean
+ * |v| under them, beside the bf16 of the result (2^-8).  A query's result
  * depends on its own positions only.
  */
 BI_API size_t bi_attention_kv4_workspace_size(int Hq, const bi_kv4_cache *cache, const bi_kv4_batch *batch);

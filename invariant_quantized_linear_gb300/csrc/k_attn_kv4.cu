@@ -51,17 +51,25 @@
 //   a span a cluster of 8 CTAs, a block a warp, the fold over the cluster's
 //     shared memory: for calls that leave SMs idle, where a chunk's eight
 //     blocks one after the other would be most of the time.
+// Both round in the same order (in a cluster a block's exponent travels with its
+// result), and so do 8 and 16 rows a CTA.  A position that a row does not see has
+// weight zero and finite operands: value groups that are not finite are set aside
+// before the products (set_aside; one reduction a block, 0.5 to 2 % of a call).
 // The CTA that finishes a row block's last span joins the spans (a counter in
 // the workspace); a second launch does where a row has many spans or the
 // counters do not suffice.
 //
 // Bound: HBM by its bytes (0.5625 B an element) up to 16 query rows a kv head;
 // within a span it reads 6.2 TB/s, instructions, shared memory and HBM all near
-// their rates; a CTA's start and end (3.1 us) and the last wave are the rest.
-// Measured (32 q and 8 kv heads of 128, caches out of L2): b 304, 2048 positions
-// each 131 us, 5.5 TB/s of codes and parameters; b 96, up to 8191: 125 us, 4.6; b 1,
-// 131072: 43 us, 3.5; b 64, 8 tokens, 4096: 137 us; b 1, 517: 6.4 us; 28 and 4 heads
-// of 64, b 6, 5 tokens, up to 40000: 47.5 us.
+// their rates; a CTA's start and end (3.1 us) and the last wave are the rest.  With
+// more rows instructions: every 16 rows unpack the codes for themselves, so that a
+// prompt of 2731 tokens runs at 159 TFLOP/s, a twelfth of the tensor cores' rate.
+// Measured (32 q and 8 kv heads of 128; one call repeated in a graph, so that caches
+// below 100 MB come from L2; emptying L2 in between adds 1 % at most): b 304, 2048
+// positions each 133 us, 5.4 TB/s of codes and parameters; b 96, up to 8191: 127 us,
+// 4.5; b 1, 131072: 43.5 us, 3.5; b 64, 8 tokens, 4096: 142 us; b 1, 517: 6.7 us; 28 and
+// 4 heads of 64, b 6, 5 tokens, up to 40000: 48.6 us; prompts of 1024 tokens behind 1024
+// positions, of 2731, and three of those: 152, 385 and 1373 us.
 #include "ptx.cuh"
 #include "row_ops.cuh"
 #include "step.cuh"

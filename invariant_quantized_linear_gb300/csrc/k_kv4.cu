@@ -8,12 +8,15 @@
 // token and stay in registers.  The 8 are consecutive (one 16-byte load, one word
 // of key codes), or, where all of a head is rotated in the half layout, 4 of each
 // half, so that an element's partner is in the same lane: no exchange, no element
-// normed twice (8193 tokens: 62 us without that form, 44 with it).  A token's
+// normed twice (8178 tokens: 62 us without that form, 44 with it).  A token's
 // heads are shared by as many warps as it takes to fill the GPU: one warp a token
 // for long prompts, one warp for every two heads of a single token.
-// Measured (32 q and 8 kv heads of 128, norms): 8193 tokens 44 us, 4.0 TB/s, what
-// is left being instructions (the norm's and the codes' IEEE divisions); one
-// token 3.0 us.  Gather of 8193 tokens 9.2 us (output in L2), of one 2.6 us.
+// Measured (32 q and 8 kv heads of 128, norms): 8178 tokens 44.5 us, 4.0 TB/s; what
+// is left is instructions (issue slots 66 % busy; every lane of a group computes the
+// group's two IEEE divisions) and latency at 17.6 warps a SM.  All six forms spill at
+// 96 registers (12 to 28 bytes stored a thread).  Heads rotated in part or in pairs
+// take 60.5 to 64.5 us: an element's partner is in another lane or is normed twice.
+// One token 3.1 us.  Gather of 8178 tokens 9.3 us (output in L2), of one 2.6 us.
 #include "ptx.cuh"
 #include "row_ops.cuh"
 #include "step.cuh"

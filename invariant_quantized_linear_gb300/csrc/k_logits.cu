@@ -16,7 +16,8 @@
 // 128259 take 48 us without rules, 6.4 TB/s.  A history is read once per slice,
 // from L2 after the first, and its four barriers and two looks are what the
 // stream of other CTAs hides in part only: 84 us with histories of 3000, biases
-// and masks (3.7 TB/s).  5 rows of 151936: 7.0 us.  Measured and not kept: the
+// and masks (3.7 TB/s), 70 when only the argmax is asked for (2 bytes a logit: 16 us
+// of copies).  5 rows of 151936: 7.1 us.  Measured and not kept: the
 // slices of a row as a cluster that sorts the history once (104 us), ids taken
 // in turn by a warp's lanes (84, small calls slower), CTAs of 128 or 512 threads
 // (89, 88), slices as long as balanced waves allow (85).  Rows of an odd vocabulary start
