@@ -257,3 +257,24 @@ def test_blocks_of_small_values_far_below_the_maximum(bi, D, sigma):
 def test_append_of_prompts_in_every_layout(bi, seqs, Hq, Hkv, D, P, rot, inter, norm):
     """Heads rotated in part, or in pairs, in calls whose warps have several steps."""
     step.test_append_and_gather(bi, seqs, Hq, Hkv, D, P, rot, inter, norm)
+
+
+@pytest.mark.parametrize("copies", [1, 60])
+@pytest.mark.parametrize("D,P", [(64, 64), (128, 16)])
+def test_a_seen_value_that_is_not_finite_spoils_its_group_alone(bi, D, P, copies):
+    """An infinite value that every row of its block sees: NaN in its group, the head's other group and the other kv head
+    as without it but for the weights' rounding."""
+    b = verify_pass(bi, [(2, 300)], 2, D, P, copies)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q = torch.randn((b.T, 8, D), device=DEV, generator=gen).bfloat16()
+    value = lambda t: t.view(torch.bfloat16).float()
+    clean = value(step.attend(bi, b, q, D ** -0.5))
+    for s in range(copies):
+        words = b.d_pool[int(b.pages[s, 70 // P]), 0, 1, P * D:].view(torch.int16).view(P, 2, D // 64, 2)
+        words[70 % P, 1, 0, 0] = 0x7F80
+    o = value(step.attend(bi, b, q, D ** -0.5))
+    assert torch.equal(o[:, :4], clean[:, :4])
+    assert o[:, 4:, :64].isnan().all()
+    # both results rounded to bf16, and their weights to f16, both ways; |v| < 6
+    was = clean[:, 4:, 64:]
+    assert ((o[:, 4:, 64:] - was).abs() <= 2 * (was.abs() * 2.0 ** -8 + 6 * 2.0 ** -10)).all()
