@@ -556,6 +556,112 @@ BI_API bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, i
                                    bi_stream_t stream);
 
 /*
+ * e4m3 linears: activations in 8-bit floating point (1 sign, 4 exponent and 3
+ * fraction bits, largest 448, no infinities) with an fp32 scale for each 128
+ * elements of a row, weights with one for each block of 128 x 128.  Blocks at
+ * the end of a row or column may be short; KB = ceil(K / 128), NB = ceil(N / 128).
+ * K is a multiple of 16, 16 .. 2^20; codes are passed as their bytes.
+ *
+ * Quantisation, every operation rounded once:
+ *   s = amax / 448 over the block, or 1 where that is 0
+ *   q = e4m3(x / s): fp32 division, round to nearest even, 448 at most
+ * x is bf16, or the fp32 gated product act(g) * u of packed rows gate|up:
+ * relu(g) = g > 0 ? g : 0, silu(g) = g / (1 + exp(-g)) with a relative error
+ * below (|g| + 8) 2^-23.  A block with an infinity or a NaN has that as its
+ * scale and NaN in its codes, so that it shows in its own row alone.
+ *   x   bf16 [M, ldx], first K columns (2 K behind a gate) read, 16-byte aligned, ldx % 8 == 0
+ *   q   e4m3 [M, K] out, 16-byte aligned;  s_a fp32 [M, KB] out;  1 <= M <= 2^20
+ * Outputs overlap neither each other nor the input.  With BI_FLAG_PDL the kernel
+ * waits for the preceding kernel first.
+ */
+enum { BI_GATE_RELU = 0, BI_GATE_SILU = 1 };
+BI_API bi_status bi_quantize_act_f8(const uint16_t *x, int64_t ldx, int M, int K, uint8_t *q, float *s_a, unsigned flags,
+                                    bi_stream_t stream);
+BI_API bi_status bi_gated_quantize_f8(const uint16_t *gu, int64_t ldgu, int M, int K, int gate, uint8_t *q, float *s_a,
+                                      unsigned flags, bi_stream_t stream);
+
+/*
+ * The weights' format from fp32, by the same rule over blocks of 128 x 128.
+ *   w    fp32 [N, ldw], first K columns, 16-byte aligned, ldw % 4 == 0;  1 <= N <= 2^24
+ *   w_q  e4m3 [N, K] out, 16-byte aligned;  s_w fp32 [NB, KB] out
+ */
+BI_API bi_status bi_quantize_weight_f8(const float *w, int64_t ldw, int N, int K, uint8_t *w_q, float *s_w,
+                                       bi_stream_t stream);
+
+/*
+ * The linear: y[m, n] = bf16_rne(acc) with acc = 0 and then, for the blocks b of
+ * K in order,
+ *   acc = fma(d, s_a[m, b] * s_w[n / 128, b], acc)   (product and fma in fp32)
+ * where d is the tensor cores' fp32 sum of the block's products of codes, added
+ * in the same way whatever M, N and the call are: a row's bits depend on that row
+ * and the weights alone.
+ *   q, s_a  as above, q 16-byte aligned;  w e4m3 [N, K], 16-byte aligned;  s_w fp32 [NB, KB]
+ *   y   bf16 [M, N] out (on 2 bytes);  1 <= M <= 2^20, 1 <= N <= 2^24
+ *   ws  workspace of at least bi_f8_workspace_size() bytes, 16-byte aligned,
+ *       zero-filled before its first use.  It holds a status alone (a wait that
+ *       gives up is reported by bi_workspace_status as BI_ERR_TIMEOUT), so that
+ *       calls that overlap may share one.
+ * y and ws overlap neither each other nor an input.
+ *
+ * bi_linear_f8_grouped: rows that belong to experts with weights of their own.
+ * Expert e has rows offsets[e] .. offsets[e + 1] - 1 of y:
+ *   y[r] = the linear of row src[r] of q (row r where src is NULL) and w[e].
+ *   q, s_a   q_rows rows, q_rows >= R where src is NULL;  1 <= q_rows, R <= 2^20
+ *   src      int32 [R] or NULL; a row that it sends outside 0 .. q_rows - 1 is 0
+ *   offsets  int32 [E + 1], non-decreasing, read on the device (a captured graph
+ *            may be replayed with other offsets).  Rows of y before offsets[0] and
+ *            from offsets[E] on are left as they were.  An offset below the one
+ *            before it counts as that one, one above R as R.
+ *   w        e4m3 [E, N, K];  s_w fp32 [E, NB, KB];  1 <= E <= 1024, E N < 2^31
+ * R and E decide how the work is split, not what a row's bits are.
+ */
+BI_API size_t bi_f8_workspace_size(void);
+BI_API bi_status bi_linear_f8(const uint8_t *q, const float *s_a, int M, int K, const uint8_t *w, const float *s_w, int N,
+                              uint16_t *y, void *ws, size_t ws_bytes, unsigned flags, bi_stream_t stream);
+BI_API bi_status bi_linear_f8_grouped(const uint8_t *q, const float *s_a, int q_rows, int K, const int32_t *src, int R,
+                                      const int32_t *offsets, int E, const uint8_t *w, const float *s_w, int N, uint16_t *y,
+                                      void *ws, size_t ws_bytes, unsigned flags, bi_stream_t stream);
+
+/*
+ * A router's selection, and the order of rows by expert that the grouped linear
+ * reads.  Token m takes the k experts with the largest logits, in that order, the
+ * lowest id first among equals.  A logit of -inf (or NaN) is never taken: where
+ * fewer than k are left, ids are -1 and weights 0.  +inf counts as the largest
+ * finite value.  Weights, fp32:
+ *   BI_ROUTE_SOFTMAX  p = exp(x - max) / sum over all experts (over the taken ones with renorm)
+ *   BI_ROUTE_SIGMOID  p = 1 / (1 + exp(-x)), divided by the taken ones' sum with renorm (by 1 where that is 0)
+ *   weights = p * scale
+ * Slot m k + j of expert e has a row; rows are in the order of experts, then slots:
+ *   logits   fp32 or bf16 (`type`) [M, ldl], ldl >= E, read only
+ *   ids      int32 [M, k] out;  weights fp32 [M, k] out
+ *   offsets  int32 [E + 1] out: first row of each expert, and the number of rows
+ *   src      int32 [M k] out: token of each row, -1 from offsets[E] on
+ *   pos      int32 [M, k] out: row of each slot, -1 for an id of -1
+ *   ws       workspace of at least bi_moe_route_workspace_size(M, E) bytes, 16-byte
+ *            aligned, scratch: calls that may overlap must not share one
+ * 1 <= M <= 65535, 1 <= E <= 1024, 1 <= k <= min(E, 32), scale finite.  Outputs and
+ * workspace overlap neither one another nor the logits.
+ */
+enum { BI_TYPE_F32 = 0, BI_TYPE_BF16 = 1 };
+enum { BI_ROUTE_SOFTMAX = 0, BI_ROUTE_SIGMOID = 1 };
+BI_API size_t bi_moe_route_workspace_size(int M, int E);
+BI_API bi_status bi_moe_route(const void *logits, int64_t ldl, int type, int M, int E, int k, int score, int renorm,
+                              float scale, int32_t *ids, float *weights, int32_t *offsets, int32_t *src, int32_t *pos,
+                              void *ws, size_t ws_bytes, unsigned flags, bi_stream_t stream);
+
+/*
+ * The weighted sum of the experts' rows: acc = 0, then acc = fma(weights[m, j],
+ * rows[pos[m, j], n], acc) in the order of j, y[m, n] = bf16_rne(base[m, n] + acc).
+ * A slot whose pos lies outside 0 .. R - 1 is left out, whatever its weight.
+ *   rows bf16 [R, N];  pos int32, weights fp32 [M, k];  base bf16 [M, N] or NULL: 0
+ *   y    bf16 [M, N] out; it may be base, and overlaps nothing else
+ * 1 <= M <= 65535, 1 <= k <= 32, 1 <= R <= 2^21, 1 <= N <= 2^24.  Rows on 2 bytes;
+ * on 16 with N a multiple of 8 they are faster.
+ */
+BI_API bi_status bi_moe_combine(const uint16_t *rows, int R, const int32_t *pos, const float *weights, int M, int k, int N,
+                                const uint16_t *base, uint16_t *y, unsigned flags, bi_stream_t stream);
+
+/*
  * Bandwidth probes, for measurement only: the device's own read-only and copy
  * ceilings with 16-byte streaming loads (8 in flight per thread) over a grid
  * of four 512-thread CTAs per SM.  A weight stream only reads, so the

@@ -120,6 +120,25 @@ lib.bi_logits_workspace_size.restype = _sz
 lib.bi_logits_process.argtypes = [_vp, _i64, _ci, _ci, ctypes.POINTER(bi_logits_rules), _vp, _i64, _vp, _vp, _sz, _cu,
                                   _vp]
 lib.bi_logits_process.restype = _ci
+lib.bi_quantize_act_f8.argtypes = [_vp, _i64, _ci, _ci, _vp, _vp, _cu, _vp]
+lib.bi_quantize_act_f8.restype = _ci
+lib.bi_gated_quantize_f8.argtypes = [_vp, _i64, _ci, _ci, _ci, _vp, _vp, _cu, _vp]
+lib.bi_gated_quantize_f8.restype = _ci
+lib.bi_quantize_weight_f8.argtypes = [_vp, _i64, _ci, _ci, _vp, _vp, _vp]
+lib.bi_quantize_weight_f8.restype = _ci
+lib.bi_f8_workspace_size.argtypes = []
+lib.bi_f8_workspace_size.restype = _sz
+lib.bi_linear_f8.argtypes = [_vp, _vp, _ci, _ci, _vp, _vp, _ci, _vp, _vp, _sz, _cu, _vp]
+lib.bi_linear_f8.restype = _ci
+lib.bi_linear_f8_grouped.argtypes = [_vp, _vp, _ci, _ci, _vp, _ci, _vp, _ci, _vp, _vp, _ci, _vp, _vp, _sz, _cu, _vp]
+lib.bi_linear_f8_grouped.restype = _ci
+lib.bi_moe_route_workspace_size.argtypes = [_ci, _ci]
+lib.bi_moe_route_workspace_size.restype = _sz
+lib.bi_moe_route.argtypes = [_vp, _i64, _ci, _ci, _ci, _ci, _ci, _ci, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _cu,
+                             _vp]
+lib.bi_moe_route.restype = _ci
+lib.bi_moe_combine.argtypes = [_vp, _ci, _vp, _vp, _ci, _ci, _ci, _vp, _vp, _cu, _vp]
+lib.bi_moe_combine.restype = _ci
 lib.bi_probe_read.argtypes = [_vp, _sz, _vp, _vp]
 lib.bi_probe_read.restype = _ci
 lib.bi_probe_copy.argtypes = [_vp, _vp, _sz, _vp]
@@ -161,6 +180,12 @@ BI_ERR_CUDA = 7
 BI_FLAG_PDL = 1
 BI_ROPE_HALF = 0
 BI_ROPE_INTERLEAVED = 1
+BI_GATE_RELU = 0
+BI_GATE_SILU = 1
+BI_TYPE_F32 = 0
+BI_TYPE_BF16 = 1
+BI_ROUTE_SOFTMAX = 0
+BI_ROUTE_SIGMOID = 1
 
 
 class BiError(RuntimeError):
@@ -466,6 +491,110 @@ def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.T
     _check(lib.bi_logits_process(logits.data_ptr(), ldl, M, V, rules, _ptr(out), ldo,
                                  None if argmax is None else _vector(argmax, M, 4), ws.data_ptr(), ws.nbytes, flags,
                                  _stream(stream)), "bi_logits_process")
+
+
+def _dense(t: torch.Tensor, shape: tuple, size: int) -> int:
+    """The address of elements of `size` bytes of this shape side by side."""
+    assert t.shape == shape and t.is_contiguous() and t.element_size() == size
+    return t.data_ptr()
+
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 elements, the last one may be short."""
+    return (n + 127) // 128
+
+
+def bi_quantize_act_f8(x: torch.Tensor, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """x: bf16 [M, >= K] (row stride x.stride(0)); q: e4m3 [M, K] (float8_e4m3fn or bytes); s_a: fp32 [M, ceil(K / 128)]."""
+    M, K = q.shape
+    _check(lib.bi_quantize_act_f8(x.data_ptr(), _rows(x, M, K, 2), M, K, _dense(q, (M, K), 1), _dense(s_a, (M, _blocks(K)), 4),
+                                  flags, _stream(stream)), "bi_quantize_act_f8")
+
+
+def bi_gated_quantize_f8(gu: torch.Tensor, gate: int, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """gu: bf16 [M, >= 2K] packed gate|up (row stride gu.stride(0)); gate: BI_GATE_RELU or BI_GATE_SILU; q: e4m3 [M, K];
+    s_a: fp32 [M, ceil(K / 128)]."""
+    M, K = q.shape
+    _check(lib.bi_gated_quantize_f8(gu.data_ptr(), _rows(gu, M, 2 * K, 2), M, K, gate, _dense(q, (M, K), 1),
+                                    _dense(s_a, (M, _blocks(K)), 4), flags, _stream(stream)), "bi_gated_quantize_f8")
+
+
+def bi_quantize_weight_f8(w: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor, stream=None) -> None:
+    """w: fp32 [N, K] (row stride w.stride(0)); w_q: e4m3 [N, K]; s_w: fp32 [ceil(N / 128), ceil(K / 128)]."""
+    N, K = w_q.shape
+    assert w.dtype == torch.float32
+    _check(lib.bi_quantize_weight_f8(w.data_ptr(), _rows(w, N, K, 4), N, K, _dense(w_q, (N, K), 1),
+                                     _dense(s_w, (_blocks(N), _blocks(K)), 4), _stream(stream)), "bi_quantize_weight_f8")
+
+
+def bi_f8_workspace_size() -> int:
+    return int(lib.bi_f8_workspace_size())
+
+
+def new_f8_workspace(device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for bi_linear_f8 and bi_linear_f8_grouped calls of any size."""
+    return torch.zeros(bi_f8_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def bi_linear_f8(q: torch.Tensor, s_a: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, y: torch.Tensor, ws: torch.Tensor,
+                 flags: int = 0, stream=None) -> None:
+    """q: e4m3 [M, K], s_a: fp32 [M, ceil(K / 128)]; w: e4m3 [N, K], s_w: fp32 [ceil(N / 128), ceil(K / 128)]; y: bf16 [M, N];
+    ws: from new_f8_workspace."""
+    (M, K), N = q.shape, w.shape[0]
+    kb = _blocks(K)
+    _check(lib.bi_linear_f8(_dense(q, (M, K), 1), _dense(s_a, (M, kb), 4), M, K, _dense(w, (N, K), 1),
+                            _dense(s_w, (_blocks(N), kb), 4), N, _dense(y, (M, N), 2), ws.data_ptr(), ws.nbytes, flags,
+                            _stream(stream)), "bi_linear_f8")
+
+
+def bi_linear_f8_grouped(q: torch.Tensor, s_a: torch.Tensor, src: torch.Tensor | None, offsets: torch.Tensor, w: torch.Tensor,
+                         s_w: torch.Tensor, y: torch.Tensor, ws: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """y: bf16 [R, N], expert e's rows offsets[e] .. offsets[e + 1] - 1 (int32 [E + 1]) = rows src[r] (int32 [R], None: r) of
+    q: e4m3 [n, K], s_a: fp32 [n, ceil(K / 128)] by w: e4m3 [E, N, K], s_w: fp32 [E, ceil(N / 128), ceil(K / 128)]."""
+    (n, K), (R, N), E = q.shape, y.shape, w.shape[0]
+    kb = _blocks(K)
+    assert offsets.dtype == torch.int32 and (src is None or src.dtype == torch.int32)
+    _check(lib.bi_linear_f8_grouped(_dense(q, (n, K), 1), _dense(s_a, (n, kb), 4), n, K,
+                                    None if src is None else _dense(src, (R,), 4), R, _dense(offsets, (E + 1,), 4), E,
+                                    _dense(w, (E, N, K), 1), _dense(s_w, (E, _blocks(N), kb), 4), N, _dense(y, (R, N), 2),
+                                    ws.data_ptr(), ws.nbytes, flags, _stream(stream)), "bi_linear_f8_grouped")
+
+
+def bi_moe_route_workspace_size(M: int, E: int) -> int:
+    return int(lib.bi_moe_route_workspace_size(M, E))
+
+
+def new_moe_route_workspace(M: int, E: int, device="cuda") -> torch.Tensor:
+    """A workspace for bi_moe_route calls of M tokens and E experts."""
+    return torch.empty(bi_moe_route_workspace_size(M, E), dtype=torch.uint8, device=device)
+
+
+def bi_moe_route(logits: torch.Tensor, score: int, renorm: bool, scale: float, ids: torch.Tensor, weights: torch.Tensor,
+                 offsets: torch.Tensor, src: torch.Tensor, pos: torch.Tensor, ws: torch.Tensor, flags: int = 0,
+                 stream=None) -> None:
+    """logits: fp32 or bf16 [M, E] (row stride logits.stride(0)); score: BI_ROUTE_SOFTMAX or BI_ROUTE_SIGMOID; ids: int32
+    [M, k]; weights: fp32 [M, k]; offsets: int32 [E + 1]; src: int32 [M k]; pos: int32 [M, k]."""
+    (M, E), k = logits.shape, ids.shape[1]
+    half = logits.dtype == torch.bfloat16
+    assert half or logits.dtype == torch.float32
+    for t in (ids, offsets, src, pos):
+        assert t.dtype == torch.int32
+    assert weights.dtype == torch.float32
+    _check(lib.bi_moe_route(logits.data_ptr(), _rows(logits, M, E, 2 if half else 4), BI_TYPE_BF16 if half else BI_TYPE_F32, M, E,
+                            k, score, renorm, scale, _dense(ids, (M, k), 4), _dense(weights, (M, k), 4),
+                            _dense(offsets, (E + 1,), 4), _dense(src, (M * k,), 4), _dense(pos, (M, k), 4), ws.data_ptr(),
+                            ws.nbytes, flags, _stream(stream)), "bi_moe_route")
+
+
+def bi_moe_combine(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, base: torch.Tensor | None, y: torch.Tensor,
+                   flags: int = 0, stream=None) -> None:
+    """rows: bf16 [R, N]; pos: int32 [M, k]; weights: fp32 [M, k]; base: bf16 [M, N] or None; y: bf16 [M, N], it may be
+    base."""
+    (M, k), (R, N) = pos.shape, rows.shape
+    assert pos.dtype == torch.int32 and weights.dtype == torch.float32
+    _check(lib.bi_moe_combine(_dense(rows, (R, N), 2), R, _dense(pos, (M, k), 4), _dense(weights, (M, k), 4), M, k, N,
+                              None if base is None else _dense(base, (M, N), 2), _dense(y, (M, N), 2), flags, _stream(stream)),
+           "bi_moe_combine")
 
 
 def bi_probe_read(buf: torch.Tensor, out: torch.Tensor, stream=None) -> None:

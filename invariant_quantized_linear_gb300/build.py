@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libbi.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["bi_api.cu", "k_quant.cu", "k_skinny.cu", "k_prefill.cu", "k_prefill_tma.cu", "bi_noalloc.cu", "k_program.cu", "k_blockq.cu", "k_attn.cu", "k_probe.cu",
-           "bi_step.cu", "k_norm.cu", "k_kv4.cu", "k_attn_kv4.cu", "k_logits.cu"]
+           "bi_step.cu", "k_norm.cu", "k_kv4.cu", "k_attn_kv4.cu", "k_logits.cu",
+           "bi_f8.cu", "k_f8_quant.cu", "k_f8_linear.cu", "k_moe.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -130,6 +130,18 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Four rows y of a 2-D tensor, whose map's box is one row high, into consecutive rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar, int x, const int (&y)[4],
+                                            uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+        "l"(policy)
+        : "memory");
+}
+
 // Prefetch one 2-D box of a tensor into L2 (no shared memory, no completion
 // signal); a later tma_load_2d of the same box then reads it from L2.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y)
