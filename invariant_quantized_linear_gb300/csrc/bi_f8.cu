@@ -99,10 +99,14 @@ bi_status linear(const uint8_t *q, const float *s_a, int q_rows, int K, const in
     bi::F8LinearArgs a;
     bi_status st = device_info(&a.sms);
     if (st != BI_OK) return st;
+    a.plan = bi::f8_plan(R, E, N, a.sms);
+    // one copy for a tile's tokens, or pieces of at most 64 where tiles differ
+    const int tiles = (R + a.plan.cols - 1) / a.plan.cols;
+    a.box = !offsets ? ((R + tiles - 1) / tiles + 15) / 16 * 16 : a.plan.T < 64 ? a.plan.T : 64;
     const long long w_rows = static_cast<long long>(E) * N;
     st = encode(&a.map_w, w, w_rows, K, 128, true);
     if (st == BI_OK) st = encode(&a.map_w16, w, w_rows, K, 16, true);
-    if (st == BI_OK) st = encode(&a.map_q, q, q_rows, K, src ? 1 : 16, false);
+    if (st == BI_OK) st = encode(&a.map_q, q, q_rows, K, src ? 1 : a.box, false);
     if (st != BI_OK) return st;
     a.s_a = s_a;
     a.s_w = s_w;
@@ -115,7 +119,6 @@ bi_status linear(const uint8_t *q, const float *s_a, int q_rows, int K, const in
     a.N = N;
     a.K = K;
     a.status = bi::workspace_view(ws).status;
-    a.plan = bi::f8_plan(R, E, N, a.sms);
     return from_cuda(bi::launch_linear_f8(a, (flags & BI_FLAG_PDL) != 0, stream));
 }
 

@@ -32,7 +32,7 @@ cudaError_t launch_quantize_weight_f8(const float *w, int64_t ldw, int N, int K,
 
 // Token columns of a tile: how a call is split into tiles (see f8_plan).
 struct F8Plan {
-    int T;            // most token columns of a tile: 16, 32, 64, 128 or 256
+    int T;            // most token columns of a tile: 16, 32, 64, 128 or 192
     int cols;         // tokens a tile is filled to (a multiple of 16, <= T)
 };
 
@@ -41,7 +41,8 @@ F8Plan f8_plan(int rows, int experts, int N, int sms);
 struct F8LinearArgs {
     CUtensorMap map_w;          // w [E N, K], box 128 B x 128 rows
     CUtensorMap map_w16;        // the same, 16 rows
-    CUtensorMap map_q;          // q [rows of q, K], box 128 B x 16 rows, or x 1 row where src is given
+    CUtensorMap map_q;          // q [rows of q, K], box 128 B x `box` rows, or x 1 row where src is given
+    int box;
     const float *s_a, *s_w;
     const int32_t *src;         // row of q for each row of y, or null: the same row
     const int32_t *offsets;     // [E + 1] rows of each expert, or null: one weight matrix, all rows

@@ -15,7 +15,7 @@
 //   warp 0     copies weight and token tiles into a ring, one block of K a stage;
 //              token rows that src names are gathered four at a time;
 //   warp 1     allocates TMEM, issues the MMAs, a block an accumulator;
-//   warp 2     multiplies the scales of 8 blocks ahead into a table;
+//   warps 2-3  multiply the scales of 8 blocks ahead into a table;
 //   warps 4 on a weight row a thread (TMEM lane), up to 128 tokens: take each
 //              accumulator out of TMEM into the fp32 sums, then store.
 //
@@ -42,25 +42,33 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kAhead = 8;                 // blocks of K in a scale table
-constexpr int kEpiWarp0 = 4;
-constexpr int kStageW = kTileRows * kF8Block;
+constexpr int kBlockW = kTileRows * kF8Block;
 
-template <int T>
+// T: token columns of a tile at most.  GATHER: token rows are fetched by src.
+template <int T_, bool GATHER_>
 struct Cfg {
-    static constexpr int kHalves = T == 256 ? 2 : 1;           // epilogue threads a weight row
-    static constexpr int kCols = T / kHalves;
-    static constexpr int kEpiWarps = 4 * kHalves;
+    static constexpr int T = T_;
+    static constexpr bool GATHER = GATHER_;
+    static constexpr bool kWide = T == 192;                    // tensor cores bound the call, not the weight stream
+    static constexpr int kParts = kWide ? 4 : T >= 64 ? 2 : 1; // warps that share a weight row's columns
+    static constexpr int kCols = T / kParts;
+    static constexpr int kEpiWarp0 = GATHER ? 8 : 4;
+    static constexpr int kEpiWarps = 4 * kParts;
     static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
-    static constexpr int kUnit = T == 256 ? 128 : 16;
-    static constexpr bool kInTurn = T == 256;
-    static constexpr int kStage = kStageW + T * kF8Block;
-    static constexpr int kStages = T == 256 ? 4 : T == 128 ? 6 : T == 64 ? 8 : 10;
-    static constexpr int kAccs = T == 256 ? 2 : T == 128 ? 4 : 8;
-    static constexpr uint32_t kTmemCols = T * kAccs;
-    static constexpr int kTables = T == 256 ? 1 : 2;           // 128-row blocks of weights that a tile meets
+    static constexpr int kUnit = kWide ? 128 : 16;
+    static constexpr int P = T <= 64 ? 2 : 1;                  // blocks of K a stage
+    static constexpr int kBlockQ = T * kF8Block;
+    static constexpr int kStage = P * (kBlockW + kBlockQ);
+    static constexpr int kStages = T == 128 ? 6 : T == 64 ? 4 : 5;
+    static constexpr int kAccs = kWide ? 2 : T >= 64 ? 4 : 8;  // accumulators in turn, each of P blocks
+    static constexpr int kAccCols = kWide ? 256 : P * T;
+    static constexpr uint32_t kTmemCols = kAccCols * kAccs;
+    static constexpr int kTables = kWide ? 1 : 2;              // 128-row blocks of weights that a tile meets
     static constexpr int kScaleLd = T + 4;                     // floats between a table's rows: bank-free for its writers
     static constexpr int kTable = kAhead * kScaleLd;
     static constexpr int kScales = 2 * kTables * kTable;       // floats, two tables in turn
+    static constexpr int kRows = GATHER ? T : 0;               // rows of q of a tile
+    static_assert(kTmemCols <= 512 && kAhead % P == 0 && kStage % 1024 == 0, "layout");
 };
 
 struct Params {
@@ -68,16 +76,33 @@ struct Params {
     const int32_t *src, *offsets;
     uint16_t *y;
     int q_rows, R, E, N, K, kb, nb, cols;
+    int box;           // token rows of a copy, where src is null
+    int pairs;         // two results may be stored together
     int *status;
     int pdl;
 };
 
-template <int T>
+constexpr int kBarBytes = 512;
+
+template <class C>
 size_t smem_bytes(int E)
 {
-    using C = Cfg<T>;
-    return 1024 + C::kStages * C::kStage + C::kScales * 4 + 512 + 8 * (E + 1) + 4 * (E + 1);
+    return 1024 + C::kStages * C::kStage + (C::kScales + C::kRows) * 4 + kBarBytes + 8 * (E + 1) + 4 * (E + 1);
 }
+
+// Position in a ring of N buffers: a consumer waits for parity `phase`, a producer for the other.
+template <int N>
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == N) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 struct Tile {
     int e;
@@ -86,6 +111,9 @@ struct Tile {
     int w0, rows;  // weight rows of the expert
     int len;       // units
 };
+
+// Where a table has column m: the four of a group of 16 that a thread's fragments hold are side by side.
+__device__ __forceinline__ int place(int m) { return (m & ~15) | ((m & 6) << 1) | ((m & 8) >> 2) | (m & 1); }
 
 // The list of units, in shared memory: first unit and first row of each expert.
 struct Work {
@@ -109,10 +137,18 @@ __device__ __forceinline__ int expert_of(const Work &w, long long x)
     return lo;
 }
 
-// The tile that starts at unit x of expert t.e or a later one, ending before `end`.
+// A value that all lanes have, known to be one: what is derived from it may stay in
+// uniform registers.  Without this, every copy, MMA and TMEM load is issued by a loop
+// over the distinct values its operands might have (300 cycles a copy for 31).
+__device__ __forceinline__ int same(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__device__ __forceinline__ long long same(long long v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// The tile that starts at unit x of expert t.e or a later one, ending before `end`.  Called by whole warps.
 __device__ __forceinline__ void tile_at(const Work &w, long long x, long long end, Tile &t)
 {
     while (w.first[t.e + 1] <= x) ++t.e;
+    t.e = same(t.e);
     const int n_e = w.row[t.e + 1] - w.row[t.e];
     const int tt = (n_e + w.cols - 1) / w.cols, nu = (w.N + w.unit - 1) / w.unit, per = kTileRows / w.unit;
     const long long off = x - w.first[t.e];
@@ -121,24 +157,95 @@ __device__ __forceinline__ void tile_at(const Work &w, long long x, long long en
     const int run = min(per, nu - chunk * per);
     const int ti = rem / run, u = rem - ti * run;
     const long long left = end - x;
-    t.len = left < run - u ? static_cast<int>(left) : run - u;
-    t.w0 = (chunk * per + u) * w.unit;
+    t.len = same(left < run - u ? static_cast<int>(left) : run - u);
+    t.w0 = same((chunk * per + u) * w.unit);
     t.rows = min(t.len * w.unit, w.N - t.w0);
     const int c = ((n_e + tt - 1) / tt + 15) & ~15;            // tokens of a tile, spread evenly
-    t.row0 = w.row[t.e] + ti * c;
-    t.n = min(c, n_e - ti * c);
+    t.row0 = same(w.row[t.e] + ti * c);
+    t.n = same(min(c, n_e - ti * c));
 }
 
-template <int T>
-__global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
+// Adds the blocks of a tile, 16 NG columns of 32 rows, into acc: columns 8 j + 2 (lane % 4), + 1 of row lane / 4 + 8 i
+// are in acc[4 j + i].  NG is a constant because a branch around each group's TMEM loads would order them one behind
+// the other (a block of 96 columns took 1,850 cycles, 560 without).  table[h]: where the scales of rows 16 h on are.
+template <class C, int NG>
+__device__ __forceinline__ bool sum_blocks(f2 *acc, int blocks, const float *scales, const int (&table)[2], uint32_t from,
+                                           uint64_t *acc_full, uint64_t *acc_empty, uint64_t *sc_full, uint64_t *sc_empty,
+                                           Ring<C::kAccs> &accs, Ring<2> &tabs, volatile int *abort_flag)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int g = 0; g < 8 * NG; ++g) acc[g] = 0;
+    for (int kb = 0; kb < blocks; kb += C::P) {
+        const int a = accs.s;
+        // warp-uniform: the TMEM loads below are warp-collective
+        if (!__all_sync(0xffffffffu, (kb % kAhead != 0 || mbar_wait_bounded(&sc_full[tabs.s], tabs.phase, abort_flag)) &&
+                                         mbar_wait_bounded(&acc_full[a], accs.phase, abort_flag)))
+            return false;
+        tc::fence_after();
+#pragma unroll
+        for (int q = 0; q < C::P; ++q) {
+            if (q > 0 && kb + q >= blocks) break;
+            const float *sc = scales + tabs.s * C::kTables * C::kTable + (kb % kAhead + q) * C::kScaleLd;
+            // 16 columns are on their way from TMEM while the 16 before them are added
+            uint32_t d[2][16];
+            const uint32_t at = from + a * C::kAccCols + q * C::T;
+            auto fetch = [&](int g) {
+                tc::ld16_frag(at + 16 * g, d[g & 1]);
+                tc::ld16_frag(at + 16 * g + (16u << 16), d[g & 1] + 8);
+            };
+            if (NG > 0) fetch(0);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float4 lo = *reinterpret_cast<const float4 *>(sc + table[0] + 16 * g);
+                const float4 hi = C::kTables == 2 ? *reinterpret_cast<const float4 *>(sc + table[1] + 16 * g) : lo;
+                tc::wait_ld();
+                if (g + 1 < NG) fetch(g + 1);
+                const uint32_t(&v)[16] = d[g & 1];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 &f = i < 2 ? lo : hi;
+                        const int r = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
+                        f2 &s = acc[8 * g + 4 * j + i];
+                        s = fma2(pk(__uint_as_float(v[r]), __uint_as_float(v[r + 1])), j ? pk(f.z, f.w) : pk(f.x, f.y), s);
+                    }
+            }
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[a]);
+        accs.next();
+        if (kb % kAhead == kAhead - C::P || kb + C::P >= blocks) {
+            if (lane == 0) mbar_arrive(&sc_empty[tabs.s]);
+            tabs.next();
+        }
+    }
+    return true;
+}
+
+// The same for `groups` groups, at most NG.
+template <class C, int NG, typename... Rest>
+__device__ __forceinline__ bool sum_any(int groups, Rest &&...rest)
+{
+    if constexpr (NG > 0) {
+        if (groups < NG) return sum_any<C, NG - 1>(groups, rest...);
+    }
+    return sum_blocks<C, NG>(rest...);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1)
     linear_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w16,
                      const __grid_constant__ CUtensorMap map_q, Params p)
 {
-    using C = Cfg<T>;
+    constexpr int T = C::T;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *scales = reinterpret_cast<float *>(smem + C::kStages * C::kStage);
-    uint64_t *full = reinterpret_cast<uint64_t *>(scales + C::kScales);   // copies landed
+    int *row_of = reinterpret_cast<int *>(scales + C::kScales);           // GATHER: the tile's rows of q
+    uint64_t *full = reinterpret_cast<uint64_t *>(row_of + C::kRows);     // copies landed
     uint64_t *empty = full + C::kStages;                                  // MMAs done reading
     uint64_t *acc_full = empty + C::kStages;                              // block summed
     uint64_t *acc_empty = acc_full + C::kAccs;                            // taken out
@@ -147,11 +254,11 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     uint64_t *drain = sc_empty + 2;                                       // all MMAs complete
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * C::kStages + 2 * C::kAccs + 4 + 1) * 8 + 8 <= 512, "barriers fit");
-    long long *first = reinterpret_cast<long long *>(full + 64);
+    static_assert((2 * C::kStages + 2 * C::kAccs + 4 + 1) * 8 + 8 <= kBarBytes, "barriers fit");
+    long long *first = reinterpret_cast<long long *>(full + kBarBytes / 8);
     int *row = reinterpret_cast<int *>(first + p.E + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -162,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             mbar_init(&acc_empty[a], C::kEpiWarps);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_full[i], 2);
             mbar_init(&sc_empty[i], C::kEpiWarps);
         }
         mbar_init(drain, 1);
@@ -212,14 +319,14 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = static_cast<uint32_t>(same(static_cast<int>(*tmem_slot)));
     const Work work{first, row, p.E, p.N, p.cols, C::kUnit};
-    const long long total = first[p.E], b = blockIdx.x, G = gridDim.x;
+    const long long total = same(first[p.E]), b = blockIdx.x, G = gridDim.x;
     // this CTA's units: a run of them, or every G-th
-    const long long x0 = C::kInTurn ? b : total * b / G, x1 = C::kInTurn ? total : total * (b + 1) / G;
-    const int e0 = x0 < x1 ? expert_of(work, x0) : 0;
-    auto next = [&](long long x, const Tile &t) { return C::kInTurn ? x + G : x + t.len; };
-    auto end_of = [&](long long x) { return C::kInTurn ? x + 1 : x1; };
+    const long long x0 = same(C::kWide ? b : total * b / G), x1 = same(C::kWide ? total : total * (b + 1) / G);
+    const int e0 = same(x0 < x1 ? expert_of(work, x0) : 0);
+    auto next = [&](long long x, const Tile &t) { return C::kWide ? x + G : x + t.len; };
+    auto end_of = [&](long long x) { return C::kWide ? x + 1 : x1; };
 
     auto fail = [&]() {
         if (!*abort_flag) {
@@ -228,222 +335,252 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
         }
     };
 
+    if (warp < 4) {
+    // with 24 warps: 4 x 32 x 72 + 4 x 32 x 24 + 16 x 32 x 96 = 24 x 32 x 80, the launch's registers
+    if (C::kWide && C::GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
         // ------------------------------------------------ copies
+        Ring<C::kStages> ring;
+        bool ok = true, wrapped = false;
+        const uint64_t pol_w = policy_evict_first(), pol_q = policy_evict_last();
         if (lane == 0) {
             prefetch_tensormap(&map_w);
             prefetch_tensormap(&map_w16);
             prefetch_tensormap(&map_q);
         }
-        const uint64_t pol_w = policy_evict_first(), pol_q = policy_evict_last();
-        long long j = 0;
-        bool ok = true;
         Tile t;
         t.e = e0;
         for (long long x = x0; ok && x < x1; x = next(x, t)) {
             tile_at(work, x, end_of(x), t);
-            const int cols = (t.n + 15) & ~15, nw = (t.rows + 15) >> 4;
+            const bool whole = t.rows > 112;
+            const int nw = whole ? 1 : (t.rows + 15) >> 4;
+            const int nq = C::GATHER ? (t.n + 3) >> 2 : (t.n + p.box - 1) / p.box;
             const int wy = t.e * p.N + t.w0;
-            const uint32_t bytes = nw * 2048 + cols * kF8Block;
-            int idx[(T + 127) / 128][4];
-            if (p.src) {
+            const uint32_t bytes = (nw * (whole ? 128 : 16) + nq * (C::GATHER ? 4 : p.box)) * kF8Block;
+            for (int kb = 0; kb < p.kb; kb += C::P) {
+                const int s = ring.s, nb = min(C::P, p.kb - kb);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ring.phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&full[s], bytes * nb);
 #pragma unroll
-                for (int i = 0; i < (T + 127) / 128; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int m = 4 * (lane + 32 * i) + k;
-                        const int r = m < t.n ? __ldg(p.src + t.row0 + m) : 0;
-                        idx[i][k] = static_cast<unsigned>(r) < static_cast<unsigned>(p.q_rows) ? r : 0;
+                    for (int b = 0; b < C::P; ++b) {
+                        if (b >= nb) break;
+                        uint8_t *sw = smem + s * C::kStage + b * kBlockW, *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
+                        const int k = (kb + b) * kF8Block;
+                        if (whole) tma_load_2d(sw, &map_w, &full[s], k, wy, pol_w);
+                        else
+                            for (int i = 0; i < nw; ++i) tma_load_2d(sw + i * 2048, &map_w16, &full[s], k, wy + i * 16, pol_w);
+                        if (!C::GATHER)
+                            for (int i = 0; i < nq; ++i)
+                                tma_load_2d(sq + i * p.box * kF8Block, &map_q, &full[s], k, t.row0 + i * p.box, pol_q);
                     }
-            }
-            for (int kb = 0; kb < p.kb; ++kb, ++j) {
-                const int s = static_cast<int>(j % C::kStages);
-                if (j >= C::kStages)
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], static_cast<uint32_t>(j / C::kStages - 1) & 1u,
-                                                                   abort_flag));
-                if (!ok) {
-                    fail();
-                    break;
                 }
-                uint8_t *sw = smem + s * C::kStage, *sq = sw + kStageW;
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
                 __syncwarp();
-                const int k = kb * kF8Block;
-                if (nw == 8) {
-                    if (lane == 0) tma_load_2d(sw, &map_w, &full[s], k, wy, pol_w);
-                } else if (lane < nw) {
-                    tma_load_2d(sw + lane * 2048, &map_w16, &full[s], k, wy + lane * 16, pol_w);
-                }
-                if (p.src) {
-#pragma unroll
-                    for (int i = 0; i < (T + 127) / 128; ++i)
-                        if (4 * (lane + 32 * i) < cols)
-                            tma_gather4(sq + (lane + 32 * i) * 512, &map_q, &full[s], k, idx[i], pol_q);
-                } else if (16 * lane < cols) {
-                    tma_load_2d(sq + lane * 2048, &map_q, &full[s], k, t.row0 + 16 * lane, pol_q);
-                }
+                ring.next();
+                wrapped |= ring.s == 0;
             }
         }
+        if (!ok) fail();
         // every copy that was issued lands before the CTA can exit
         volatile int never = 0;
-        for (long long jj = j > C::kStages ? j - C::kStages : 0; jj < j; ++jj)
-            mbar_wait_bounded(&full[jj % C::kStages], static_cast<uint32_t>(jj / C::kStages) & 1u, &never);
+        for (int s = 0; ok && s < C::kStages; ++s)
+            if (s < ring.s || wrapped) mbar_wait_bounded(&full[s], s < ring.s ? ring.phase : ring.phase ^ 1u, &never);
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs
-        long long j = 0;
+        Ring<C::kStages> ring;
+        Ring<C::kAccs> accs;
         bool ok = true;
+        const uint64_t dw0 = tc::sdesc_kmajor_sw128(smem_u32(smem)), dq0 = tc::sdesc_kmajor_sw128(smem_u32(smem) + C::P * kBlockW);
         Tile t;
         t.e = e0;
         for (long long x = x0; ok && x < x1; x = next(x, t)) {
             tile_at(work, x, end_of(x), t);
             // rows of the stage beyond the tile's hold old bytes: their sums are never looked at
             const uint32_t idesc = tc::idesc_e4m3_f32(kTileRows, (t.n + 15) & ~15);
-            for (int kb = 0; kb < p.kb; ++kb, ++j) {
-                const int a = static_cast<int>(j % C::kAccs), s = static_cast<int>(j % C::kStages);
-                if (j >= C::kAccs)
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[a], static_cast<uint32_t>(j / C::kAccs - 1) & 1u,
-                                                                   abort_flag));
-                if (ok)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait_bounded(&full[s], static_cast<uint32_t>(j / C::kStages) & 1u, abort_flag));
+            for (int kb = 0; kb < p.kb; kb += C::P) {
+                const int a = accs.s, s = ring.s;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[a], accs.phase ^ 1u, abort_flag) &&
+                                                 mbar_wait_bounded(&full[s], ring.phase, abort_flag));
                 if (!ok) break;
                 tc::fence_after();
-                if (lane == 0) {
-                    const uint32_t sw = smem_u32(smem + s * C::kStage), sq = sw + kStageW;
+                if (elect_one()) {
+                    const uint64_t at = static_cast<uint32_t>(s * (C::kStage >> 4));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc::mma_e4m3_ss(tmem + a * T, tc::sdesc_kmajor_sw128(sw + 32 * k), tc::sdesc_kmajor_sw128(sq + 32 * k),
-                                        idesc, k > 0 ? 1u : 0u);
+                    for (int b = 0; b < C::P; ++b) {
+                        if (b > 0 && kb + b >= p.kb) break;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_e4m3_ss(tmem + a * C::kAccCols + b * T, dw0 + at + b * (kBlockW >> 4) + 2 * k,
+                                            dq0 + at + b * (C::kBlockQ >> 4) + 2 * k, idesc, k > 0 ? 1u : 0u);
+                    }
                     tc::commit(&empty[s]);
                     tc::commit(&acc_full[a]);
                 }
                 __syncwarp();
+                ring.next();
+                accs.next();
             }
         }
         if (!ok) fail();
-        tc::fence_before();
-        if (lane == 0) tc::commit(drain);
+        // the same thread as above: commit counts what its thread issued
+        if (elect_one()) {
+            tc::commit(drain);
+            volatile int never = 0;
+            mbar_wait_bounded(drain, 0, &never);
+        }
         __syncwarp();
-        volatile int never = 0;
-        mbar_wait_bounded(drain, 0, &never);
-        __syncwarp();
-    } else if (warp == 2) {
+    } else {
         // ------------------------------------------------ scales
-        // lane: block lane % 8 of the table, tokens lane / 8, + 4, ...
-        long long c = 0;
+        // lane: block lane % 8 of the table, tokens m1, m1 + 8, ...; kBatch of them on their way at once
+        Ring<2> tabs;
         bool ok = true;
         Tile t;
         t.e = e0;
-        const int i = lane & 7, m1 = lane >> 3;
+        constexpr int kBatch = T / 8;
+        const int i = lane & 7, m1 = (lane >> 3) + 4 * (warp - 2);
         for (long long x = x0; ok && x < x1; x = next(x, t)) {
             tile_at(work, x, end_of(x), t);
             const int cols = (t.n + 15) & ~15;
             const float *sw = p.s_w + (static_cast<long long>(t.e) * p.nb + t.w0 / kF8Block) * p.kb;
             const bool two = C::kTables == 2 && t.w0 / kF8Block != (t.w0 + t.rows - 1) / kF8Block;
-            for (int k0 = 0; k0 < p.kb; k0 += kAhead, ++c) {
-                const int s = static_cast<int>(c & 1);
-                if (c >= 2)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait_bounded(&sc_empty[s], static_cast<uint32_t>((c >> 1) - 1) & 1u, abort_flag));
+            for (int k0 = 0; k0 < p.kb; k0 += kAhead) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sc_empty[tabs.s], tabs.phase ^ 1u, abort_flag));
                 if (!ok) {
                     fail();
                     break;
                 }
-                float *table = scales + s * C::kTables * C::kTable + i * C::kScaleLd;
-                const bool in = k0 + i < p.kb;
-                const float f0 = in ? __ldg(sw + k0 + i) : 0.0f, f1 = in && two ? __ldg(sw + p.kb + k0 + i) : 0.0f;
-#pragma unroll 4
-                for (int m = m1; m < cols; m += 4) {
-                    float v = 0.0f;
-                    if (in && m < t.n) {
-                        int r = t.row0 + m;
-                        if (p.src) r = __ldg(p.src + r);
-                        if (static_cast<unsigned>(r) < static_cast<unsigned>(p.q_rows))
-                            v = __ldg(p.s_a + static_cast<long long>(r) * p.kb + k0 + i);
+                float *table = scales + tabs.s * C::kTables * C::kTable + i * C::kScaleLd;
+                const int k = min(k0 + i, p.kb - 1);         // entries beyond the last block are not looked at
+                const float f0 = __ldg(sw + k), f1 = two ? __ldg(sw + p.kb + k) : 0.0f;
+                for (int m0 = m1; m0 < cols; m0 += 8 * kBatch) {
+                    int r[kBatch];
+                    float v[kBatch];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        r[u] = t.row0 + min(m0 + 8 * u, t.n - 1);
+                        if (C::GATHER) r[u] = __ldg(p.src + r[u]);
+                        if (static_cast<unsigned>(r[u]) >= static_cast<unsigned>(p.q_rows)) r[u] = 0;
                     }
-                    table[m] = __fmul_rn(v, f0);
-                    if (two) table[C::kTable + m] = __fmul_rn(v, f1);
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) v[u] = __ldg(p.s_a + static_cast<long long>(r[u]) * p.kb + k);
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        if (m0 + 8 * u < cols) {
+                            const int at = place(m0 + 8 * u);
+                            table[at] = __fmul_rn(v[u], f0);
+                            if (two) table[C::kTable + at] = __fmul_rn(v[u], f1);
+                        }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sc_full[s]);
+                if (lane == 0) mbar_arrive(&sc_full[tabs.s]);
+                tabs.next();
             }
         }
-    } else if (warp >= kEpiWarp0) {
+    }
+    } else if (warp < C::kEpiWarp0) {
+        // ------------------------------------------------ token rows by src: every fourth group of four rows a warp
+        if (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+        Ring<C::kStages> ring;
+        bool ok = true;
+        const uint64_t pol_q = policy_evict_last();
+        Tile t;
+        t.e = e0;
+        for (long long x = x0; ok && x < x1; x = next(x, t)) {
+            tile_at(work, x, end_of(x), t);
+            const int nq = (t.n + 3) >> 2;
+            __syncwarp();                                    // the tile before is read
+            for (int i = lane; i < C::kRows / 4; i += 32) {
+                const int m = 16 * (i >> 2) + 4 * (warp & 3) + (i & 3);
+                const int r = m < t.n ? __ldg(p.src + t.row0 + m) : 0;
+                row_of[m] = static_cast<unsigned>(r) < static_cast<unsigned>(p.q_rows) ? r : 0;
+            }
+            __syncwarp();
+            for (int kb = 0; kb < p.kb; kb += C::P) {
+                const int s = ring.s, nb = min(C::P, p.kb - kb);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ring.phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (elect_one()) {
+                    for (int b = 0; b < nb; ++b) {
+                        uint8_t *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
+                        for (int g = warp & 3; g < nq; g += 4) {
+                            const int4 r = *reinterpret_cast<const int4 *>(row_of + 4 * g);
+                            const int y[4] = {r.x, r.y, r.z, r.w};
+                            tma_gather4(sq + g * 512, &map_q, &full[s], (kb + b) * kF8Block, y, pol_q);
+                        }
+                    }
+                }
+                __syncwarp();
+                ring.next();
+            }
+        }
+    } else {
         // ------------------------------------------------ sums and results
-        const int qd = warp & 3, half = (warp - kEpiWarp0) >> 2;
-        long long j = 0, c = 0;
+        if (C::kWide && C::GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        const int qd = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
+        Ring<C::kAccs> accs;
+        Ring<2> tabs;
         bool ok = true;
         Tile t;
         t.e = e0;
         for (long long x = x0; ok && x < x1; x = next(x, t)) {
             tile_at(work, x, end_of(x), t);
             const int cols = (t.n + 15) & ~15;
-            const int share = C::kHalves == 2 ? (cols / 2 + 15) & ~15 : cols;
-            const int c0 = half * share, nc = min(share, cols - c0);
-            const int mine = 32 * qd + lane;
-            const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * qd) << 16) + c0;
-            const int table = C::kTables == 2 && (t.w0 + mine) / kF8Block != t.w0 / kF8Block && mine < t.rows ? C::kTable : 0;
+            const int share = (cols / C::kParts + 15) & ~15;
+            const int c0 = part * share, nc = max(0, min(share, cols - c0));
+            // the table of rows 32 qd + 16 h on (16 rows lie in one block of the weights)
+            int table[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 32 * qd + 16 * h;
+                table[h] = C::kTables == 2 && r < t.rows && (t.w0 + r) / kF8Block != t.w0 / kF8Block ? C::kTable : 0;
+            }
             f2 acc[C::kCols / 2];
+            const float *sc = scales + c0 + 4 * (lane & 3);
+            const uint32_t from = tmem + (static_cast<uint32_t>(32 * qd) << 16) + c0;
+            ok = sum_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p.kb, sc, table, from, acc_full, acc_empty, sc_full, sc_empty, accs, tabs,
+                                           abort_flag);
+            if (!ok) {
+                fail();
+                break;
+            }
+            // 8 tokens at a time, transposed: token lane / 4, weight rows 8 i + 2 (lane % 4) and the one after it
 #pragma unroll
-            for (int g = 0; g < C::kCols / 2; ++g) acc[g] = 0;
-            for (int kb = 0; kb < p.kb; ++kb, ++j) {
-                const int a = static_cast<int>(j % C::kAccs), s = static_cast<int>(c & 1);
-                if (kb % kAhead == 0)
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sc_full[s], static_cast<uint32_t>(c >> 1) & 1u, abort_flag));
-                // warp-uniform: the TMEM loads below are warp-collective
-                if (ok)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait_bounded(&acc_full[a], static_cast<uint32_t>(j / C::kAccs) & 1u, abort_flag));
-                if (!ok) {
-                    fail();
-                    break;
-                }
-                tc::fence_after();
-                const float *sc = scales + s * C::kTables * C::kTable + table + (kb % kAhead) * C::kScaleLd + c0;
+            for (int g = 0; g < C::kCols / 8; ++g) {
+                if (8 * g < nc) {
+                    const int m = c0 + 8 * g + (lane >> 2), r = 32 * qd + 2 * (lane & 3);
+                    const bool there = m < t.n;
+                    const bool zero = C::GATHER && there && static_cast<unsigned>(__ldg(p.src + t.row0 + m)) >= static_cast<unsigned>(p.q_rows);
+                    uint16_t *y = p.y + static_cast<long long>(t.row0 + m) * p.N + t.w0 + r;
+                    uint32_t w[4];
 #pragma unroll
-                for (int g = 0; g < C::kCols / 16; ++g) {
-                    if (16 * g < nc) {
-                        uint32_t d[16];
-                        tc::ld16(lane_addr + a * T + 16 * g, d);
-                        float4 f[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float4 *>(sc + 16 * g + 4 * i);
-                        tc::wait_ld();
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = upk(acc[4 * g + i]);
+                        const __nv_bfloat162 o = __floats2bfloat162_rn(v.x, v.y);
+                        w[i] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&o));
+                    }
+                    if (there) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            acc[8 * g + 2 * i] = fma2(pk(__uint_as_float(d[4 * i]), __uint_as_float(d[4 * i + 1])),
-                                                      pk(f[i].x, f[i].y), acc[8 * g + 2 * i]);
-                            acc[8 * g + 2 * i + 1] = fma2(pk(__uint_as_float(d[4 * i + 2]), __uint_as_float(d[4 * i + 3])),
-                                                          pk(f[i].z, f[i].w), acc[8 * g + 2 * i + 1]);
+                            if (zero) w[i] = 0;
+                            if (p.pairs && r + 8 * i + 1 < t.rows) {
+                                *reinterpret_cast<uint32_t *>(y + 8 * i) = w[i];
+                            } else {
+                                if (r + 8 * i < t.rows) y[8 * i] = static_cast<uint16_t>(w[i]);
+                                if (r + 8 * i + 1 < t.rows) y[8 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+                            }
                         }
-                    }
-                }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[a]);
-                if (kb % kAhead == kAhead - 1 || kb == p.kb - 1) {
-                    if (lane == 0) mbar_arrive(&sc_empty[s]);
-                    ++c;
-                }
-            }
-            if (!ok) break;
-            if (mine < t.rows) {
-                const int n = min(nc, t.n - c0);
-                uint16_t *y = p.y + static_cast<long long>(t.row0 + c0) * p.N + t.w0 + mine;
-#pragma unroll
-                for (int g = 0; g < C::kCols; ++g) {
-                    if (g < n) {
-                        const float2 v = upk(acc[g / 2]);
-                        float o = (g & 1) ? v.y : v.x;
-                        // a row that src sends nowhere
-                        if (p.src && static_cast<unsigned>(__ldg(p.src + t.row0 + c0 + g)) >= static_cast<unsigned>(p.q_rows)) o = 0.0f;
-                        y[static_cast<long long>(g) * p.N] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
                     }
                 }
             }
         }
     }
     __syncwarp();
+    if (*abort_flag) {
+        // copies that were issued around the failure land within this time
+        const unsigned long long t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 100000ull) {}
+    }
     tc::fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -452,13 +589,12 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     }
 }
 
-template <int T>
+template <class C>
 cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
 {
-    using C = Cfg<T>;
-    const size_t smem = smem_bytes<T>(a.E);
+    const size_t smem = smem_bytes<C>(a.E);
     // a few hundred ns of host time, and right on every device
-    cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     Params p;
     p.s_a = a.s_a;
@@ -474,6 +610,8 @@ cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
     p.kb = f8_blocks(a.K);
     p.nb = f8_blocks(a.N);
     p.cols = a.plan.cols;
+    p.box = a.box;
+    p.pairs = a.N % 2 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 3u) == 0 ? 1 : 0;
     p.status = a.status;
     p.pdl = pdl ? 1 : 0;
     // units at most: each expert's last token tile may be a part of one
@@ -489,7 +627,7 @@ cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, linear_f8_kernel<T>, a.map_w, a.map_w16, a.map_q, p);
+    return cudaLaunchKernelEx(&cfg, linear_f8_kernel<C>, a.map_w, a.map_w16, a.map_q, p);
 }
 
 }  // namespace
@@ -502,29 +640,35 @@ F8Plan f8_plan(int rows, int experts, int N, int sms)
     for (int T = 16; T <= 64; T *= 2)
         if (need <= T) return {T, T};
     const long long tall = (N + kTileRows - 1) / kTileRows;
-    if (mean <= 128 || busy * tall * ((mean + 255) / 256) < sms) return {128, 128};
-    if (experts > 1) return {256, 256};
+    if (mean <= 128 || busy * tall * ((mean + 191) / 192) < sms) return {128, 128};
+    if (experts > 1) return {192, 192};
     // fewest tensor cycles: waves of tiles, each as long as its columns
-    int best = 256;
+    int best = 192;
     long long least = 1LL << 62;
-    for (int cols = 256; cols >= 144; cols -= 16) {
+    for (int cols = 192; cols > 128; cols -= 16) {
         const long long tiles = tall * ((rows + cols - 1) / cols), cost = (tiles + sms - 1) / sms * cols;
         if (cost < least) {
             least = cost;
             best = cols;
         }
     }
-    return {256, best};
+    return {192, best};
+}
+
+template <int T>
+static cudaError_t launch_any(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
+{
+    return a.src ? launch<Cfg<T, true>>(a, pdl, stream) : launch<Cfg<T, false>>(a, pdl, stream);
 }
 
 cudaError_t launch_linear_f8(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
 {
     switch (a.plan.T) {
-    case 16: return launch<16>(a, pdl, stream);
-    case 32: return launch<32>(a, pdl, stream);
-    case 64: return launch<64>(a, pdl, stream);
-    case 128: return launch<128>(a, pdl, stream);
-    default: return launch<256>(a, pdl, stream);
+    case 16: return launch_any<16>(a, pdl, stream);
+    case 32: return launch_any<32>(a, pdl, stream);
+    case 64: return launch_any<64>(a, pdl, stream);
+    case 128: return launch_any<128>(a, pdl, stream);
+    default: return launch_any<192>(a, pdl, stream);
     }
 }
 

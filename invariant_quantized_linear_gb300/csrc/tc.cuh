@@ -125,6 +125,17 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr));
 }
 
+// 16 consecutive columns of 16 lanes (the warp's lower 16 or, with 16 added to the
+// address's lane, its upper 16) as tensor-core fragments: thread i gets, for the
+// column groups j = 0, 1 of 8, lane i / 4 in r[4 j], r[4 j + 1] and lane i / 4 + 8 in
+// r[4 j + 2], r[4 j + 3], both of columns 8 j + 2 (i % 4) and the one after it.
+__device__ __forceinline__ void ld16_frag(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32])
 {
     asm volatile(
