@@ -100,9 +100,9 @@ bi_status linear(const uint8_t *q, const float *s_a, int q_rows, int K, const in
     bi_status st = device_info(&a.sms);
     if (st != BI_OK) return st;
     a.plan = bi::f8_plan(R, E, N, a.sms);
-    // one copy for a tile's tokens, or pieces of at most 64 where tiles differ
+    // rows of the copy of a tile's tokens: with one expert all tiles but the last have as many
     const int tiles = (R + a.plan.cols - 1) / a.plan.cols;
-    a.box = !offsets ? ((R + tiles - 1) / tiles + 15) / 16 * 16 : a.plan.T < 64 ? a.plan.T : 64;
+    a.box = !offsets ? ((R + tiles - 1) / tiles + 15) / 16 * 16 : a.plan.T;
     const long long w_rows = static_cast<long long>(E) * N;
     st = encode(&a.map_w, w, w_rows, K, 128, true);
     if (st == BI_OK) st = encode(&a.map_w16, w, w_rows, K, 16, true);

@@ -21,11 +21,12 @@
 //
 // Tiles.  Expert e with n_e rows has ceil(n_e / cols) token tiles.  Calls that
 // are bound by the weight stream cut the weight rows into units of 16, order the
-// units by expert, 128-row chunk, token tile and row, and give each CTA an equal
-// run of them: every SM streams the same bytes, whatever N is, and a chunk's
-// token tiles follow one another on one SM.  Calls that are bound by the tensor
-// cores have units of 128 rows, dealt in turn, so that CTAs that run together
-// share weight and token tiles in L2.
+// units by expert, token tile and row, and give each CTA an equal run of them, in
+// tiles of up to 128 rows that are about as high as one another: every SM streams
+// the same bytes, whatever N is, and no tile is so low that its MMAs (350 cycles a
+// block, however few its rows) take longer than its bytes.  Calls that are bound
+// by the tensor cores have units of 128 rows, dealt in turn, so that CTAs that run
+// together share weight and token tiles in L2.
 //
 // Every wait is bounded: a role that gives up sets the status word and all
 // return; copies in flight are waited for and TMEM is freed.
@@ -76,7 +77,7 @@ struct Params {
     const int32_t *src, *offsets;
     uint16_t *y;
     int q_rows, R, E, N, K, kb, nb, cols;
-    int box;           // token rows of a copy, where src is null
+    int box;           // token rows of a tile's copy, where src is null
     int pairs;         // two results may be stored together
     int *status;
     int pdl;
@@ -89,6 +90,11 @@ size_t smem_bytes(int E)
 {
     return 1024 + C::kStages * C::kStage + (C::kScales + C::kRows) * 4 + kBarBytes + 8 * (E + 1) + 4 * (E + 1);
 }
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
 
 // Position in a ring of N buffers: a consumer waits for parity `phase`, a producer for the other.
 template <int N>
@@ -140,7 +146,7 @@ __device__ __forceinline__ int expert_of(const Work &w, long long x)
 // A value that all lanes have, known to be one: what is derived from it may stay in
 // uniform registers.  Without this, every copy, MMA and TMEM load is issued by a loop
 // over the distinct values its operands might have (300 cycles a copy for 31).
-__device__ __forceinline__ int same(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int same(int v) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(v))); }
 
 __device__ __forceinline__ long long same(long long v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -151,14 +157,21 @@ __device__ __forceinline__ void tile_at(const Work &w, long long x, long long en
     t.e = same(t.e);
     const int n_e = w.row[t.e + 1] - w.row[t.e];
     const int tt = (n_e + w.cols - 1) / w.cols, nu = (w.N + w.unit - 1) / w.unit, per = kTileRows / w.unit;
-    const long long off = x - w.first[t.e];
-    const int chunk = static_cast<int>(off / (per * tt));
-    const int rem = static_cast<int>(off - static_cast<long long>(chunk) * per * tt);
-    const int run = min(per, nu - chunk * per);
-    const int ti = rem / run, u = rem - ti * run;
-    const long long left = end - x;
-    t.len = same(left < run - u ? static_cast<int>(left) : run - u);
-    t.w0 = same((chunk * per + u) * w.unit);
+    const int off = static_cast<int>(x - w.first[t.e]);
+    int ti, u, run;
+    if (per == 1) {
+        u = off / tt;                                // a weight tile's token tiles side by side
+        ti = off - u * tt;
+        run = 1;
+    } else {
+        ti = off / nu;
+        u = off - ti * nu;
+        const long long left = end - x;
+        run = left < nu - u ? static_cast<int>(left) : nu - u;   // units up to the end of the rows or of the CTA's share,
+        run = (run + (run + per - 1) / per - 1) / ((run + per - 1) / per);   // in tiles that are about as high
+    }
+    t.len = same(run);
+    t.w0 = same(u * w.unit);
     t.rows = min(t.len * w.unit, w.N - t.w0);
     const int c = ((n_e + tt - 1) / tt + 15) & ~15;            // tokens of a tile, spread evenly
     t.row0 = same(w.row[t.e] + ti * c);
@@ -176,51 +189,63 @@ __device__ __forceinline__ bool sum_blocks(f2 *acc, int blocks, const float *sca
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int g = 0; g < 8 * NG; ++g) acc[g] = 0;
-    for (int kb = 0; kb < blocks; kb += C::P) {
+    bool ready = false;                              // the next accumulator has been seen to be full
+    // NB blocks of an accumulator, whose scales start at sc
+    auto unit = [&](auto nb, const float *sc) {
+        constexpr int NB = decltype(nb)::value;
         const int a = accs.s;
         // warp-uniform: the TMEM loads below are warp-collective
-        if (!__all_sync(0xffffffffu, (kb % kAhead != 0 || mbar_wait_bounded(&sc_full[tabs.s], tabs.phase, abort_flag)) &&
-                                         mbar_wait_bounded(&acc_full[a], accs.phase, abort_flag)))
-            return false;
-        tc::fence_after();
-#pragma unroll
-        for (int q = 0; q < C::P; ++q) {
-            if (q > 0 && kb + q >= blocks) break;
-            const float *sc = scales + tabs.s * C::kTables * C::kTable + (kb % kAhead + q) * C::kScaleLd;
-            // 16 columns are on their way from TMEM while the 16 before them are added
-            uint32_t d[2][16];
-            const uint32_t at = from + a * C::kAccCols + q * C::T;
-            auto fetch = [&](int g) {
-                tc::ld16_frag(at + 16 * g, d[g & 1]);
-                tc::ld16_frag(at + 16 * g + (16u << 16), d[g & 1] + 8);
-            };
-            if (NG > 0) fetch(0);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float4 lo = *reinterpret_cast<const float4 *>(sc + table[0] + 16 * g);
-                const float4 hi = C::kTables == 2 ? *reinterpret_cast<const float4 *>(sc + table[1] + 16 * g) : lo;
-                tc::wait_ld();
-                if (g + 1 < NG) fetch(g + 1);
-                const uint32_t(&v)[16] = d[g & 1];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 &f = i < 2 ? lo : hi;
-                        const int r = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
-                        f2 &s = acc[8 * g + 4 * j + i];
-                        s = fma2(pk(__uint_as_float(v[r]), __uint_as_float(v[r + 1])), j ? pk(f.z, f.w) : pk(f.x, f.y), s);
-                    }
-            }
-        }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[a]);
+        if (!__all_sync(0xffffffffu, ready || mbar_wait_short(&acc_full[a], accs.phase, abort_flag))) return false;
         accs.next();
-        if (kb % kAhead == kAhead - C::P || kb + C::P >= blocks) {
-            if (lane == 0) mbar_arrive(&sc_empty[tabs.s]);
-            tabs.next();
+        tc::fence_after();
+        // 16 columns are on their way from TMEM while the 16 before them are added
+        uint32_t d[2][16];
+        auto fetch = [&](int i) {
+            const uint32_t at = from + a * C::kAccCols + i / (NG > 0 ? NG : 1) * C::T + 16 * (i % (NG > 0 ? NG : 1));
+            tc::ld16_frag(at, d[i & 1]);
+            tc::ld16_frag(at + (16u << 16), d[i & 1] + 8);
+        };
+        if (NG > 0) fetch(0);
+#pragma unroll
+        for (int u = 0; u < NG * NB; ++u) {
+            const int g = u % (NG > 0 ? NG : 1);
+            const float *f0 = sc + u / (NG > 0 ? NG : 1) * C::kScaleLd + 16 * g;
+            const float4 lo = *reinterpret_cast<const float4 *>(f0 + table[0]);
+            const float4 hi = C::kTables == 2 ? *reinterpret_cast<const float4 *>(f0 + table[1]) : lo;
+            tc::wait_ld();
+            if (u + 1 < NG * NB) {
+                fetch(u + 1);
+            } else {
+                // the accumulator is in registers: the next one is looked at while it is added
+                tc::fence_before();
+                if (lane == 0) mbar_arrive(&acc_empty[a]);
+                ready = mbar_test_wait(&acc_full[accs.s], accs.phase);
+            }
+            const uint32_t(&v)[16] = d[u & 1];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 &f = i < 2 ? lo : hi;
+                    const int r = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
+                    f2 &s = acc[8 * g + 4 * j + i];
+                    s = fma2(pk(__uint_as_float(v[r]), __uint_as_float(v[r + 1])), j ? pk(f.z, f.w) : pk(f.x, f.y), s);
+                }
         }
+        if (NG == 0 && lane == 0) mbar_arrive(&acc_empty[a]);
+        return true;
+    };
+    for (int k0 = 0; k0 < blocks; k0 += kAhead) {
+        if (!__all_sync(0xffffffffu, mbar_wait_short(&sc_full[tabs.s], tabs.phase, abort_flag))) return false;
+        const float *sc = scales + tabs.s * C::kTables * C::kTable;
+        const int n = min(kAhead, blocks - k0);
+        int i = 0;
+        for (; i + C::P <= n; i += C::P)
+            if (!unit(Int<C::P>(), sc + i * C::kScaleLd)) return false;
+        if (i < n && !unit(Int<1>(), sc + i * C::kScaleLd)) return false;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[tabs.s]);
+        tabs.next();
     }
     return true;
 }
@@ -352,40 +377,65 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         t.e = e0;
         for (long long x = x0; ok && x < x1; x = next(x, t)) {
             tile_at(work, x, end_of(x), t);
-            const bool whole = t.rows > 112;
-            const int nw = whole ? 1 : (t.rows + 15) >> 4;
-            const int nq = C::GATHER ? (t.n + 3) >> 2 : (t.n + p.box - 1) / p.box;
             const int wy = t.e * p.N + t.w0;
-            const uint32_t bytes = (nw * (whole ? 128 : 16) + nq * (C::GATHER ? 4 : p.box)) * kF8Block;
-            for (int kb = 0; kb < p.kb; kb += C::P) {
-                const int s = ring.s, nb = min(C::P, p.kb - kb);
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ring.phase ^ 1u, abort_flag));
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&full[s], bytes * nb);
+            const uint32_t bytes_q = C::GATHER ? ((t.n + 3) >> 2) * 4 * kF8Block : p.box * kF8Block;
+            // NW copies of 16 weight rows, or (8) one of 128; no branch but the waits'
+            auto stages = [&](auto nw) {
+                constexpr int NW = decltype(nw)::value;
+                const uint32_t bytes = NW * 16 * kF8Block + bytes_q;
+                auto copy = [&](int s, int b, int k) {
+                    uint8_t *sw = smem + s * C::kStage + b * kBlockW, *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
+                    if constexpr (NW == 8) {
+                        tma_load_2d(sw, &map_w, &full[s], k, wy, pol_w);
+                    } else {
 #pragma unroll
-                    for (int b = 0; b < C::P; ++b) {
-                        if (b >= nb) break;
-                        uint8_t *sw = smem + s * C::kStage + b * kBlockW, *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
-                        const int k = (kb + b) * kF8Block;
-                        if (whole) tma_load_2d(sw, &map_w, &full[s], k, wy, pol_w);
-                        else
-                            for (int i = 0; i < nw; ++i) tma_load_2d(sw + i * 2048, &map_w16, &full[s], k, wy + i * 16, pol_w);
-                        if (!C::GATHER)
-                            for (int i = 0; i < nq; ++i)
-                                tma_load_2d(sq + i * p.box * kF8Block, &map_q, &full[s], k, t.row0 + i * p.box, pol_q);
+                        for (int i = 0; i < NW; ++i) tma_load_2d(sw + i * 2048, &map_w16, &full[s], k, wy + i * 16, pol_w);
                     }
+                    if constexpr (!C::GATHER) tma_load_2d(sq, &map_q, &full[s], k, t.row0, pol_q);
+                };
+                int kb = 0;
+                for (; kb + C::P <= p.kb; kb += C::P) {
+                    const int s = ring.s;
+                    ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[s], ring.phase ^ 1u, abort_flag));
+                    if (!ok) return;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&full[s], bytes * C::P);
+#pragma unroll
+                        for (int b = 0; b < C::P; ++b) copy(s, b, (kb + b) * kF8Block);
+                    }
+                    __syncwarp();
+                    ring.next();
+                    wrapped |= ring.s == 0;
                 }
-                __syncwarp();
-                ring.next();
-                wrapped |= ring.s == 0;
+                if (kb < p.kb) {                             // the last block of an odd number
+                    const int s = ring.s;
+                    ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[s], ring.phase ^ 1u, abort_flag));
+                    if (!ok) return;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&full[s], bytes);
+                        copy(s, 0, kb * kF8Block);
+                    }
+                    __syncwarp();
+                    ring.next();
+                    wrapped |= ring.s == 0;
+                }
+            };
+            switch (t.rows > 112 ? 8 : (t.rows + 15) >> 4) {
+            case 1: stages(Int<1>()); break;
+            case 2: stages(Int<2>()); break;
+            case 3: stages(Int<3>()); break;
+            case 4: stages(Int<4>()); break;
+            case 5: stages(Int<5>()); break;
+            case 6: stages(Int<6>()); break;
+            case 7: stages(Int<7>()); break;
+            default: stages(Int<8>());
             }
         }
         if (!ok) fail();
         // every copy that was issued lands before the CTA can exit
         volatile int never = 0;
         for (int s = 0; ok && s < C::kStages; ++s)
-            if (s < ring.s || wrapped) mbar_wait_bounded(&full[s], s < ring.s ? ring.phase : ring.phase ^ 1u, &never);
+            if (s < ring.s || wrapped) mbar_wait_short(&full[s], s < ring.s ? ring.phase : ring.phase ^ 1u, &never);
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs
         Ring<C::kStages> ring;
@@ -398,29 +448,32 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             tile_at(work, x, end_of(x), t);
             // rows of the stage beyond the tile's hold old bytes: their sums are never looked at
             const uint32_t idesc = tc::idesc_e4m3_f32(kTileRows, (t.n + 15) & ~15);
-            for (int kb = 0; kb < p.kb; kb += C::P) {
+            auto block = [&](int s, int a, int b) {
+                const uint64_t at = static_cast<uint32_t>(s * (C::kStage >> 4));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_e4m3_ss(tmem + a * C::kAccCols + b * T, dw0 + at + b * (kBlockW >> 4) + 2 * k,
+                                    dq0 + at + b * (C::kBlockQ >> 4) + 2 * k, idesc, k > 0 ? 1u : 0u);
+            };
+            auto stage = [&](auto nb) {
                 const int a = accs.s, s = ring.s;
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[a], accs.phase ^ 1u, abort_flag) &&
-                                                 mbar_wait_bounded(&full[s], ring.phase, abort_flag));
-                if (!ok) break;
+                ok = __all_sync(0xffffffffu, mbar_wait_short(&acc_empty[a], accs.phase ^ 1u, abort_flag) &&
+                                                 mbar_wait_short(&full[s], ring.phase, abort_flag));
+                if (!ok) return;
                 tc::fence_after();
                 if (elect_one()) {
-                    const uint64_t at = static_cast<uint32_t>(s * (C::kStage >> 4));
 #pragma unroll
-                    for (int b = 0; b < C::P; ++b) {
-                        if (b > 0 && kb + b >= p.kb) break;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma_e4m3_ss(tmem + a * C::kAccCols + b * T, dw0 + at + b * (kBlockW >> 4) + 2 * k,
-                                            dq0 + at + b * (C::kBlockQ >> 4) + 2 * k, idesc, k > 0 ? 1u : 0u);
-                    }
+                    for (int b = 0; b < decltype(nb)::value; ++b) block(s, a, b);
                     tc::commit(&empty[s]);
                     tc::commit(&acc_full[a]);
                 }
                 __syncwarp();
                 ring.next();
                 accs.next();
-            }
+            };
+            int kb = 0;
+            for (; ok && kb + C::P <= p.kb; kb += C::P) stage(Int<C::P>());
+            if (ok && kb < p.kb) stage(Int<1>());
         }
         if (!ok) fail();
         // the same thread as above: commit counts what its thread issued
@@ -445,7 +498,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const float *sw = p.s_w + (static_cast<long long>(t.e) * p.nb + t.w0 / kF8Block) * p.kb;
             const bool two = C::kTables == 2 && t.w0 / kF8Block != (t.w0 + t.rows - 1) / kF8Block;
             for (int k0 = 0; k0 < p.kb; k0 += kAhead) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sc_empty[tabs.s], tabs.phase ^ 1u, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait_short(&sc_empty[tabs.s], tabs.phase ^ 1u, abort_flag));
                 if (!ok) {
                     fail();
                     break;
@@ -498,7 +551,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             __syncwarp();
             for (int kb = 0; kb < p.kb; kb += C::P) {
                 const int s = ring.s, nb = min(C::P, p.kb - kb);
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ring.phase ^ 1u, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[s], ring.phase ^ 1u, abort_flag));
                 if (!ok) break;
                 if (elect_one()) {
                     for (int b = 0; b < nb; ++b) {

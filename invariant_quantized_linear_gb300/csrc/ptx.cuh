@@ -112,6 +112,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// The same with the first look at the timer after 64 attempts: for waits that last
+// hundreds of cycles, where that look would itself be the longest part.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    for (int it = 0; it < 64; ++it)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, abort);
+}
+
 // ------------------------------------------------------------------ TMA
 
 // L2 cache policy: evict-first, for data that is streamed exactly once.
