@@ -78,7 +78,7 @@ struct Params {
     uint16_t *y;
     int q_rows, R, E, N, K, kb, nb, cols;
     int box;           // token rows of a tile's copy, where src is null
-    int pairs;         // two results may be stored together
+    int vec;           // eight results may be stored together
     int *status;
     int pdl;
 };
@@ -258,6 +258,58 @@ __device__ __forceinline__ bool sum_any(int groups, Rest &&...rest)
         if (groups < NG) return sum_any<C, NG - 1>(groups, rest...);
     }
     return sum_blocks<C, NG>(rest...);
+}
+
+// Stores 16 NG columns (tokens from c0 on) of the weight rows r0 .. r0 + 31 of a tile.  Eight tokens at a time are
+// transposed: lane i then has token i / 4 and the weight rows 8 j + 2 (i % 4), + 1 in word j; where rows of y allow it,
+// the four lanes of a token exchange words so that each stores 16 bytes (64 side by side a token).
+template <class C, int NG>
+__device__ __forceinline__ void store_tile(const f2 *acc, const Params &p, const Tile &t, int c0, int r0)
+{
+    const int lane = threadIdx.x & 31, quad = lane & 3;
+    const bool wide = p.vec && r0 + 32 <= t.rows;
+    uint16_t *y = p.y + static_cast<long long>(t.row0 + c0 + (lane >> 2)) * p.N + t.w0 + r0;
+#pragma unroll
+    for (int g = 0; g < 2 * NG; ++g, y += 8 * static_cast<long long>(p.N)) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = upk(acc[4 * g + i]);
+            const __nv_bfloat162 o = __floats2bfloat162_rn(v.x, v.y);
+            w[i] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&o));
+        }
+        const int m = c0 + 8 * g + (lane >> 2);
+        const bool there = m < t.n;
+        if (C::GATHER) {                             // a row that src sends nowhere
+            const int r = __ldg(p.src + t.row0 + min(m, t.n - 1));
+            if (static_cast<unsigned>(r) >= static_cast<unsigned>(p.q_rows)) w[0] = w[1] = w[2] = w[3] = 0;
+        }
+        if (wide) {
+            // words 4 x 4 of the quad, transposed: pairs of lanes exchange pairs of words, then single ones
+            const bool b1 = quad & 1, b2 = quad & 2;
+            const uint32_t s0 = __shfl_xor_sync(0xffffffffu, b2 ? w[0] : w[2], 2), s1 = __shfl_xor_sync(0xffffffffu, b2 ? w[1] : w[3], 2);
+            const uint32_t a0 = b2 ? s0 : w[0], a1 = b2 ? s1 : w[1], a2 = b2 ? w[2] : s0, a3 = b2 ? w[3] : s1;
+            const uint32_t x0 = __shfl_xor_sync(0xffffffffu, b1 ? a0 : a1, 1), x1 = __shfl_xor_sync(0xffffffffu, b1 ? a2 : a3, 1);
+            const uint4 o = make_uint4(b1 ? x0 : a0, b1 ? a1 : x0, b1 ? x1 : a2, b1 ? a3 : x1);
+            if (there) *reinterpret_cast<uint4 *>(y + 8 * quad) = o;
+        } else if (there) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = 8 * i + 2 * quad;
+                if (r0 + n < t.rows) y[n] = static_cast<uint16_t>(w[i]);
+                if (r0 + n + 1 < t.rows) y[n + 1] = static_cast<uint16_t>(w[i] >> 16);
+            }
+        }
+    }
+}
+
+template <class C, int NG, typename... Rest>
+__device__ __forceinline__ void store_any(int groups, const Rest &...rest)
+{
+    if constexpr (NG > 0) {
+        if (groups < NG) return store_any<C, NG - 1>(groups, rest...);
+        store_tile<C, NG>(rest...);
+    }
 }
 
 template <class C>
@@ -597,35 +649,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 fail();
                 break;
             }
-            // 8 tokens at a time, transposed: token lane / 4, weight rows 8 i + 2 (lane % 4) and the one after it
-#pragma unroll
-            for (int g = 0; g < C::kCols / 8; ++g) {
-                if (8 * g < nc) {
-                    const int m = c0 + 8 * g + (lane >> 2), r = 32 * qd + 2 * (lane & 3);
-                    const bool there = m < t.n;
-                    const bool zero = C::GATHER && there && static_cast<unsigned>(__ldg(p.src + t.row0 + m)) >= static_cast<unsigned>(p.q_rows);
-                    uint16_t *y = p.y + static_cast<long long>(t.row0 + m) * p.N + t.w0 + r;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 v = upk(acc[4 * g + i]);
-                        const __nv_bfloat162 o = __floats2bfloat162_rn(v.x, v.y);
-                        w[i] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&o));
-                    }
-                    if (there) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (zero) w[i] = 0;
-                            if (p.pairs && r + 8 * i + 1 < t.rows) {
-                                *reinterpret_cast<uint32_t *>(y + 8 * i) = w[i];
-                            } else {
-                                if (r + 8 * i < t.rows) y[8 * i] = static_cast<uint16_t>(w[i]);
-                                if (r + 8 * i + 1 < t.rows) y[8 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
-                            }
-                        }
-                    }
-                }
-            }
+            store_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p, t, c0, 32 * qd);
         }
     }
     __syncwarp();
@@ -664,7 +688,7 @@ cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
     p.nb = f8_blocks(a.N);
     p.cols = a.plan.cols;
     p.box = a.box;
-    p.pairs = a.N % 2 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 3u) == 0 ? 1 : 0;
+    p.vec = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 ? 1 : 0;
     p.status = a.status;
     p.pdl = pdl ? 1 : 0;
     // units at most: each expert's last token tile may be a part of one
