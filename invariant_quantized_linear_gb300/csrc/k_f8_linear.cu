@@ -179,16 +179,16 @@ __device__ __forceinline__ void tile_at(const Work &w, long long x, long long en
 }
 
 // Adds the blocks of a tile, 16 NG columns of 32 rows, into acc: columns 8 j + 2 (lane % 4), + 1 of row lane / 4 + 8 i
-// are in acc[4 j + i].  NG is a constant because a branch around each group's TMEM loads would order them one behind
+// are in acc[8 j + 2 i], + 1.  NG is a constant because a branch around each group's TMEM loads would order them one behind
 // the other (a block of 96 columns took 1,850 cycles, 560 without).  table[h]: where the scales of rows 16 h on are.
 template <class C, int NG>
-__device__ __forceinline__ bool sum_blocks(f2 *acc, int blocks, const float *scales, const int (&table)[2], uint32_t from,
+__device__ __forceinline__ bool sum_blocks(float *acc, int blocks, const float *scales, const int (&table)[2], uint32_t from,
                                            uint64_t *acc_full, uint64_t *acc_empty, uint64_t *sc_full, uint64_t *sc_empty,
                                            Ring<C::kAccs> &accs, Ring<2> &tabs, volatile int *abort_flag)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int g = 0; g < 8 * NG; ++g) acc[g] = 0;
+    for (int g = 0; g < 16 * NG; ++g) acc[g] = 0.0f;
     bool ready = false;                              // the next accumulator has been seen to be full
     // NB blocks of an accumulator, whose scales start at sc
     auto unit = [&](auto nb, const float *sc) {
@@ -228,8 +228,9 @@ __device__ __forceinline__ bool sum_blocks(f2 *acc, int blocks, const float *sca
                 for (int i = 0; i < 4; ++i) {
                     const float4 &f = i < 2 ? lo : hi;
                     const int r = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
-                    f2 &s = acc[8 * g + 4 * j + i];
-                    s = fma2(pk(__uint_as_float(v[r]), __uint_as_float(v[r + 1])), j ? pk(f.z, f.w) : pk(f.x, f.y), s);
+                    float *s = acc + 2 * (8 * g + 4 * j + i);
+                    s[0] = __fmaf_rn(__uint_as_float(v[r]), j ? f.z : f.x, s[0]);
+                    s[1] = __fmaf_rn(__uint_as_float(v[r + 1]), j ? f.w : f.y, s[1]);
                 }
         }
         if (NG == 0 && lane == 0) mbar_arrive(&acc_empty[a]);
@@ -264,7 +265,7 @@ __device__ __forceinline__ bool sum_any(int groups, Rest &&...rest)
 // transposed: lane i then has token i / 4 and the weight rows 8 j + 2 (i % 4), + 1 in word j; where rows of y allow it,
 // the four lanes of a token exchange words so that each stores 16 bytes (64 side by side a token).
 template <class C, int NG>
-__device__ __forceinline__ void store_tile(const f2 *acc, const Params &p, const Tile &t, int c0, int r0)
+__device__ __forceinline__ void store_tile(const float *acc, const Params &p, const Tile &t, int c0, int r0)
 {
     const int lane = threadIdx.x & 31, quad = lane & 3;
     const bool wide = p.vec && r0 + 32 <= t.rows;
@@ -274,8 +275,7 @@ __device__ __forceinline__ void store_tile(const f2 *acc, const Params &p, const
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 v = upk(acc[4 * g + i]);
-            const __nv_bfloat162 o = __floats2bfloat162_rn(v.x, v.y);
+            const __nv_bfloat162 o = __floats2bfloat162_rn(acc[8 * g + 2 * i], acc[8 * g + 2 * i + 1]);
             w[i] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&o));
         }
         const int m = c0 + 8 * g + (lane >> 2);
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 const int r = 32 * qd + 16 * h;
                 table[h] = C::kTables == 2 && r < t.rows && (t.w0 + r) / kF8Block != t.w0 / kF8Block ? C::kTable : 0;
             }
-            f2 acc[C::kCols / 2];
+            float acc[C::kCols];
             const float *sc = scales + c0 + 4 * (lane & 3);
             const uint32_t from = tmem + (static_cast<uint32_t>(32 * qd) << 16) + c0;
             ok = sum_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p.kb, sc, table, from, acc_full, acc_empty, sc_full, sc_empty, accs, tabs,
