@@ -106,8 +106,9 @@ bi_status linear(const uint8_t *q, const float *s_a, int q_rows, int K, const in
     const long long w_rows = static_cast<long long>(E) * N;
     st = encode(&a.map_w, w, w_rows, K, 128, true);
     if (st == BI_OK) st = encode(&a.map_w16, w, w_rows, K, 16, true);
-    if (st == BI_OK) st = encode(&a.map_q, q, q_rows, K, src ? 1 : a.box, false);
+    if (st == BI_OK && !src) st = encode(&a.map_q, q, q_rows, K, a.box, false);
     if (st != BI_OK) return st;
+    a.q = q;
     a.s_a = s_a;
     a.s_w = s_w;
     a.src = src;

@@ -41,8 +41,9 @@ F8Plan f8_plan(int rows, int experts, int N, int sms);
 struct F8LinearArgs {
     CUtensorMap map_w;          // w [E N, K], box 128 B x 128 rows
     CUtensorMap map_w16;        // the same, 16 rows
-    CUtensorMap map_q;          // q [rows of q, K], box 128 B x `box` rows, or x 1 row where src is given
+    CUtensorMap map_q;          // q [rows of q, K], box 128 B x `box` rows; not set where src is given
     int box;
+    const uint8_t *q;
     const float *s_a, *s_w;
     const int32_t *src;         // row of q for each row of y, or null: the same row
     const int32_t *offsets;     // [E + 1] rows of each expert, or null: one weight matrix, all rows

@@ -12,12 +12,12 @@
 // rows and tokens alone.
 //
 // Roles of a CTA (one a SM, persistent):
-//   warp 0     copies weight and token tiles into a ring, one block of K a stage;
-//              token rows that src names are gathered four at a time;
+//   warp 0     copies weight and token tiles into a ring, one or two blocks of K a stage;
 //   warp 1     allocates TMEM, issues the MMAs, a block an accumulator;
 //   warps 2-3  multiply the scales of 8 blocks ahead into a table;
-//   warps 4 on a weight row a thread (TMEM lane), up to 128 tokens: take each
-//              accumulator out of TMEM into the fp32 sums, then store.
+//   warps 4-7  where src names the token rows: fetch them;
+//   the others take each accumulator out of TMEM into the fp32 sums, then store:
+//              32 weight rows and all or half of the tokens a warp.
 //
 // Tiles.  Expert e with n_e rows has ceil(n_e / cols) token tiles.  Calls that
 // are bound by the weight stream cut the weight rows into units of 16, order the
@@ -51,7 +51,7 @@ struct Cfg {
     static constexpr int T = T_;
     static constexpr bool GATHER = GATHER_;
     static constexpr bool kWide = T == 192;                    // tensor cores bound the call, not the weight stream
-    static constexpr int kParts = kWide ? 4 : T >= 64 ? 2 : 1; // warps that share a weight row's columns
+    static constexpr int kParts = T >= 64 ? 2 : 1; // warps that share a weight row's columns
     static constexpr int kCols = T / kParts;
     static constexpr int kEpiWarp0 = GATHER ? 8 : 4;
     static constexpr int kEpiWarps = 4 * kParts;
@@ -68,11 +68,11 @@ struct Cfg {
     static constexpr int kScaleLd = T + 4;                     // floats between a table's rows: bank-free for its writers
     static constexpr int kTable = kAhead * kScaleLd;
     static constexpr int kScales = 2 * kTables * kTable;       // floats, two tables in turn
-    static constexpr int kRows = GATHER ? T : 0;               // rows of q of a tile
     static_assert(kTmemCols <= 512 && kAhead % P == 0 && kStage % 1024 == 0, "layout");
 };
 
 struct Params {
+    const uint8_t *q;
     const float *s_a, *s_w;
     const int32_t *src, *offsets;
     uint16_t *y;
@@ -88,7 +88,7 @@ constexpr int kBarBytes = 512;
 template <class C>
 size_t smem_bytes(int E)
 {
-    return 1024 + C::kStages * C::kStage + (C::kScales + C::kRows) * 4 + kBarBytes + 8 * (E + 1) + 4 * (E + 1);
+    return 1024 + C::kStages * C::kStage + C::kScales * 4 + kBarBytes + 8 * (E + 1) + 4 * (E + 1);
 }
 
 template <int V>
@@ -263,9 +263,10 @@ __device__ __forceinline__ bool sum_any(int groups, Rest &&...rest)
 
 // Stores 16 NG columns (tokens from c0 on) of the weight rows r0 .. r0 + 31 of a tile.  Eight tokens at a time are
 // transposed: lane i then has token i / 4 and the weight rows 8 j + 2 (i % 4), + 1 in word j; where rows of y allow it,
-// the four lanes of a token exchange words so that each stores 16 bytes (64 side by side a token).
+// the four lanes of a token exchange words so that each stores 16 bytes (64 side by side a token).  Bit g of `nowhere`:
+// src sends the g-th of a lane's tokens nowhere.
 template <class C, int NG>
-__device__ __forceinline__ void store_tile(const float *acc, const Params &p, const Tile &t, int c0, int r0)
+__device__ __forceinline__ void store_tile(const float *acc, const Params &p, const Tile &t, int c0, int r0, uint32_t nowhere)
 {
     const int lane = threadIdx.x & 31, quad = lane & 3;
     const bool wide = p.vec && r0 + 32 <= t.rows;
@@ -280,10 +281,7 @@ __device__ __forceinline__ void store_tile(const float *acc, const Params &p, co
         }
         const int m = c0 + 8 * g + (lane >> 2);
         const bool there = m < t.n;
-        if (C::GATHER) {                             // a row that src sends nowhere
-            const int r = __ldg(p.src + t.row0 + min(m, t.n - 1));
-            if (static_cast<unsigned>(r) >= static_cast<unsigned>(p.q_rows)) w[0] = w[1] = w[2] = w[3] = 0;
-        }
+        if (C::GATHER && (nowhere >> g & 1)) w[0] = w[1] = w[2] = w[3] = 0;
         if (wide) {
             // words 4 x 4 of the quad, transposed: pairs of lanes exchange pairs of words, then single ones
             const bool b1 = quad & 1, b2 = quad & 2;
@@ -321,8 +319,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *scales = reinterpret_cast<float *>(smem + C::kStages * C::kStage);
-    int *row_of = reinterpret_cast<int *>(scales + C::kScales);           // GATHER: the tile's rows of q
-    uint64_t *full = reinterpret_cast<uint64_t *>(row_of + C::kRows);     // copies landed
+    uint64_t *full = reinterpret_cast<uint64_t *>(scales + C::kScales);   // copies landed
     uint64_t *empty = full + C::kStages;                                  // MMAs done reading
     uint64_t *acc_full = empty + C::kStages;                              // block summed
     uint64_t *acc_empty = acc_full + C::kAccs;                            // taken out
@@ -338,7 +335,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int warp = warp_index(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], C::GATHER ? 5 : 1);   // the weights' copies, and four warps' rows
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < C::kAccs; ++a) {
@@ -413,7 +410,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     };
 
     if (warp < 4) {
-    // with 24 warps: 4 x 32 x 72 + 4 x 32 x 24 + 16 x 32 x 96 = 24 x 32 x 80, the launch's registers
+    // with 16 warps: 4 x 32 x 72 + 4 x 32 x 56 + 8 x 32 x 192 = 16 x 32 x 128, the launch's registers
     if (C::kWide && C::GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
         // ------------------------------------------------ copies
@@ -423,14 +420,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (lane == 0) {
             prefetch_tensormap(&map_w);
             prefetch_tensormap(&map_w16);
-            prefetch_tensormap(&map_q);
+            if (!C::GATHER) prefetch_tensormap(&map_q);
         }
         Tile t;
         t.e = e0;
         for (long long x = x0; ok && x < x1; x = next(x, t)) {
             tile_at(work, x, end_of(x), t);
             const int wy = t.e * p.N + t.w0;
-            const uint32_t bytes_q = C::GATHER ? ((t.n + 3) >> 2) * 4 * kF8Block : p.box * kF8Block;
+            const uint32_t bytes_q = C::GATHER ? 0 : p.box * kF8Block;
             // NW copies of 16 weight rows, or (8) one of 128; no branch but the waits'
             auto stages = [&](auto nw) {
                 constexpr int NW = decltype(nw)::value;
@@ -584,44 +581,60 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
     }
     } else if (warp < C::kEpiWarp0) {
-        // ------------------------------------------------ token rows by src: every fourth group of four rows a warp
-        if (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
-        Ring<C::kStages> ring;
+        // ------------------------------------------------ token rows by src
+        // Four rows an instruction, a lane 16 bytes: rows 16 i + 4 (warp % 4) + lane / 8.  A stage is handed over when
+        // its copies have landed, kDepth - 1 stages later.  (Gathers of four rows by TMA took 32 cycles each, 1,530 a block of 192.)
+        if (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        constexpr int kDepth = C::kStages - 1;
+        const int quarter = warp & 3, r4 = 4 * quarter + (lane >> 3), chunk = lane & 7;
+        const uint32_t to = smem_u32(smem) + C::P * kBlockW + r4 * 128 + ((chunk ^ (r4 & 7)) << 4);
+        Ring<C::kStages> ring, landed;
+        int flying = 0;
         bool ok = true;
-        const uint64_t pol_q = policy_evict_last();
+        auto hand_over = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[landed.s]);
+            landed.next();
+            --flying;
+        };
         Tile t;
         t.e = e0;
         for (long long x = x0; ok && x < x1; x = next(x, t)) {
             tile_at(work, x, end_of(x), t);
-            const int nq = (t.n + 3) >> 2;
-            __syncwarp();                                    // the tile before is read
-            for (int i = lane; i < C::kRows / 4; i += 32) {
-                const int m = 16 * (i >> 2) + 4 * (warp & 3) + (i & 3);
-                const int r = m < t.n ? __ldg(p.src + t.row0 + m) : 0;
-                row_of[m] = static_cast<unsigned>(r) < static_cast<unsigned>(p.q_rows) ? r : 0;
+            int row[T / 16];
+#pragma unroll
+            for (int i = 0; i < T / 16; ++i) {
+                const int r = __ldg(p.src + t.row0 + min(16 * i + r4, t.n - 1));
+                row[i] = static_cast<unsigned>(r) < static_cast<unsigned>(p.q_rows) ? r : 0;
             }
-            __syncwarp();
             for (int kb = 0; kb < p.kb; kb += C::P) {
-                const int s = ring.s, nb = min(C::P, p.kb - kb);
-                ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[s], ring.phase ^ 1u, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[ring.s], ring.phase ^ 1u, abort_flag));
                 if (!ok) break;
-                if (elect_one()) {
-                    for (int b = 0; b < nb; ++b) {
-                        uint8_t *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
-                        for (int g = warp & 3; g < nq; g += 4) {
-                            const int4 r = *reinterpret_cast<const int4 *>(row_of + 4 * g);
-                            const int y[4] = {r.x, r.y, r.z, r.w};
-                            tma_gather4(sq + g * 512, &map_q, &full[s], (kb + b) * kF8Block, y, pol_q);
-                        }
-                    }
+#pragma unroll
+                for (int b = 0; b < C::P; ++b) {
+                    const int k = (kb + b) * kF8Block + 16 * chunk;
+                    const int there = k < p.K ? 16 : 0;      // zeros behind the last element
+                    const uint32_t at = to + ring.s * C::kStage + b * C::kBlockQ;
+                    const uint8_t *from = p.q + (there ? k : 0);
+#pragma unroll
+                    for (int i = 0; i < T / 16; ++i)
+                        if (16 * i < t.n) cp_async16(at + i * 2048, from + static_cast<long long>(row[i]) * p.K, there);
                 }
-                __syncwarp();
+                cp_async_commit();
                 ring.next();
+                if (++flying == kDepth) {
+                    cp_async_wait<kDepth - 1>();
+                    hand_over();
+                }
             }
         }
+        if (!ok) fail();
+        cp_async_wait<0>();
+        while (flying > 0) hand_over();
     } else {
         // ------------------------------------------------ sums and results
-        if (C::kWide && C::GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        if (C::kWide && C::GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int qd = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
         Ring<C::kAccs> accs;
         Ring<2> tabs;
@@ -640,6 +653,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 const int r = 32 * qd + 16 * h;
                 table[h] = C::kTables == 2 && r < t.rows && (t.w0 + r) / kF8Block != t.w0 / kF8Block ? C::kTable : 0;
             }
+            uint32_t nowhere = 0;                            // read here: the loads' latency passes behind the first block
+            if (C::GATHER) {
+#pragma unroll
+                for (int g = 0; g < C::kCols / 8; ++g) {
+                    const int r = __ldg(p.src + t.row0 + min(c0 + 8 * g + (lane >> 2), t.n - 1));
+                    if (static_cast<unsigned>(r) >= static_cast<unsigned>(p.q_rows)) nowhere |= 1u << g;
+                }
+            }
             float acc[C::kCols];
             const float *sc = scales + c0 + 4 * (lane & 3);
             const uint32_t from = tmem + (static_cast<uint32_t>(32 * qd) << 16) + c0;
@@ -649,7 +670,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 fail();
                 break;
             }
-            store_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p, t, c0, 32 * qd);
+            store_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p, t, c0, 32 * qd, nowhere);
         }
     }
     __syncwarp();
@@ -674,6 +695,7 @@ cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
     cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     Params p;
+    p.q = a.q;
     p.s_a = a.s_a;
     p.s_w = a.s_w;
     p.src = a.src;
