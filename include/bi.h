@@ -629,7 +629,7 @@ BI_API bi_status bi_linear_f8_grouped(const uint8_t *q, const float *s_a, int q_
  * fewer than k are left, ids are -1 and weights 0.  +inf counts as the largest
  * finite value.  Weights, fp32:
  *   BI_ROUTE_SOFTMAX  p = exp(x - max) / sum over all experts (over the taken ones with renorm)
- *   BI_ROUTE_SIGMOID  p = 1 / (1 + exp(-x)), divided by the taken ones' sum with renorm (by 1 where that is 0)
+ *   BI_ROUTE_SIGMOID  p = 1 / (1 + exp(-x)), divided by the taken ones' sum with renorm
  *   weights = p * scale
  * Slot m k + j of expert e has a row; rows are in the order of experts, then slots:
  *   logits   fp32 or bf16 (`type`) [M, ldl], ldl >= E, read only

@@ -43,7 +43,7 @@ __device__ __forceinline__ uint2 codes8(const float (&t)[8], float s, bool plain
     float v[8];
     if (plain) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = quotient_rn(t[e], s, inv);
+        for (int e = 0; e < 8; ++e) v[e] = copysignf(quotient_rn(t[e], s, inv), t[e]);   // its zeros have lost their sign
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = __fdiv_rn(t[e], s);

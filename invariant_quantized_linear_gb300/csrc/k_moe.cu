@@ -108,9 +108,18 @@ __device__ __forceinline__ void select(const RouteArgs &a, int64_t m, int &id, f
         }
     }
     weight = 0.0f;
-    if (id >= 0) weight = a.score == BI_ROUTE_SOFTMAX ? expf(__fsub_rn(x, high)) : __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
+    if (a.score == BI_ROUTE_SOFTMAX) {
+        if (id >= 0) weight = expf(__fsub_rn(x, high));
+    } else {
+        // exp(x - low) / (1 + exp(x)) for x <= 0: with renorm all are taken exp(low) apart, low the largest x below 0, so that
+        // their quotients stay where the sigmoids themselves leave fp32
+        const float low = a.renorm ? fminf(__shfl_sync(0xffffffffu, x, 0), 0.0f) : 0.0f;
+        if (id >= 0)
+            weight = x > 0.0f ? __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)))
+                              : __fdiv_rn(expf(__fsub_rn(x, low)), __fadd_rn(1.0f, expf(x)));
+        whole = 1.0f;
+    }
     if (a.renorm) whole = warp_sum(weight);
-    else if (a.score != BI_ROUTE_SOFTMAX) whole = 1.0f;
     weight = __fmul_rn(__fdiv_rn(weight, whole > 0.0f ? whole : 1.0f), a.scale);
 }
 
