@@ -2,14 +2,14 @@
 
 A decoder with random weights serves a few sequences at once: RMS norm with the
 residual update into int8 codes, W8A8 linears, rotation with the append to the
-4-bit paged cache, attention over it, the gated MLP, and logits under penalties
-and a token mask.  Drafts come from the sequence itself (what followed the last
+4-bit paged cache, attention over it, the gated MLP or experts in e4m3 that a router
+chooses from, and logits under penalties and a token mask.  Drafts come from the sequence itself (what followed the last
 occurrence of its last two tokens); a verify pass runs them all at once and
 keeps the prefix that plain decoding would have chosen.  Every row of every call
 has the same bits whatever shares the call, so both ways give the same tokens,
 which main() checks.
 
-    python examples/generate.py [--new 64] [--draft 4]
+    python examples/generate.py [--new 64] [--draft 4] [--experts 8]
 """
 import argparse
 import os
@@ -33,7 +33,9 @@ class Config:
     heads: int = 8
     kv_heads: int = 2
     head_size: int = 128
-    inner: int = 2816
+    inner: int = 2816                                # width of the MLP, or of each expert
+    experts: int = 0                                 # 0: one MLP
+    top_k: int = 2
     vocab: int = 32003
     page: int = 64
     max_len: int = 1024
@@ -57,12 +59,24 @@ class Decoder:
             bi.bi_requant_pow2(codes, scale, codes, scale)
             return codes, scale
 
+        def experts(n, k):
+            codes = torch.empty((cfg.experts, n, k), dtype=torch.uint8, device=device)
+            scale = torch.empty((cfg.experts, -(-n // 128), -(-k // 128)), device=device)
+            for e in range(cfg.experts):
+                bi.bi_quantize_weight_f8(torch.randn((n, k), device=device, generator=gen) * k ** -0.5, codes[e], scale[e])
+            return codes, scale
+
+        def mlp():
+            if cfg.experts:
+                return dict(router=linear(cfg.experts, H), gu=experts(2 * I, H), down=experts(H, I))
+            return dict(gu=linear(2 * I, H), down=linear(H, I))
+
         def norm(n):
             return (1 + 0.1 * torch.randn(n, device=device, generator=gen)).bfloat16()
 
         self.embed = torch.randn((cfg.vocab, H), device=device, generator=gen).bfloat16()
         self.layers = [dict(norm1=norm(H), qkv=linear(qkv, H), q_norm=norm(D), k_norm=norm(D), o=linear(H, cfg.heads * D),
-                            norm2=norm(H), gu=linear(2 * I, H), down=linear(H, I)) for _ in range(cfg.layers)]
+                            norm2=norm(H), **mlp()) for _ in range(cfg.layers)]
         self.norm, self.head = norm(H), linear(cfg.vocab, H)
         inv = cfg.rope_base ** (-torch.arange(0, D, 2, dtype=torch.float64, device=device) / D)
         self.rope = torch.empty((cfg.max_len, D // 2, 2), device=device)
@@ -74,6 +88,7 @@ class Decoder:
         self.caches = [bi.kv4_cache(self.pool[:, i], cfg.page, D) for i in range(cfg.layers)]
         self.pages = torch.randperm(sequences * n, device=device, generator=gen).int().view(sequences, n)
         self.ws, self.tokens = None, 0
+        self.f8_ws = bi.new_f8_workspace(device)
 
     def _room(self, T: int) -> None:
         """Buffers for passes of up to T tokens."""
@@ -85,17 +100,40 @@ class Decoder:
         def buf(n, dtype=torch.bfloat16):
             return torch.empty((T, n), dtype=dtype, device=dev)
         self.tokens = T
-        self.y = dict(qkv=buf(QR + 2 * c.kv_heads * D), o=buf(c.hidden), gu=buf(2 * c.inner), down=buf(c.hidden))
-        self.codes = dict(h=buf(c.hidden, torch.int8), o=buf(QR, torch.int8), m=buf(c.inner, torch.int8))
+        self.y = dict(qkv=buf(QR + 2 * c.kv_heads * D), o=buf(c.hidden), down=buf(c.hidden))
+        self.codes = dict(h=buf(c.hidden, torch.int8), o=buf(QR, torch.int8))
+        if not c.experts:
+            self.y["gu"], self.codes["m"] = buf(2 * c.inner), buf(c.inner, torch.int8)
         self.scales = torch.empty(T, device=dev)
         self.q, self.o = (torch.empty((T, c.heads, D), dtype=torch.bfloat16, device=dev) for _ in range(2))
-        shapes = [self.layers[0][n][0].shape for n in ("qkv", "o", "gu", "down")] + [self.head[0].shape]
+        shapes = [w[0].shape for w in (*self.layers[0].values(), self.head) if type(w) is tuple and w[0].dim() == 2]
         self.ws = torch.zeros(max(bi.bi_linear_workspace_size(t, *s) for s in shapes for t in (1, T)), dtype=torch.uint8,
                               device=dev)
         bound = bi.kv4_batch(torch.zeros(self.B + 1, dtype=torch.int32), torch.zeros(self.B, dtype=torch.int32), self.pages, T,
                              T, c.max_len)
         self.attn_ws = bi.new_attention_kv4_workspace(c.heads, self.caches[0], bound, dev)
         self.logits_ws = bi.new_logits_workspace(T, dev)
+
+    def _experts(self, w: dict, h: torch.Tensor, logits: torch.Tensor, y: torch.Tensor) -> None:
+        """y: the weighted sum of what each token's experts make of h, bf16 [T, hidden]."""
+        c, dev, (T, H) = self.cfg, self.device, h.shape
+        R = T * c.top_k
+
+        def ints(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=dev)
+
+        def f8(m, k):
+            return torch.empty((m, k), dtype=torch.uint8, device=dev), torch.empty((m, -(-k // 128)), device=dev)
+        ids, weights, offsets, src, pos = ints(T, c.top_k), torch.empty((T, c.top_k), device=dev), ints(c.experts + 1), ints(R), ints(T, c.top_k)
+        bi.bi_moe_route(logits, bi.BI_ROUTE_SOFTMAX, True, 1.0, ids, weights, offsets, src, pos,
+                        bi.new_moe_route_workspace(T, c.experts, dev))
+        q, m = f8(T, H), f8(R, c.inner)
+        gu, rows = (torch.empty((R, n), dtype=torch.bfloat16, device=dev) for n in (2 * c.inner, H))
+        bi.bi_quantize_act_f8(h, *q)
+        bi.bi_linear_f8_grouped(*q, src, offsets, *w["gu"], gu, self.f8_ws)
+        bi.bi_gated_quantize_f8(gu, bi.BI_GATE_SILU, *m)
+        bi.bi_linear_f8_grouped(*m, None, offsets, *w["down"], rows, self.f8_ws)
+        bi.bi_moe_combine(rows, pos, weights, None, y)
 
     def forward(self, ids: torch.Tensor, counts: list[int], lengths: list[int], rows: torch.Tensor) -> torch.Tensor:
         """Appends counts[b] new tokens (ids int32 [T], in order) of each sequence, whose length becomes lengths[b], and
@@ -121,9 +159,14 @@ class Decoder:
             bi.bi_quantize_act(o.view(T, QR), codes["o"], s)
             bi.bi_linear_w8a8(codes["o"], s, *w["o"], y["o"], self.ws)
             bi.bi_rmsnorm_quantize(h, y["o"], w["norm2"], c.eps, h, codes["h"], s)
-            bi.bi_linear_w8a8(codes["h"], s, *w["gu"], y["gu"], self.ws)
-            bi.bi_relu_mul_quantize(y["gu"], c.inner, codes["m"], s)
-            bi.bi_linear_w8a8(codes["m"], s, *w["down"], y["down"], self.ws)
+            if c.experts:
+                logits = torch.empty((T, c.experts), dtype=torch.bfloat16, device=dev)
+                bi.bi_linear_w8a8(codes["h"], s, *w["router"], logits, self.ws)
+                self._experts(w, (codes["h"].float() * s[:, None]).bfloat16(), logits, y["down"])
+            else:
+                bi.bi_linear_w8a8(codes["h"], s, *w["gu"], y["gu"], self.ws)
+                bi.bi_relu_mul_quantize(y["gu"], c.inner, codes["m"], s)
+                bi.bi_linear_w8a8(codes["m"], s, *w["down"], y["down"], self.ws)
             add = y["down"]
         bi.bi_rmsnorm_quantize(h, add, self.norm, c.eps, h, codes["h"], s)
         logits = torch.empty((len(rows), c.vocab), dtype=torch.bfloat16, device=dev)
@@ -199,8 +242,9 @@ def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--new", type=int, default=64, help="tokens to generate")
     ap.add_argument("--draft", type=int, default=4, help="drafted tokens a pass")
+    ap.add_argument("--experts", type=int, default=0, help="experts of each MLP, two a token (0: one MLP)")
     args = ap.parse_args()
-    cfg = Config()
+    cfg = Config(experts=args.experts)
     gen = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, cfg.vocab, (n,), generator=gen).tolist() for n in (17, 300, 64)]
     model = Decoder(cfg, len(prompts))
@@ -219,6 +263,7 @@ def main() -> None:
                                                      (time.perf_counter() - t0) * 1e3 / args.new))
         outs.append(texts)
     assert bi.bi_workspace_status(model.attn_ws) == bi.BI_OK and bi.bi_workspace_status(model.ws) == bi.BI_OK
+    assert bi.bi_workspace_status(model.f8_ws) == bi.BI_OK
     assert outs[0] == outs[1], "speculative decoding changed the output"
     print("the same %d tokens for each of %d sequences" % (args.new, len(prompts)))
 
