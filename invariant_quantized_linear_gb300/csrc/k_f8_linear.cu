@@ -61,13 +61,15 @@ struct Cfg {
     static constexpr int kBlockQ = T * kF8Block;
     static constexpr int kStage = P * (kBlockW + kBlockQ);
     static constexpr int kStages = T == 128 ? 6 : T == 64 ? 4 : 5;
-    static constexpr int kAccs = kWide ? 2 : T >= 64 ? 4 : 8;  // accumulators in turn, each of P blocks
+    static constexpr int kAccs = kWide ? 2 : 4;                // accumulators in turn, each of P blocks
     static constexpr int kAccCols = kWide ? 256 : P * T;
     static constexpr uint32_t kTmemCols = kAccCols * kAccs;
     static constexpr int kTables = kWide ? 1 : 2;              // 128-row blocks of weights that a tile meets
     static constexpr int kScaleLd = T + 4;                     // floats between a table's rows: bank-free for its writers
     static constexpr int kTable = kAhead * kScaleLd;
     static constexpr int kScales = 2 * kTables * kTable;       // floats, two tables in turn
+    // a stage's MMAs are waited for by its producers and by the sums: no stage comes round twice before its sums are taken
+    static_assert(kStages >= kAccs, "the sums see every phase of done[]");
     static_assert(kTmemCols <= 512 && kAhead % P == 0 && kStage % 1024 == 0, "layout");
 };
 
@@ -183,8 +185,8 @@ __device__ __forceinline__ void tile_at(const Work &w, long long x, long long en
 // the other (a block of 96 columns took 1,850 cycles, 560 without).  table[h]: where the scales of rows 16 h on are.
 template <class C, int NG>
 __device__ __forceinline__ bool sum_blocks(float *acc, int blocks, const float *scales, const int (&table)[2], uint32_t from,
-                                           uint64_t *acc_full, uint64_t *acc_empty, uint64_t *sc_full, uint64_t *sc_empty,
-                                           Ring<C::kAccs> &accs, Ring<2> &tabs, volatile int *abort_flag)
+                                           uint64_t *done, uint64_t *acc_empty, uint64_t *sc_full, uint64_t *sc_empty,
+                                           Ring<C::kStages> &ring, Ring<C::kAccs> &accs, Ring<2> &tabs, volatile int *abort_flag)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -195,7 +197,8 @@ __device__ __forceinline__ bool sum_blocks(float *acc, int blocks, const float *
         constexpr int NB = decltype(nb)::value;
         const int a = accs.s;
         // warp-uniform: the TMEM loads below are warp-collective
-        if (!__all_sync(0xffffffffu, ready || mbar_wait_short(&acc_full[a], accs.phase, abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, ready || mbar_wait_short(&done[ring.s], ring.phase, abort_flag))) return false;
+        ring.next();
         accs.next();
         tc::fence_after();
         // 16 columns are on their way from TMEM while the 16 before them are added
@@ -219,7 +222,7 @@ __device__ __forceinline__ bool sum_blocks(float *acc, int blocks, const float *
                 // the accumulator is in registers: the next one is looked at while it is added
                 tc::fence_before();
                 if (lane == 0) mbar_arrive(&acc_empty[a]);
-                ready = mbar_test_wait(&acc_full[accs.s], accs.phase);
+                ready = mbar_test_wait(&done[ring.s], ring.phase);
             }
             const uint32_t(&v)[16] = d[u & 1];
 #pragma unroll
@@ -271,32 +274,54 @@ __device__ __forceinline__ void store_tile(const float *acc, const Params &p, co
     const int lane = threadIdx.x & 31, quad = lane & 3;
     const bool wide = p.vec && r0 + 32 <= t.rows;
     uint16_t *y = p.y + static_cast<long long>(t.row0 + c0 + (lane >> 2)) * p.N + t.w0 + r0;
+    constexpr int kBatch = NG % 2 == 0 ? 4 : 2;      // groups of 8 tokens whose exchanges overlap
 #pragma unroll
-    for (int g = 0; g < 2 * NG; ++g, y += 8 * static_cast<long long>(p.N)) {
-        uint32_t w[4];
+    for (int g0 = 0; g0 < 2 * NG; g0 += kBatch) {
+        uint32_t w[kBatch][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 o = __floats2bfloat162_rn(acc[8 * g + 2 * i], acc[8 * g + 2 * i + 1]);
-            w[i] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&o));
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 o = __floats2bfloat162_rn(acc[8 * (g0 + b) + 2 * i], acc[8 * (g0 + b) + 2 * i + 1]);
+                w[b][i] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&o));
+            }
+        if (C::GATHER) {
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (nowhere >> (g0 + b) & 1) w[b][0] = w[b][1] = w[b][2] = w[b][3] = 0;
         }
-        const int m = c0 + 8 * g + (lane >> 2);
-        const bool there = m < t.n;
-        if (C::GATHER && (nowhere >> g & 1)) w[0] = w[1] = w[2] = w[3] = 0;
         if (wide) {
             // words 4 x 4 of the quad, transposed: pairs of lanes exchange pairs of words, then single ones
             const bool b1 = quad & 1, b2 = quad & 2;
-            const uint32_t s0 = __shfl_xor_sync(0xffffffffu, b2 ? w[0] : w[2], 2), s1 = __shfl_xor_sync(0xffffffffu, b2 ? w[1] : w[3], 2);
-            const uint32_t a0 = b2 ? s0 : w[0], a1 = b2 ? s1 : w[1], a2 = b2 ? w[2] : s0, a3 = b2 ? w[3] : s1;
-            const uint32_t x0 = __shfl_xor_sync(0xffffffffu, b1 ? a0 : a1, 1), x1 = __shfl_xor_sync(0xffffffffu, b1 ? a2 : a3, 1);
-            const uint4 o = make_uint4(b1 ? x0 : a0, b1 ? a1 : x0, b1 ? x1 : a2, b1 ? a3 : x1);
-            if (there) *reinterpret_cast<uint4 *>(y + 8 * quad) = o;
-        } else if (there) {
+            uint32_t a[kBatch][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = 8 * i + 2 * quad;
-                if (r0 + n < t.rows) y[n] = static_cast<uint16_t>(w[i]);
-                if (r0 + n + 1 < t.rows) y[n + 1] = static_cast<uint16_t>(w[i] >> 16);
+            for (int b = 0; b < kBatch; ++b) {
+                const uint32_t s0 = __shfl_xor_sync(0xffffffffu, b2 ? w[b][0] : w[b][2], 2);
+                const uint32_t s1 = __shfl_xor_sync(0xffffffffu, b2 ? w[b][1] : w[b][3], 2);
+                a[b][0] = b2 ? s0 : w[b][0];
+                a[b][1] = b2 ? s1 : w[b][1];
+                a[b][2] = b2 ? w[b][2] : s0;
+                a[b][3] = b2 ? w[b][3] : s1;
             }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const uint32_t x0 = __shfl_xor_sync(0xffffffffu, b1 ? a[b][0] : a[b][1], 1);
+                const uint32_t x1 = __shfl_xor_sync(0xffffffffu, b1 ? a[b][2] : a[b][3], 1);
+                const uint4 o = make_uint4(b1 ? x0 : a[b][0], b1 ? a[b][1] : x0, b1 ? x1 : a[b][2], b1 ? a[b][3] : x1);
+                const int m = 8 * (g0 + b);
+                if (c0 + m + (lane >> 2) < t.n) *reinterpret_cast<uint4 *>(y + m * static_cast<long long>(p.N) + 8 * quad) = o;
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = 8 * i + 2 * quad, m = 8 * (g0 + b);
+                    if (c0 + m + (lane >> 2) >= t.n) continue;
+                    uint16_t *at = y + m * static_cast<long long>(p.N) + n;
+                    if (r0 + n < t.rows) at[0] = static_cast<uint16_t>(w[b][i]);
+                    if (r0 + n + 1 < t.rows) at[1] = static_cast<uint16_t>(w[b][i] >> 16);
+                }
         }
     }
 }
@@ -320,15 +345,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *scales = reinterpret_cast<float *>(smem + C::kStages * C::kStage);
     uint64_t *full = reinterpret_cast<uint64_t *>(scales + C::kScales);   // copies landed
-    uint64_t *empty = full + C::kStages;                                  // MMAs done reading
-    uint64_t *acc_full = empty + C::kStages;                              // block summed
-    uint64_t *acc_empty = acc_full + C::kAccs;                            // taken out
+    uint64_t *done = full + C::kStages;                                   // MMAs complete: stage free, accumulator full
+    uint64_t *acc_empty = done + C::kStages;                              // taken out
     uint64_t *sc_full = acc_empty + C::kAccs;                             // [2] table written
     uint64_t *sc_empty = sc_full + 2;                                     // [2] read
     uint64_t *drain = sc_empty + 2;                                       // all MMAs complete
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * C::kStages + 2 * C::kAccs + 4 + 1) * 8 + 8 <= kBarBytes, "barriers fit");
+    static_assert((2 * C::kStages + C::kAccs + 4 + 1) * 8 + 8 <= kBarBytes, "barriers fit");
     long long *first = reinterpret_cast<long long *>(full + kBarBytes / 8);
     int *row = reinterpret_cast<int *>(first + p.E + 1);
 
@@ -336,12 +360,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], C::GATHER ? 5 : 1);   // the weights' copies, and four warps' rows
-            mbar_init(&empty[s], 1);
+            mbar_init(&done[s], 1);
         }
-        for (int a = 0; a < C::kAccs; ++a) {
-            mbar_init(&acc_full[a], 1);
-            mbar_init(&acc_empty[a], C::kEpiWarps);
-        }
+        for (int a = 0; a < C::kAccs; ++a) mbar_init(&acc_empty[a], C::kEpiWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sc_full[i], 2);
             mbar_init(&sc_empty[i], C::kEpiWarps);
@@ -445,7 +466,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 int kb = 0;
                 for (; kb + C::P <= p.kb; kb += C::P) {
                     const int s = ring.s;
-                    ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[s], ring.phase ^ 1u, abort_flag));
+                    ok = __all_sync(0xffffffffu, mbar_wait_short(&done[s], ring.phase ^ 1u, abort_flag));
                     if (!ok) return;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&full[s], bytes * C::P);
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 }
                 if (kb < p.kb) {                             // the last block of an odd number
                     const int s = ring.s;
-                    ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[s], ring.phase ^ 1u, abort_flag));
+                    ok = __all_sync(0xffffffffu, mbar_wait_short(&done[s], ring.phase ^ 1u, abort_flag));
                     if (!ok) return;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&full[s], bytes);
@@ -506,15 +527,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             };
             auto stage = [&](auto nb) {
                 const int a = accs.s, s = ring.s;
-                ok = __all_sync(0xffffffffu, mbar_wait_short(&acc_empty[a], accs.phase ^ 1u, abort_flag) &&
-                                                 mbar_wait_short(&full[s], ring.phase, abort_flag));
+                // half the lanes look at each barrier: one look's latency for both
+                const bool odd = lane & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_short(odd ? &full[s] : &acc_empty[a], odd ? ring.phase : accs.phase ^ 1u,
+                                                             abort_flag));
                 if (!ok) return;
                 tc::fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int b = 0; b < decltype(nb)::value; ++b) block(s, a, b);
-                    tc::commit(&empty[s]);
-                    tc::commit(&acc_full[a]);
+                    tc::commit(&done[s]);
                 }
                 __syncwarp();
                 ring.next();
@@ -609,7 +631,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 row[i] = static_cast<unsigned>(r) < static_cast<unsigned>(p.q_rows) ? r : 0;
             }
             for (int kb = 0; kb < p.kb; kb += C::P) {
-                ok = __all_sync(0xffffffffu, mbar_wait_short(&empty[ring.s], ring.phase ^ 1u, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait_short(&done[ring.s], ring.phase ^ 1u, abort_flag));
                 if (!ok) break;
 #pragma unroll
                 for (int b = 0; b < C::P; ++b) {
@@ -636,6 +658,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // ------------------------------------------------ sums and results
         if (C::kWide && C::GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int qd = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
+        Ring<C::kStages> ring;
         Ring<C::kAccs> accs;
         Ring<2> tabs;
         bool ok = true;
@@ -664,7 +687,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             float acc[C::kCols];
             const float *sc = scales + c0 + 4 * (lane & 3);
             const uint32_t from = tmem + (static_cast<uint32_t>(32 * qd) << 16) + c0;
-            ok = sum_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p.kb, sc, table, from, acc_full, acc_empty, sc_full, sc_empty, accs, tabs,
+            ok = sum_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p.kb, sc, table, from, done, acc_empty, sc_full, sc_empty, ring, accs, tabs,
                                            abort_flag);
             if (!ok) {
                 fail();

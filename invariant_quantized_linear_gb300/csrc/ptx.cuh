@@ -199,7 +199,7 @@ __device__ __forceinline__ void ldmatrix_x2(uint32_t addr, uint32_t &r0, uint32_
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
 {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
