@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, int c
     const int words = chunk / 32;
     int *base = reinterpret_cast<int *>(mask + a.E * words);
     for (int i = threadIdx.x; i < a.E * words; i += kRouteThreads) mask[i] = 0;
+    if (gridDim.x > 1) pdl_launch_dependents();          // the second launch waits for this one's end before it reads
     if (pdl) pdl_wait();
     __syncthreads();
     const int first = blockIdx.x * chunk, tokens = min(chunk, a.M - first), lane = threadIdx.x & 31;
@@ -206,7 +207,6 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, int c
         for (int j = 0; j < words; ++j) n += __popc(mask[e * words + j]);
     if (gridDim.x > 1) {
         if (e < a.E) static_cast<int *>(a.ws)[static_cast<int64_t>(blockIdx.x) * a.E + e] = n;
-        pdl_launch_dependents();
         return;
     }
     int all;

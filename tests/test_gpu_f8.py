@@ -321,6 +321,22 @@ def test_route_borders(bi, softmax, renorm):
     check_route(bi, x, 6, softmax, renorm)
 
 
+def test_route_of_the_longest_calls(bi):
+    """Chunks whose masks take more than 48 KB of shared memory."""
+    M, E = 65535, 1024
+    x = torch.rand((M, E), device=DEV)
+    x[::7] = -float("inf")
+    x.scatter_(1, torch.randint(0, E, (M, 1), device=DEV), 2.0)
+    want = x.argmax(1).int()
+    ints = [torch.empty(s, dtype=torch.int32, device=DEV) for s in ((M, 1), (E + 1,), (M,), (M, 1))]
+    w = torch.empty((M, 1), device=DEV)
+    bi.bi_moe_route(x, bi.BI_ROUTE_SOFTMAX, True, 1.0, ints[0], w, *ints[1:], bi.new_moe_route_workspace(M, E))
+    assert torch.equal(ints[0][:, 0], want) and (w == 1).all()
+    assert torch.equal(ints[2].long(), torch.sort(want, stable=True).indices)
+    assert torch.equal(ints[1].long(), torch.cat((torch.zeros(1, device=DEV), torch.bincount(want, minlength=E).cumsum(0))).long())
+    assert torch.equal(ints[2][ints[3][:, 0].long()].long(), torch.arange(M, device=DEV))
+
+
 def test_route_rows_of_any_stride(bi):
     rng = np.random.default_rng(2)
     x = rng.normal(size=(70, 30)).astype(np.float32)
