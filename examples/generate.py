@@ -3,9 +3,9 @@
 A decoder with random weights serves a few sequences at once: RMS norm with the
 residual update into int8 codes, W8A8 linears, rotation with the append to the
 4-bit paged cache, attention over it, the gated MLP or experts in e4m3 that a router
-chooses from, and logits under penalties and a token mask.  Drafts come from the sequence itself (what followed the last
-occurrence of its last two tokens); a verify pass runs them all at once and
-keeps the prefix that plain decoding would have chosen.  Every row of every call
+chooses from, and logits under penalties and a token mask.  Drafts come from the
+sequence itself (what followed the last occurrence of its last two tokens); a verify
+pass runs them all at once and keeps the prefix that plain decoding would have chosen.  Every row of every call
 has the same bits whatever shares the call, so both ways give the same tokens,
 which main() checks.
 
@@ -124,7 +124,8 @@ class Decoder:
 
         def f8(m, k):
             return torch.empty((m, k), dtype=torch.uint8, device=dev), torch.empty((m, -(-k // 128)), device=dev)
-        ids, weights, offsets, src, pos = ints(T, c.top_k), torch.empty((T, c.top_k), device=dev), ints(c.experts + 1), ints(R), ints(T, c.top_k)
+        ids, offsets, src, pos = ints(T, c.top_k), ints(c.experts + 1), ints(R), ints(T, c.top_k)
+        weights = torch.empty((T, c.top_k), device=dev)
         bi.bi_moe_route(logits, bi.BI_ROUTE_SOFTMAX, True, 1.0, ids, weights, offsets, src, pos,
                         bi.new_moe_route_workspace(T, c.experts, dev))
         q, m = f8(T, H), f8(R, c.inner)

@@ -1,7 +1,8 @@
 """Batch-invariant verify pass for GB300 (sm_103a): Python binding of the W8A8
 linear and LM head, the verify-pass executor, the block-scaled variant, the
-split-KV verify attention and the decoder-step operators (norm, rotation with the
-4-bit paged cache, attention over it, logit rules).
+split-KV verify attention, the decoder-step operators (norm, rotation with the
+4-bit paged cache, attention over it, logit rules), and the e4m3 linears with the
+mixture of experts made of them.
 
 A thin ctypes layer over ``libbi.so`` (C ABI declared in ``include/bi.h``).
 Each function has the name of the C entry point it calls and only marshals

@@ -30,6 +30,17 @@
 //
 // Every wait is bounded: a role that gives up sets the status word and all
 // return; copies in flight are waited for and TMEM is freed.
+//
+// Bound.  8 x 4096 x 24576: 20.4 us, 5.0 TB/s of weights (0.73 of the copy rate),
+// the stream and a CTA's start and end.  Few rows of weights: the MMA warp, 345
+// cycles a block (16 x 12288 x 64: 20.7 us for 96 blocks).  2048 x 4096 x 12288:
+// 126 us, 1,630 TFLOP/s, 0.42 of twice the bf16 rate: the MMA warp again, 480 cycles
+// to issue a block's four MMAs and commit them and 350 of waits and loop around
+// them, where the tensor cores need 384 for 128 x 192 x 128.  Neither the sums (8,
+// 12 or 16 warps: 127, 131, 132 us), nor the loads, nor the scales are seen in that
+// time.  Each role runs as a whole warp that elects a thread for the issue, without
+// branches in its loop: single-thread loops and branches around copies, MMAs or TMEM
+// loads cost two to four times as much.
 #include "f8.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -431,181 +442,184 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     };
 
     if (warp < 4) {
-    // with 16 warps: 4 x 32 x 72 + 4 x 32 x 56 + 8 x 32 x 192 = 16 x 32 x 128, the launch's registers
-    if (C::kWide && C::GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0) {
-        // ------------------------------------------------ copies
-        Ring<C::kStages> ring;
-        bool ok = true, wrapped = false;
-        const uint64_t pol_w = policy_evict_first(), pol_q = policy_evict_last();
-        if (lane == 0) {
-            prefetch_tensormap(&map_w);
-            prefetch_tensormap(&map_w16);
-            if (!C::GATHER) prefetch_tensormap(&map_q);
-        }
-        Tile t;
-        t.e = e0;
-        for (long long x = x0; ok && x < x1; x = next(x, t)) {
-            tile_at(work, x, end_of(x), t);
-            const int wy = t.e * p.N + t.w0;
-            const uint32_t bytes_q = C::GATHER ? 0 : p.box * kF8Block;
-            // NW copies of 16 weight rows, or (8) one of 128; no branch but the waits'
-            auto stages = [&](auto nw) {
-                constexpr int NW = decltype(nw)::value;
-                const uint32_t bytes = NW * 16 * kF8Block + bytes_q;
-                auto copy = [&](int s, int b, int k) {
-                    uint8_t *sw = smem + s * C::kStage + b * kBlockW, *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
-                    if constexpr (NW == 8) {
-                        tma_load_2d(sw, &map_w, &full[s], k, wy, pol_w);
-                    } else {
+        // with 16 warps: 4 x 32 x 72 + 4 x 32 x 56 + 8 x 32 x 192 = 16 x 32 x 128, the launch's registers
+        if (C::kWide && C::GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            // ------------------------------------------------ copies
+            Ring<C::kStages> ring;
+            bool ok = true, wrapped = false;
+            const uint64_t pol_w = policy_evict_first(), pol_q = policy_evict_last();
+            if (lane == 0) {
+                prefetch_tensormap(&map_w);
+                prefetch_tensormap(&map_w16);
+                if (!C::GATHER) prefetch_tensormap(&map_q);
+            }
+            Tile t;
+            t.e = e0;
+            for (long long x = x0; ok && x < x1; x = next(x, t)) {
+                tile_at(work, x, end_of(x), t);
+                const int wy = t.e * p.N + t.w0;
+                const uint32_t bytes_q = C::GATHER ? 0 : p.box * kF8Block;
+                // NW copies of 16 weight rows, or (8) one of 128; no branch but the waits'
+                auto stages = [&](auto nw) {
+                    constexpr int NW = decltype(nw)::value;
+                    const uint32_t bytes = NW * 16 * kF8Block + bytes_q;
+                    auto copy = [&](int s, int b, int k) {
+                        uint8_t *sw = smem + s * C::kStage + b * kBlockW;
+                        uint8_t *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
+                        if constexpr (NW == 8) {
+                            tma_load_2d(sw, &map_w, &full[s], k, wy, pol_w);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < NW; ++i) tma_load_2d(sw + i * 2048, &map_w16, &full[s], k, wy + i * 16, pol_w);
+                            for (int i = 0; i < NW; ++i) tma_load_2d(sw + i * 2048, &map_w16, &full[s], k, wy + i * 16, pol_w);
+                        }
+                        if constexpr (!C::GATHER) tma_load_2d(sq, &map_q, &full[s], k, t.row0, pol_q);
+                    };
+                    int kb = 0;
+                    for (; kb + C::P <= p.kb; kb += C::P) {
+                        const int s = ring.s;
+                        ok = __all_sync(0xffffffffu, mbar_wait_short(&done[s], ring.phase ^ 1u, abort_flag));
+                        if (!ok) return;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&full[s], bytes * C::P);
+#pragma unroll
+                            for (int b = 0; b < C::P; ++b) copy(s, b, (kb + b) * kF8Block);
+                        }
+                        __syncwarp();
+                        ring.next();
+                        wrapped |= ring.s == 0;
                     }
-                    if constexpr (!C::GATHER) tma_load_2d(sq, &map_q, &full[s], k, t.row0, pol_q);
+                    if (kb < p.kb) {                             // the last block of an odd number
+                        const int s = ring.s;
+                        ok = __all_sync(0xffffffffu, mbar_wait_short(&done[s], ring.phase ^ 1u, abort_flag));
+                        if (!ok) return;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&full[s], bytes);
+                            copy(s, 0, kb * kF8Block);
+                        }
+                        __syncwarp();
+                        ring.next();
+                        wrapped |= ring.s == 0;
+                    }
+                };
+                switch (t.rows > 112 ? 8 : (t.rows + 15) >> 4) {
+                case 1: stages(Int<1>()); break;
+                case 2: stages(Int<2>()); break;
+                case 3: stages(Int<3>()); break;
+                case 4: stages(Int<4>()); break;
+                case 5: stages(Int<5>()); break;
+                case 6: stages(Int<6>()); break;
+                case 7: stages(Int<7>()); break;
+                default: stages(Int<8>());
+                }
+            }
+            if (!ok) fail();
+            // every copy that was issued lands before the CTA can exit
+            volatile int never = 0;
+            for (int s = 0; ok && s < C::kStages; ++s)
+                if (s < ring.s || wrapped) mbar_wait_short(&full[s], s < ring.s ? ring.phase : ring.phase ^ 1u, &never);
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMAs
+            Ring<C::kStages> ring;
+            Ring<C::kAccs> accs;
+            bool ok = true;
+            const uint64_t dw0 = tc::sdesc_kmajor_sw128(smem_u32(smem));
+            const uint64_t dq0 = tc::sdesc_kmajor_sw128(smem_u32(smem) + C::P * kBlockW);
+            Tile t;
+            t.e = e0;
+            for (long long x = x0; ok && x < x1; x = next(x, t)) {
+                tile_at(work, x, end_of(x), t);
+                // rows of the stage beyond the tile's hold old bytes: their sums are never looked at
+                const uint32_t idesc = tc::idesc_e4m3_f32(kTileRows, (t.n + 15) & ~15);
+                auto block = [&](int s, int a, int b) {
+                    const uint64_t at = static_cast<uint32_t>(s * (C::kStage >> 4));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma_e4m3_ss(tmem + a * C::kAccCols + b * T, dw0 + at + b * (kBlockW >> 4) + 2 * k,
+                                        dq0 + at + b * (C::kBlockQ >> 4) + 2 * k, idesc, k > 0 ? 1u : 0u);
+                };
+                auto stage = [&](auto nb) {
+                    const int a = accs.s, s = ring.s;
+                    // half the lanes look at each barrier: one look's latency for both
+                    const bool odd = lane & 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait_short(odd ? &full[s] : &acc_empty[a], odd ? ring.phase : accs.phase ^ 1u,
+                                                                 abort_flag));
+                    if (!ok) return;
+                    tc::fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int b = 0; b < decltype(nb)::value; ++b) block(s, a, b);
+                        tc::commit(&done[s]);
+                    }
+                    __syncwarp();
+                    ring.next();
+                    accs.next();
                 };
                 int kb = 0;
-                for (; kb + C::P <= p.kb; kb += C::P) {
-                    const int s = ring.s;
-                    ok = __all_sync(0xffffffffu, mbar_wait_short(&done[s], ring.phase ^ 1u, abort_flag));
-                    if (!ok) return;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&full[s], bytes * C::P);
-#pragma unroll
-                        for (int b = 0; b < C::P; ++b) copy(s, b, (kb + b) * kF8Block);
-                    }
-                    __syncwarp();
-                    ring.next();
-                    wrapped |= ring.s == 0;
-                }
-                if (kb < p.kb) {                             // the last block of an odd number
-                    const int s = ring.s;
-                    ok = __all_sync(0xffffffffu, mbar_wait_short(&done[s], ring.phase ^ 1u, abort_flag));
-                    if (!ok) return;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&full[s], bytes);
-                        copy(s, 0, kb * kF8Block);
-                    }
-                    __syncwarp();
-                    ring.next();
-                    wrapped |= ring.s == 0;
-                }
-            };
-            switch (t.rows > 112 ? 8 : (t.rows + 15) >> 4) {
-            case 1: stages(Int<1>()); break;
-            case 2: stages(Int<2>()); break;
-            case 3: stages(Int<3>()); break;
-            case 4: stages(Int<4>()); break;
-            case 5: stages(Int<5>()); break;
-            case 6: stages(Int<6>()); break;
-            case 7: stages(Int<7>()); break;
-            default: stages(Int<8>());
+                for (; ok && kb + C::P <= p.kb; kb += C::P) stage(Int<C::P>());
+                if (ok && kb < p.kb) stage(Int<1>());
             }
-        }
-        if (!ok) fail();
-        // every copy that was issued lands before the CTA can exit
-        volatile int never = 0;
-        for (int s = 0; ok && s < C::kStages; ++s)
-            if (s < ring.s || wrapped) mbar_wait_short(&full[s], s < ring.s ? ring.phase : ring.phase ^ 1u, &never);
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMAs
-        Ring<C::kStages> ring;
-        Ring<C::kAccs> accs;
-        bool ok = true;
-        const uint64_t dw0 = tc::sdesc_kmajor_sw128(smem_u32(smem)), dq0 = tc::sdesc_kmajor_sw128(smem_u32(smem) + C::P * kBlockW);
-        Tile t;
-        t.e = e0;
-        for (long long x = x0; ok && x < x1; x = next(x, t)) {
-            tile_at(work, x, end_of(x), t);
-            // rows of the stage beyond the tile's hold old bytes: their sums are never looked at
-            const uint32_t idesc = tc::idesc_e4m3_f32(kTileRows, (t.n + 15) & ~15);
-            auto block = [&](int s, int a, int b) {
-                const uint64_t at = static_cast<uint32_t>(s * (C::kStage >> 4));
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    tc::mma_e4m3_ss(tmem + a * C::kAccCols + b * T, dw0 + at + b * (kBlockW >> 4) + 2 * k,
-                                    dq0 + at + b * (C::kBlockQ >> 4) + 2 * k, idesc, k > 0 ? 1u : 0u);
-            };
-            auto stage = [&](auto nb) {
-                const int a = accs.s, s = ring.s;
-                // half the lanes look at each barrier: one look's latency for both
-                const bool odd = lane & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_short(odd ? &full[s] : &acc_empty[a], odd ? ring.phase : accs.phase ^ 1u,
-                                                             abort_flag));
-                if (!ok) return;
-                tc::fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int b = 0; b < decltype(nb)::value; ++b) block(s, a, b);
-                    tc::commit(&done[s]);
-                }
-                __syncwarp();
-                ring.next();
-                accs.next();
-            };
-            int kb = 0;
-            for (; ok && kb + C::P <= p.kb; kb += C::P) stage(Int<C::P>());
-            if (ok && kb < p.kb) stage(Int<1>());
-        }
-        if (!ok) fail();
-        // the same thread as above: commit counts what its thread issued
-        if (elect_one()) {
-            tc::commit(drain);
-            volatile int never = 0;
-            mbar_wait_bounded(drain, 0, &never);
-        }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------ scales
-        // lane: block lane % 8 of the table, tokens m1, m1 + 8, ...; kBatch of them on their way at once
-        Ring<2> tabs;
-        bool ok = true;
-        Tile t;
-        t.e = e0;
-        constexpr int kBatch = T / 8;
-        const int i = lane & 7, m1 = (lane >> 3) + 4 * (warp - 2);
-        for (long long x = x0; ok && x < x1; x = next(x, t)) {
-            tile_at(work, x, end_of(x), t);
-            const int cols = (t.n + 15) & ~15;
-            const float *sw = p.s_w + (static_cast<long long>(t.e) * p.nb + t.w0 / kF8Block) * p.kb;
-            const bool two = C::kTables == 2 && t.w0 / kF8Block != (t.w0 + t.rows - 1) / kF8Block;
-            for (int k0 = 0; k0 < p.kb; k0 += kAhead) {
-                ok = __all_sync(0xffffffffu, mbar_wait_short(&sc_empty[tabs.s], tabs.phase ^ 1u, abort_flag));
-                if (!ok) {
-                    fail();
-                    break;
-                }
-                float *table = scales + tabs.s * C::kTables * C::kTable + i * C::kScaleLd;
-                const int k = min(k0 + i, p.kb - 1);         // entries beyond the last block are not looked at
-                const float f0 = __ldg(sw + k), f1 = two ? __ldg(sw + p.kb + k) : 0.0f;
-                for (int m0 = m1; m0 < cols; m0 += 8 * kBatch) {
-                    int r[kBatch];
-                    float v[kBatch];
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        r[u] = t.row0 + min(m0 + 8 * u, t.n - 1);
-                        if (C::GATHER) r[u] = __ldg(p.src + r[u]);
-                        if (static_cast<unsigned>(r[u]) >= static_cast<unsigned>(p.q_rows)) r[u] = 0;
+            if (!ok) fail();
+            // the same thread as above: commit counts what its thread issued
+            if (elect_one()) {
+                tc::commit(drain);
+                volatile int never = 0;
+                mbar_wait_bounded(drain, 0, &never);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------ scales
+            // lane: block lane % 8 of the table, tokens m1, m1 + 8, ...; kBatch of them on their way at once
+            Ring<2> tabs;
+            bool ok = true;
+            Tile t;
+            t.e = e0;
+            constexpr int kBatch = T / 8;
+            const int i = lane & 7, m1 = (lane >> 3) + 4 * (warp - 2);
+            for (long long x = x0; ok && x < x1; x = next(x, t)) {
+                tile_at(work, x, end_of(x), t);
+                const int cols = (t.n + 15) & ~15;
+                const float *sw = p.s_w + (static_cast<long long>(t.e) * p.nb + t.w0 / kF8Block) * p.kb;
+                const bool two = C::kTables == 2 && t.w0 / kF8Block != (t.w0 + t.rows - 1) / kF8Block;
+                for (int k0 = 0; k0 < p.kb; k0 += kAhead) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_short(&sc_empty[tabs.s], tabs.phase ^ 1u, abort_flag));
+                    if (!ok) {
+                        fail();
+                        break;
                     }
+                    float *table = scales + tabs.s * C::kTables * C::kTable + i * C::kScaleLd;
+                    const int k = min(k0 + i, p.kb - 1);         // entries beyond the last block are not looked at
+                    const float f0 = __ldg(sw + k), f1 = two ? __ldg(sw + p.kb + k) : 0.0f;
+                    for (int m0 = m1; m0 < cols; m0 += 8 * kBatch) {
+                        int r[kBatch];
+                        float v[kBatch];
 #pragma unroll
-                    for (int u = 0; u < kBatch; ++u) v[u] = __ldg(p.s_a + static_cast<long long>(r[u]) * p.kb + k);
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u)
-                        if (m0 + 8 * u < cols) {
-                            const int at = place(m0 + 8 * u);
-                            table[at] = __fmul_rn(v[u], f0);
-                            if (two) table[C::kTable + at] = __fmul_rn(v[u], f1);
+                        for (int u = 0; u < kBatch; ++u) {
+                            r[u] = t.row0 + min(m0 + 8 * u, t.n - 1);
+                            if (C::GATHER) r[u] = __ldg(p.src + r[u]);
+                            if (static_cast<unsigned>(r[u]) >= static_cast<unsigned>(p.q_rows)) r[u] = 0;
                         }
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u) v[u] = __ldg(p.s_a + static_cast<long long>(r[u]) * p.kb + k);
+#pragma unroll
+                        for (int u = 0; u < kBatch; ++u)
+                            if (m0 + 8 * u < cols) {
+                                const int at = place(m0 + 8 * u);
+                                table[at] = __fmul_rn(v[u], f0);
+                                if (two) table[C::kTable + at] = __fmul_rn(v[u], f1);
+                            }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[tabs.s]);
+                    tabs.next();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sc_full[tabs.s]);
-                tabs.next();
             }
         }
-    }
     } else if (warp < C::kEpiWarp0) {
         // ------------------------------------------------ token rows by src
         // Four rows an instruction, a lane 16 bytes: rows 16 i + 4 (warp % 4) + lane / 8.  A stage is handed over when
-        // its copies have landed, kDepth - 1 stages later.  (Gathers of four rows by TMA took 32 cycles each, 1,530 a block of 192.)
+        // its copies have landed, kDepth - 1 stages later.  (Gathers of four rows by TMA took 32 cycles each, 1,530 a
+        // block of 192.)
         if (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         constexpr int kDepth = C::kStages - 1;
         const int quarter = warp & 3, r4 = 4 * quarter + (lane >> 3), chunk = lane & 7;
@@ -687,8 +701,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             float acc[C::kCols];
             const float *sc = scales + c0 + 4 * (lane & 3);
             const uint32_t from = tmem + (static_cast<uint32_t>(32 * qd) << 16) + c0;
-            ok = sum_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p.kb, sc, table, from, done, acc_empty, sc_full, sc_empty, ring, accs, tabs,
-                                           abort_flag);
+            ok = sum_any<C, C::kCols / 16>((nc + 15) >> 4, acc, p.kb, sc, table, from, done, acc_empty, sc_full, sc_empty, ring,
+                                           accs, tabs, abort_flag);
             if (!ok) {
                 fail();
                 break;
@@ -715,7 +729,8 @@ cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
 {
     const size_t smem = smem_bytes<C>(a.E);
     // a few hundred ns of host time, and right on every device
-    cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     Params p;
     p.q = a.q;

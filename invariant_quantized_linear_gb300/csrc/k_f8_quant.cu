@@ -8,7 +8,9 @@
 //
 // Bound: HBM; 3 bytes an element read and written, 5 behind the gate.  Half a warp
 // takes a block, 8 elements (16 bytes) a lane, so that the block's largest is four
-// shuffles away and its elements stay in registers.
+// shuffles away and its elements stay in registers.  8192 x 12288 behind silu: 106 us,
+// 4.8 TB/s (0.71 of the copy rate): the codes' and the gate's instructions show beside
+// the stream.  One row of 4096: 1.9 us, a launch and one read's latency.
 #include "f8.cuh"
 #include "ptx.cuh"
 #include "row_ops.cuh"
@@ -175,10 +177,12 @@ cudaError_t launch(const F8QuantArgs &a, unsigned grid, int kb, long long blocks
 
 cudaError_t launch_quantize_f8(const F8QuantArgs &a, int sms, bool pdl, cudaStream_t stream)
 {
+    // Up to eight CTAs a SM a block of 128 a half warp; longer calls read two ahead.
     const int kb = f8_blocks(a.K);
     const long long blocks = static_cast<long long>(a.M) * kb, ctas = (blocks + kThreads / 16 - 1) / (kThreads / 16);
     if (ctas <= 8LL * sms) return launch<1>(a, static_cast<unsigned>(ctas), kb, blocks, pdl, stream);
-    return launch<2>(a, static_cast<unsigned>((ctas + 1) / 2 < 64LL * sms ? (ctas + 1) / 2 : 64LL * sms), kb, blocks, pdl, stream);
+    const long long half = (ctas + 1) / 2, most = 64LL * sms;
+    return launch<2>(a, static_cast<unsigned>(half < most ? half : most), kb, blocks, pdl, stream);
 }
 
 cudaError_t launch_quantize_weight_f8(const float *w, int64_t ldw, int N, int K, uint8_t *w_q, float *s_w, cudaStream_t stream)
@@ -186,8 +190,8 @@ cudaError_t launch_quantize_weight_f8(const float *w, int64_t ldw, int N, int K,
     const int kb = f8_blocks(K), most = 65535 * kF8Block;
     for (int n = 0; n < N; n += most) {                  // a grid's second axis ends at 65535
         const int rows = N - n < most ? N - n : most;
-        quantize_weight_f8_kernel<<<dim3(kb, f8_blocks(rows)), kThreads, 0, stream>>>(w + n * ldw, ldw, rows, K, w_q + static_cast<int64_t>(n) * K,
-                                                                                     s_w + static_cast<int64_t>(n / kF8Block) * kb);
+        quantize_weight_f8_kernel<<<dim3(kb, f8_blocks(rows)), kThreads, 0, stream>>>(
+            w + n * ldw, ldw, rows, K, w_q + static_cast<int64_t>(n) * K, s_w + static_cast<int64_t>(n / kF8Block) * kb);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || N - n <= most) return e;
     }
