@@ -31,14 +31,14 @@
 // Every wait is bounded: a role that gives up sets the status word and all
 // return; copies in flight are waited for and TMEM is freed.
 //
-// Bound.  8 x 4096 x 24576: 20.4 us, 5.0 TB/s of weights (0.73 of the copy rate),
-// the stream and a CTA's start and end.  Few rows of weights: the MMA warp, 345
-// cycles a block (16 x 12288 x 64: 20.7 us for 96 blocks).  2048 x 4096 x 12288:
-// 126 us, 1,630 TFLOP/s, 0.42 of twice the bf16 rate: the MMA warp again, 480 cycles
-// to issue a block's four MMAs and commit them and 350 of waits and loop around
-// them, where the tensor cores need 384 for 128 x 192 x 128.  Neither the sums (8,
-// 12 or 16 warps: 127, 131, 132 us), nor the loads, nor the scales are seen in that
-// time.  Each role runs as a whole warp that elects a thread for the issue, without
+// Bound.  8 x 4096 x 24576: 19.6 us, 5.2 TB/s of weights (0.76 of the copy rate),
+// the stream and a CTA's start and end.  Few rows of weights: the chain of blocks,
+// of which the MMAs take 345 cycles each (16 x 12288 x 64: 17.7 us for 96 blocks).
+// 2048 x 4096 x 12288: 125 us, 1,650 TFLOP/s, 0.42 of twice the bf16 rate: the roles'
+// own instructions around each block, of the MMA warp above all (400 cycles to issue
+// four MMAs and a commit, 250 of looks and loop), where the tensor cores need 384 for
+// 128 x 192 x 128.  Fewer bytes, fewer MMAs or fewer sums do not shorten it (8, 12 or
+// 16 warps of sums: 127, 134, 134 us).  Each role runs as a whole warp that elects a thread for the issue, without
 // branches in its loop: single-thread loops and branches around copies, MMAs or TMEM
 // loads cost two to four times as much.
 #include "f8.cuh"
@@ -540,26 +540,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 };
                 auto stage = [&](auto nb) {
                     const int a = accs.s, s = ring.s;
-                    // half the lanes look at each barrier: one look's latency for both
+                    // Half the lanes look at each barrier: one look's latency for both.  A wait that gave up is
+                    // noted and the tile's MMAs are issued all the same, on what is there: the call's results mean
+                    // nothing then, and the loop is spared a vote and a branch (16 x 12288 x 64: 20.7 us with them,
+                    // 17.7 without).
                     const bool odd = lane & 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait_short(odd ? &full[s] : &acc_empty[a], odd ? ring.phase : accs.phase ^ 1u,
-                                                                 abort_flag));
-                    if (!ok) return;
+                    if (!mbar_wait_short(odd ? &full[s] : &acc_empty[a], odd ? ring.phase : accs.phase ^ 1u, abort_flag)) fail();
+                    __syncwarp();
                     tc::fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int b = 0; b < decltype(nb)::value; ++b) block(s, a, b);
                         tc::commit(&done[s]);
                     }
-                    __syncwarp();
                     ring.next();
                     accs.next();
                 };
                 int kb = 0;
-                for (; ok && kb + C::P <= p.kb; kb += C::P) stage(Int<C::P>());
-                if (ok && kb < p.kb) stage(Int<1>());
+                if constexpr (!C::kWide) {
+                    for (; kb + 2 * C::P <= p.kb; kb += 2 * C::P) {
+                        stage(Int<C::P>());
+                        stage(Int<C::P>());
+                    }
+                }
+                for (; kb + C::P <= p.kb; kb += C::P) stage(Int<C::P>());
+                if (kb < p.kb) stage(Int<1>());
+                __syncwarp();
+                ok = !__any_sync(0xffffffffu, *abort_flag);
             }
-            if (!ok) fail();
             // the same thread as above: commit counts what its thread issued
             if (elect_one()) {
                 tc::commit(drain);

@@ -118,6 +118,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, 
 {
     for (int it = 0; it < 64; ++it)
         if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
     return mbar_wait_bounded(bar, parity, abort);
 }
 
