@@ -500,6 +500,18 @@ def _dense(t: torch.Tensor, shape: tuple, size: int) -> int:
     return t.data_ptr()
 
 
+def _launch(name: str, tensors: tuple, stream, *args) -> None:
+    """Calls the library's `name` with args and the stream.  The library takes addresses and cannot see whose memory they
+    are: the tensors behind them (None: not given) must be on the current GPU, or the kernels would fault."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            device = -1
+    if device < 0 or device != torch._C._cuda_getDevice():
+        raise BiError(BI_ERR_INVALID_ARG, name + ", a tensor that is not on the current GPU")
+    _check(getattr(lib, name)(*args, _stream(stream)), name)
+
+
 def _blocks(n: int) -> int:
     """Blocks of 128 elements, the last one may be short."""
     return (n + 127) // 128
@@ -508,24 +520,24 @@ def _blocks(n: int) -> int:
 def bi_quantize_act_f8(x: torch.Tensor, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0, stream=None) -> None:
     """x: bf16 [M, >= K] (row stride x.stride(0)); q: e4m3 [M, K] (float8_e4m3fn or bytes); s_a: fp32 [M, ceil(K / 128)]."""
     M, K = q.shape
-    _check(lib.bi_quantize_act_f8(x.data_ptr(), _rows(x, M, K, 2), M, K, _dense(q, (M, K), 1), _dense(s_a, (M, _blocks(K)), 4),
-                                  flags, _stream(stream)), "bi_quantize_act_f8")
+    _launch("bi_quantize_act_f8", (x, q, s_a), stream, x.data_ptr(), _rows(x, M, K, 2), M, K, _dense(q, (M, K), 1),
+            _dense(s_a, (M, _blocks(K)), 4), flags)
 
 
 def bi_gated_quantize_f8(gu: torch.Tensor, gate: int, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0, stream=None) -> None:
     """gu: bf16 [M, >= 2K] packed gate|up (row stride gu.stride(0)); gate: BI_GATE_RELU or BI_GATE_SILU; q: e4m3 [M, K];
     s_a: fp32 [M, ceil(K / 128)]."""
     M, K = q.shape
-    _check(lib.bi_gated_quantize_f8(gu.data_ptr(), _rows(gu, M, 2 * K, 2), M, K, gate, _dense(q, (M, K), 1),
-                                    _dense(s_a, (M, _blocks(K)), 4), flags, _stream(stream)), "bi_gated_quantize_f8")
+    _launch("bi_gated_quantize_f8", (gu, q, s_a), stream, gu.data_ptr(), _rows(gu, M, 2 * K, 2), M, K, gate,
+            _dense(q, (M, K), 1), _dense(s_a, (M, _blocks(K)), 4), flags)
 
 
 def bi_quantize_weight_f8(w: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor, stream=None) -> None:
     """w: fp32 [N, K] (row stride w.stride(0)); w_q: e4m3 [N, K]; s_w: fp32 [ceil(N / 128), ceil(K / 128)]."""
     N, K = w_q.shape
     assert w.dtype == torch.float32
-    _check(lib.bi_quantize_weight_f8(w.data_ptr(), _rows(w, N, K, 4), N, K, _dense(w_q, (N, K), 1),
-                                     _dense(s_w, (_blocks(N), _blocks(K)), 4), _stream(stream)), "bi_quantize_weight_f8")
+    _launch("bi_quantize_weight_f8", (w, w_q, s_w), stream, w.data_ptr(), _rows(w, N, K, 4), N, K, _dense(w_q, (N, K), 1),
+            _dense(s_w, (_blocks(N), _blocks(K)), 4))
 
 
 def bi_f8_workspace_size() -> int:
@@ -543,9 +555,8 @@ def bi_linear_f8(q: torch.Tensor, s_a: torch.Tensor, w: torch.Tensor, s_w: torch
     ws: from new_f8_workspace."""
     (M, K), N = q.shape, w.shape[0]
     kb = _blocks(K)
-    _check(lib.bi_linear_f8(_dense(q, (M, K), 1), _dense(s_a, (M, kb), 4), M, K, _dense(w, (N, K), 1),
-                            _dense(s_w, (_blocks(N), kb), 4), N, _dense(y, (M, N), 2), ws.data_ptr(), ws.nbytes, flags,
-                            _stream(stream)), "bi_linear_f8")
+    _launch("bi_linear_f8", (q, s_a, w, s_w, y, ws), stream, _dense(q, (M, K), 1), _dense(s_a, (M, kb), 4), M, K,
+            _dense(w, (N, K), 1), _dense(s_w, (_blocks(N), kb), 4), N, _dense(y, (M, N), 2), ws.data_ptr(), ws.nbytes, flags)
 
 
 def bi_linear_f8_grouped(q: torch.Tensor, s_a: torch.Tensor, src: torch.Tensor | None, offsets: torch.Tensor, w: torch.Tensor,
@@ -555,10 +566,10 @@ def bi_linear_f8_grouped(q: torch.Tensor, s_a: torch.Tensor, src: torch.Tensor |
     (n, K), (R, N), E = q.shape, y.shape, w.shape[0]
     kb = _blocks(K)
     assert offsets.dtype == torch.int32 and (src is None or src.dtype == torch.int32)
-    _check(lib.bi_linear_f8_grouped(_dense(q, (n, K), 1), _dense(s_a, (n, kb), 4), n, K,
-                                    None if src is None else _dense(src, (R,), 4), R, _dense(offsets, (E + 1,), 4), E,
-                                    _dense(w, (E, N, K), 1), _dense(s_w, (E, _blocks(N), kb), 4), N, _dense(y, (R, N), 2),
-                                    ws.data_ptr(), ws.nbytes, flags, _stream(stream)), "bi_linear_f8_grouped")
+    _launch("bi_linear_f8_grouped", (q, s_a, src, offsets, w, s_w, y, ws), stream, _dense(q, (n, K), 1),
+            _dense(s_a, (n, kb), 4), n, K, None if src is None else _dense(src, (R,), 4), R, _dense(offsets, (E + 1,), 4), E,
+            _dense(w, (E, N, K), 1), _dense(s_w, (E, _blocks(N), kb), 4), N, _dense(y, (R, N), 2), ws.data_ptr(), ws.nbytes,
+            flags)
 
 
 def bi_moe_route_workspace_size(M: int, E: int) -> int:
@@ -581,10 +592,10 @@ def bi_moe_route(logits: torch.Tensor, score: int, renorm: bool, scale: float, i
     for t in (ids, offsets, src, pos):
         assert t.dtype == torch.int32
     assert weights.dtype == torch.float32
-    _check(lib.bi_moe_route(logits.data_ptr(), _rows(logits, M, E, 2 if half else 4), BI_TYPE_BF16 if half else BI_TYPE_F32, M, E,
-                            k, score, renorm, scale, _dense(ids, (M, k), 4), _dense(weights, (M, k), 4),
-                            _dense(offsets, (E + 1,), 4), _dense(src, (M * k,), 4), _dense(pos, (M, k), 4), ws.data_ptr(),
-                            ws.nbytes, flags, _stream(stream)), "bi_moe_route")
+    _launch("bi_moe_route", (logits, ids, weights, offsets, src, pos, ws), stream, logits.data_ptr(),
+            _rows(logits, M, E, 2 if half else 4), BI_TYPE_BF16 if half else BI_TYPE_F32, M, E, k, score, renorm, scale,
+            _dense(ids, (M, k), 4), _dense(weights, (M, k), 4), _dense(offsets, (E + 1,), 4), _dense(src, (M * k,), 4),
+            _dense(pos, (M, k), 4), ws.data_ptr(), ws.nbytes, flags)
 
 
 def bi_moe_combine(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, base: torch.Tensor | None, y: torch.Tensor,
@@ -593,9 +604,8 @@ def bi_moe_combine(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
     base."""
     (M, k), (R, N) = pos.shape, rows.shape
     assert pos.dtype == torch.int32 and weights.dtype == torch.float32
-    _check(lib.bi_moe_combine(_dense(rows, (R, N), 2), R, _dense(pos, (M, k), 4), _dense(weights, (M, k), 4), M, k, N,
-                              None if base is None else _dense(base, (M, N), 2), _dense(y, (M, N), 2), flags, _stream(stream)),
-           "bi_moe_combine")
+    _launch("bi_moe_combine", (rows, pos, weights, base, y), stream, _dense(rows, (R, N), 2), R, _dense(pos, (M, k), 4),
+            _dense(weights, (M, k), 4), M, k, N, None if base is None else _dense(base, (M, N), 2), _dense(y, (M, N), 2), flags)
 
 
 def bi_probe_read(buf: torch.Tensor, out: torch.Tensor, stream=None) -> None:
