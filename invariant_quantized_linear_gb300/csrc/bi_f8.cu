@@ -14,6 +14,7 @@ using bi::host::aligned4;
 using bi::host::device_info;
 using bi::host::from_cuda;
 using bi::host::overlaps;
+using bi::kMaxTokens;
 
 constexpr int kMaxRows = 1 << 20;
 constexpr int kMaxK = 1 << 20;
@@ -170,15 +171,15 @@ bi_status bi_linear_f8_grouped(const uint8_t *q, const float *s_a, int q_rows, i
 
 size_t bi_moe_route_workspace_size(int M, int E)
 {
-    return M < 1 || M > 65535 || E < 1 || E > bi::kMaxExperts ? 0 : bi::moe_route_workspace(M, E);
+    return M < 1 || M > kMaxTokens || E < 1 || E > bi::kMaxExperts ? 0 : bi::moe_route_workspace(M, E);
 }
 
 bi_status bi_moe_route(const void *logits, int64_t ldl, int type, int M, int E, int k, int score, int renorm, float scale,
                        int32_t *ids, float *weights, int32_t *offsets, int32_t *src, int32_t *pos, void *ws, size_t ws_bytes,
                        unsigned flags, bi_stream_t stream)
 {
-    if (!logits || !ids || !weights || !offsets || !src || !pos || M < 1 || M > 65535 || E < 1 || E > bi::kMaxExperts || k < 1 ||
-        k > bi::kMaxTopK || k > E || ldl < E || (type != BI_TYPE_F32 && type != BI_TYPE_BF16) ||
+    if (!logits || !ids || !weights || !offsets || !src || !pos || M < 1 || M > kMaxTokens || E < 1 || E > bi::kMaxExperts ||
+        k < 1 || k > bi::kMaxTopK || k > E || ldl < E || (type != BI_TYPE_F32 && type != BI_TYPE_BF16) ||
         (score != BI_ROUTE_SOFTMAX && score != BI_ROUTE_SIGMOID) || !(scale >= -3.402823466e38f && scale <= 3.402823466e38f))
         return BI_ERR_INVALID_ARG;
     if (!(type == BI_TYPE_F32 ? aligned4(logits) : aligned2(logits)) || !aligned4(ids) || !aligned4(weights) ||
@@ -215,8 +216,8 @@ bi_status bi_moe_route(const void *logits, int64_t ldl, int type, int M, int E, 
 bi_status bi_moe_combine(const uint16_t *rows, int R, const int32_t *pos, const float *weights, int M, int k, int N,
                          const uint16_t *base, uint16_t *y, unsigned flags, bi_stream_t stream)
 {
-    if (!rows || !pos || !weights || !y || R < 1 || R > kMaxRows * 2 || M < 1 || M > 65535 || k < 1 || k > bi::kMaxTopK || N < 1 ||
-        N > kMaxCols)
+    if (!rows || !pos || !weights || !y || R < 1 || R > kMaxRows * 2 || M < 1 || M > kMaxTokens || k < 1 || k > bi::kMaxTopK ||
+        N < 1 || N > kMaxCols)
         return BI_ERR_INVALID_ARG;
     if (!aligned2(rows) || !aligned4(pos) || !aligned4(weights) || (base && !aligned2(base)) || !aligned2(y))
         return BI_ERR_ALIGNMENT;

@@ -13,6 +13,7 @@ namespace bi {
 constexpr int kF8Block = 128;       // elements of a row (and of a weight's column) that share a scale
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
+constexpr int kMaxTokens = 65535;   // of the routing and the weighted sum
 
 inline int f8_blocks(int n) { return (n + kF8Block - 1) / kF8Block; }
 

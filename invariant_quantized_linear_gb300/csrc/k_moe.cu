@@ -27,6 +27,7 @@ constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kChunk = 64;                        // tokens of a chunk, where that gives at most kMostChunks
 constexpr int kMostChunks = 152;
+constexpr size_t kPlainSmem = 47 * 1024;          // dynamic shared memory that needs no opt-in, the static share beside it
 
 int chunk_tokens(int M)
 {
@@ -267,11 +268,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(RouteArgs a, 
     pdl_launch_dependents();
 }
 
+// Dynamic shared memory of a call: the masks of a chunk's tokens and three numbers an expert.
+size_t route_smem(int chunk, int E) { return static_cast<size_t>(E) * (chunk / 32) * 4 + 3 * static_cast<size_t>(E) * 4; }
+
 template <int EP>
 cudaError_t route(const RouteArgs &a, bool pdl, cudaStream_t stream)
 {
     const int chunk = chunk_tokens(a.M), chunks = (a.M + chunk - 1) / chunk;
-    const size_t smem = static_cast<size_t>(a.E) * (chunk / 32) * 4 + 3 * static_cast<size_t>(a.E) * 4;
+    const size_t smem = route_smem(chunk, a.E);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -283,10 +287,12 @@ cudaError_t route(const RouteArgs &a, bool pdl, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(route_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(route_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // Without an opt-in a kernel has 48 KB, its static share among them.  The opt-in is the kernel's, not the call's, so
+    // it is always the largest call's: a smaller one would take it from a call of another thread.
+    if (smem > kPlainSmem) {
+        const int most = static_cast<int>(route_smem(chunk_tokens(kMaxTokens), kMaxExperts));
+        e = cudaFuncSetAttribute(route_kernel<EP>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(route_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
     e = cudaLaunchKernelEx(&cfg, route_kernel<EP>, a, chunk, pdl ? 1 : 0);
