@@ -91,39 +91,41 @@ inline EncodeTiledFn encode_fn()
     return fn;
 }
 
-// 2-D int8 tensor [rows, cols] (row stride cols bytes), box box_cols x box_rows,
-// 128-byte swizzle, zero fill outside the tensor.
+// 2-D tensor [rows, cols] of elements of esz bytes, rows side by side, box box_cols x box_rows, 128-byte swizzle, zero fill
+// outside the tensor.  The driver wants a context that is current in the calling host thread, which nothing has made so
+// where this is the thread's first call: the runtime's calls before it ask for the device's number and attributes alone.
+inline bi_status encode_2d(CUtensorMap *map, CUtensorMapDataType type, size_t esz, const void *base, long long rows,
+                           long long cols, int box_cols, int box_rows, CUtensorMapL2promotion promotion)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return BI_ERR_UNSUPPORTED;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * esz};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    auto encode = [&] {
+        return fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return BI_OK;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode() ? BI_OK : BI_ERR_CUDA;
+}
+
+// int8 (row stride cols bytes).
 inline bi_status encode_int8_2d(CUtensorMap *map, const void *base, long long rows, long long cols, int box_cols,
                                 int box_rows, bool stream_once)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return BI_ERR_UNSUPPORTED;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    stream_once ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? BI_OK : BI_ERR_CUDA;
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, cols, box_cols, box_rows,
+                     stream_once ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
-// 2-D f16 tensor [rows, cols] (row stride 2 * cols bytes), box box_cols x
-// box_rows, 128-byte swizzle, zero fill outside the tensor.
+// f16 (row stride 2 * cols bytes).
 inline bi_status encode_f16_2d(CUtensorMap *map, const void *base, long long rows, long long cols, int box_cols,
                                int box_rows)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return BI_ERR_UNSUPPORTED;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * cols)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? BI_OK : BI_ERR_CUDA;
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, rows, cols, box_cols, box_rows,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // CTAs of the weight-streaming kernel: two per SM for a large weight matrix

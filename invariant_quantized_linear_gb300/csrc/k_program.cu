@@ -17,6 +17,7 @@
 // arithmetic of each op is that of bi_quantize_act / bi_linear_w8a8 /
 // bi_lmhead_argmax (exact int32 sums, fixed per-element epilogue).
 #include "bi.h"
+#include "host_common.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
 #include "row_ops.cuh"
@@ -27,7 +28,6 @@
 #include <cuda_runtime.h>
 
 #include <cstring>
-#include <mutex>
 #include <vector>
 
 namespace bi {
@@ -702,38 +702,7 @@ cudaError_t launch_program(const void *prog, void *wsp, int grid, cudaStream_t s
 
 // ------------------------------------------------------------------- host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-bool encode(CUtensorMap *map, const void *base, long long rows, long long cols, int box_rows, bool once)
-{
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-    cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              once ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+using host::encode_int8_2d;
 
 bool is_quantising(int kind)
 {
@@ -875,9 +844,9 @@ BI_API bi_status bi_program_build(const bi_op *ops, int n_ops, void *program, si
             d.upr = (o.K + kUnitK - 1) / kUnitK;
             d.units = static_cast<long long>((o.N + kBM - 1) / kBM) * d.upr;
             d.map_w = n_maps;
-            if (!encode(&maps[n_maps++], o.w_q, o.N, o.K, kBM, true)) return BI_ERR_CUDA;
+            if (encode_int8_2d(&maps[n_maps++], o.w_q, o.N, o.K, 128, kBM, true) != BI_OK) return BI_ERR_CUDA;
             d.map_q = n_maps;
-            if (!encode(&maps[n_maps++], o.q, o.M, o.K, 8 * mt, false)) return BI_ERR_CUDA;
+            if (encode_int8_2d(&maps[n_maps++], o.q, o.M, o.K, 128, 8 * mt, false) != BI_OK) return BI_ERR_CUDA;
         } else {
             return BI_ERR_INVALID_ARG;
         }
