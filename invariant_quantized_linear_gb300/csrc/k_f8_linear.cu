@@ -99,8 +99,9 @@ struct Params {
 constexpr int kBarBytes = 512;
 
 template <class C>
-size_t smem_bytes(int E)
+constexpr size_t smem_bytes(int E)
 {
+    static_assert(C::kStages * C::kStage + C::kScales * 4 + kBarBytes + 12 * (kMaxExperts + 1) + 1024 <= 227 * 1024, "fits an SM");
     return 1024 + C::kStages * C::kStage + C::kScales * 4 + kBarBytes + 8 * (E + 1) + 4 * (E + 1);
 }
 
@@ -738,9 +739,10 @@ template <class C>
 cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
 {
     const size_t smem = smem_bytes<C>(a.E);
-    // a few hundred ns of host time, and right on every device
+    // A few hundred ns of host time, and right on every device.  The opt-in is the kernel's, not the call's, so it is always
+    // the largest call's: a smaller one would take it from a call that another thread is about to launch.
     cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(smem_bytes<C>(kMaxExperts)));
     if (e != cudaSuccess) return e;
     Params p;
     p.q = a.q;
