@@ -494,22 +494,16 @@ def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.T
                                  _stream(stream)), "bi_logits_process")
 
 
-def _dense(t: torch.Tensor, shape: tuple, size: int) -> int:
-    """The address of elements of `size` bytes of this shape side by side."""
-    assert t.shape == shape and t.is_contiguous() and t.element_size() == size
+def _flat(t: torch.Tensor, size: int) -> int:
+    """The address of elements of `size` bytes side by side."""
+    assert t.is_contiguous() and t.element_size() == size
     return t.data_ptr()
 
 
-def _launch(name: str, tensors: tuple, stream, *args) -> None:
-    """Calls the library's `name` with args and the stream.  The library takes addresses and cannot see whose memory they
-    are: the tensors behind them (None: not given) must be on the current GPU, or the kernels would fault."""
-    device = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            device = -1
-    if device < 0 or device != torch._C._cuda_getDevice():
-        raise BiError(BI_ERR_INVALID_ARG, name + ", a tensor that is not on the current GPU")
-    _check(getattr(lib, name)(*args, _stream(stream)), name)
+def _dense(t: torch.Tensor, shape: tuple, size: int) -> int:
+    """The same of this shape."""
+    assert t.shape == shape and t.is_contiguous() and t.element_size() == size
+    return t.data_ptr()
 
 
 def _blocks(n: int) -> int:
@@ -517,27 +511,46 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _here(d: int, name: str) -> None:
+    """Refuses a call unless d, where its tensors are (-1: host memory), is the current GPU.  The library takes addresses and
+    cannot see whose memory they are; its kernels would fault on them."""
+    if d < 0 or d != torch._C._cuda_getDevice():
+        raise BiError(BI_ERR_INVALID_ARG, name + ", a tensor that is not on the current GPU")
+
+
+def _stream_at(d: int, stream) -> int:
+    """The handle of a stream; None: torch's current one of GPU d."""
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else _stream(stream)
+
+
 def bi_quantize_act_f8(x: torch.Tensor, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0, stream=None) -> None:
     """x: bf16 [M, >= K] (row stride x.stride(0)); q: e4m3 [M, K] (float8_e4m3fn or bytes); s_a: fp32 [M, ceil(K / 128)]."""
     M, K = q.shape
-    _launch("bi_quantize_act_f8", (x, q, s_a), stream, x.data_ptr(), _rows(x, M, K, 2), M, K, _dense(q, (M, K), 1),
-            _dense(s_a, (M, _blocks(K)), 4), flags)
+    ld, at_q, at_s = _rows(x, M, K, 2), _flat(q, 1), _dense(s_a, (M, (K + 127) // 128), 4)
+    d = x.get_device()
+    _here(d if d == q.get_device() == s_a.get_device() else -1, "bi_quantize_act_f8")
+    _check(lib.bi_quantize_act_f8(x.data_ptr(), ld, M, K, at_q, at_s, flags, _stream_at(d, stream)), "bi_quantize_act_f8")
 
 
 def bi_gated_quantize_f8(gu: torch.Tensor, gate: int, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0, stream=None) -> None:
     """gu: bf16 [M, >= 2K] packed gate|up (row stride gu.stride(0)); gate: BI_GATE_RELU or BI_GATE_SILU; q: e4m3 [M, K];
     s_a: fp32 [M, ceil(K / 128)]."""
     M, K = q.shape
-    _launch("bi_gated_quantize_f8", (gu, q, s_a), stream, gu.data_ptr(), _rows(gu, M, 2 * K, 2), M, K, gate,
-            _dense(q, (M, K), 1), _dense(s_a, (M, _blocks(K)), 4), flags)
+    ld, at_q, at_s = _rows(gu, M, 2 * K, 2), _flat(q, 1), _dense(s_a, (M, (K + 127) // 128), 4)
+    d = gu.get_device()
+    _here(d if d == q.get_device() == s_a.get_device() else -1, "bi_gated_quantize_f8")
+    _check(lib.bi_gated_quantize_f8(gu.data_ptr(), ld, M, K, gate, at_q, at_s, flags, _stream_at(d, stream)),
+           "bi_gated_quantize_f8")
 
 
 def bi_quantize_weight_f8(w: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor, stream=None) -> None:
     """w: fp32 [N, K] (row stride w.stride(0)); w_q: e4m3 [N, K]; s_w: fp32 [ceil(N / 128), ceil(K / 128)]."""
     N, K = w_q.shape
     assert w.dtype == torch.float32
-    _launch("bi_quantize_weight_f8", (w, w_q, s_w), stream, w.data_ptr(), _rows(w, N, K, 4), N, K, _dense(w_q, (N, K), 1),
-            _dense(s_w, (_blocks(N), _blocks(K)), 4))
+    ld, at_q, at_s = _rows(w, N, K, 4), _flat(w_q, 1), _dense(s_w, (_blocks(N), _blocks(K)), 4)
+    d = w.get_device()
+    _here(d if d == w_q.get_device() == s_w.get_device() else -1, "bi_quantize_weight_f8")
+    _check(lib.bi_quantize_weight_f8(w.data_ptr(), ld, N, K, at_q, at_s, _stream_at(d, stream)), "bi_quantize_weight_f8")
 
 
 def bi_f8_workspace_size() -> int:
@@ -553,23 +566,34 @@ def bi_linear_f8(q: torch.Tensor, s_a: torch.Tensor, w: torch.Tensor, s_w: torch
                  flags: int = 0, stream=None) -> None:
     """q: e4m3 [M, K], s_a: fp32 [M, ceil(K / 128)]; w: e4m3 [N, K], s_w: fp32 [ceil(N / 128), ceil(K / 128)]; y: bf16 [M, N];
     ws: from new_f8_workspace."""
-    (M, K), N = q.shape, w.shape[0]
+    (M, K), (N, k) = q.shape, w.shape
+    assert k == K
     kb = _blocks(K)
-    _launch("bi_linear_f8", (q, s_a, w, s_w, y, ws), stream, _dense(q, (M, K), 1), _dense(s_a, (M, kb), 4), M, K,
-            _dense(w, (N, K), 1), _dense(s_w, (_blocks(N), kb), 4), N, _dense(y, (M, N), 2), ws.data_ptr(), ws.nbytes, flags)
+    at_q, at_sa, at_w = _flat(q, 1), _dense(s_a, (M, kb), 4), _flat(w, 1)
+    at_sw, at_y = _dense(s_w, (_blocks(N), kb), 4), _dense(y, (M, N), 2)
+    d = q.get_device()
+    _here(d if d == s_a.get_device() == w.get_device() == s_w.get_device() == y.get_device() == ws.get_device() else -1,
+          "bi_linear_f8")
+    _check(lib.bi_linear_f8(at_q, at_sa, M, K, at_w, at_sw, N, at_y, ws.data_ptr(), ws.nbytes, flags, _stream_at(d, stream)),
+           "bi_linear_f8")
 
 
 def bi_linear_f8_grouped(q: torch.Tensor, s_a: torch.Tensor, src: torch.Tensor | None, offsets: torch.Tensor, w: torch.Tensor,
                          s_w: torch.Tensor, y: torch.Tensor, ws: torch.Tensor, flags: int = 0, stream=None) -> None:
     """y: bf16 [R, N], expert e's rows offsets[e] .. offsets[e + 1] - 1 (int32 [E + 1]) = rows src[r] (int32 [R], None: r) of
     q: e4m3 [n, K], s_a: fp32 [n, ceil(K / 128)] by w: e4m3 [E, N, K], s_w: fp32 [E, ceil(N / 128), ceil(K / 128)]."""
-    (n, K), (R, N), E = q.shape, y.shape, w.shape[0]
+    (n, K), (R, N), (E, _, k) = q.shape, y.shape, w.shape
+    assert w.shape[1] == N and k == K
     kb = _blocks(K)
     assert offsets.dtype == torch.int32 and (src is None or src.dtype == torch.int32)
-    _launch("bi_linear_f8_grouped", (q, s_a, src, offsets, w, s_w, y, ws), stream, _dense(q, (n, K), 1),
-            _dense(s_a, (n, kb), 4), n, K, None if src is None else _dense(src, (R,), 4), R, _dense(offsets, (E + 1,), 4), E,
-            _dense(w, (E, N, K), 1), _dense(s_w, (E, _blocks(N), kb), 4), N, _dense(y, (R, N), 2), ws.data_ptr(), ws.nbytes,
-            flags)
+    at_src = None if src is None else _dense(src, (R,), 4)
+    at_q, at_sa, at_off, at_w = _flat(q, 1), _dense(s_a, (n, kb), 4), _dense(offsets, (E + 1,), 4), _flat(w, 1)
+    at_sw, at_y = _dense(s_w, (E, _blocks(N), kb), 4), _flat(y, 2)
+    d = q.get_device()
+    _here(d if d == s_a.get_device() == offsets.get_device() == w.get_device() == s_w.get_device() == y.get_device() ==
+          ws.get_device() and (src is None or d == src.get_device()) else -1, "bi_linear_f8_grouped")
+    _check(lib.bi_linear_f8_grouped(at_q, at_sa, n, K, at_src, R, at_off, E, at_w, at_sw, N, at_y, ws.data_ptr(), ws.nbytes,
+                                    flags, _stream_at(d, stream)), "bi_linear_f8_grouped")
 
 
 def bi_moe_route_workspace_size(M: int, E: int) -> int:
@@ -592,10 +616,14 @@ def bi_moe_route(logits: torch.Tensor, score: int, renorm: bool, scale: float, i
     for t in (ids, offsets, src, pos):
         assert t.dtype == torch.int32
     assert weights.dtype == torch.float32
-    _launch("bi_moe_route", (logits, ids, weights, offsets, src, pos, ws), stream, logits.data_ptr(),
-            _rows(logits, M, E, 2 if half else 4), BI_TYPE_BF16 if half else BI_TYPE_F32, M, E, k, score, renorm, scale,
-            _dense(ids, (M, k), 4), _dense(weights, (M, k), 4), _dense(offsets, (E + 1,), 4), _dense(src, (M * k,), 4),
-            _dense(pos, (M, k), 4), ws.data_ptr(), ws.nbytes, flags)
+    ld = _rows(logits, M, E, 2 if half else 4)
+    at_ids, at_w, at_off = _dense(ids, (M, k), 4), _dense(weights, (M, k), 4), _dense(offsets, (E + 1,), 4)
+    at_src, at_pos = _dense(src, (M * k,), 4), _dense(pos, (M, k), 4)
+    d = logits.get_device()
+    _here(d if d == ids.get_device() == weights.get_device() == offsets.get_device() == src.get_device() ==
+          pos.get_device() == ws.get_device() else -1, "bi_moe_route")
+    _check(lib.bi_moe_route(logits.data_ptr(), ld, BI_TYPE_BF16 if half else BI_TYPE_F32, M, E, k, score, renorm, scale, at_ids,
+                            at_w, at_off, at_src, at_pos, ws.data_ptr(), ws.nbytes, flags, _stream_at(d, stream)), "bi_moe_route")
 
 
 def bi_moe_combine(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, base: torch.Tensor | None, y: torch.Tensor,
@@ -604,8 +632,12 @@ def bi_moe_combine(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
     base."""
     (M, k), (R, N) = pos.shape, rows.shape
     assert pos.dtype == torch.int32 and weights.dtype == torch.float32
-    _launch("bi_moe_combine", (rows, pos, weights, base, y), stream, _dense(rows, (R, N), 2), R, _dense(pos, (M, k), 4),
-            _dense(weights, (M, k), 4), M, k, N, None if base is None else _dense(base, (M, N), 2), _dense(y, (M, N), 2), flags)
+    at_rows, at_pos, at_w = _flat(rows, 2), _flat(pos, 4), _dense(weights, (M, k), 4)
+    at_base, at_y = None if base is None else _dense(base, (M, N), 2), _dense(y, (M, N), 2)
+    d = rows.get_device()
+    _here(d if d == pos.get_device() == weights.get_device() == y.get_device() and
+          (base is None or d == base.get_device()) else -1, "bi_moe_combine")
+    _check(lib.bi_moe_combine(at_rows, R, at_pos, at_w, M, k, N, at_base, at_y, flags, _stream_at(d, stream)), "bi_moe_combine")
 
 
 def bi_probe_read(buf: torch.Tensor, out: torch.Tensor, stream=None) -> None:
