@@ -494,16 +494,33 @@ def bi_logits_process(logits: torch.Tensor, rules: bi_logits_rules, out: torch.T
                                  _stream(stream)), "bi_logits_process")
 
 
-def _flat(t: torch.Tensor, size: int) -> int:
-    """The address of elements of `size` bytes side by side."""
-    assert t.is_contiguous() and t.element_size() == size
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)       # codes as such, or as bytes
+
+
+def _codes(t: torch.Tensor) -> int:
+    """The address of e4m3 codes side by side."""
+    assert t.dtype in _E4M3 and t.is_contiguous()
     return t.data_ptr()
 
 
-def _dense(t: torch.Tensor, shape: tuple, size: int) -> int:
+def _flat(t: torch.Tensor, dtype: torch.dtype) -> int:
+    """The address of elements side by side."""
+    assert t.dtype is dtype and t.is_contiguous()
+    return t.data_ptr()
+
+
+def _dense(t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> int:
     """The same of this shape."""
-    assert t.shape == shape and t.is_contiguous() and t.element_size() == size
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous()
     return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, M: int, K: int, dtype: torch.dtype) -> int:
+    """The row stride of elements [>= M, >= K]; of a single row, whose stride may be anything, K."""
+    (m, k), (ld, s) = t.shape, t.stride()
+    assert t.dtype is dtype and m >= M and k >= K and (s == 1 or k == 1)
+    return ld if M > 1 else K
 
 
 def _blocks(n: int) -> int:
@@ -526,7 +543,7 @@ def _stream_at(d: int, stream) -> int:
 def bi_quantize_act_f8(x: torch.Tensor, q: torch.Tensor, s_a: torch.Tensor, flags: int = 0, stream=None) -> None:
     """x: bf16 [M, >= K] (row stride x.stride(0)); q: e4m3 [M, K] (float8_e4m3fn or bytes); s_a: fp32 [M, ceil(K / 128)]."""
     M, K = q.shape
-    ld, at_q, at_s = _rows(x, M, K, 2), _flat(q, 1), _dense(s_a, (M, (K + 127) // 128), 4)
+    ld, at_q, at_s = _matrix(x, M, K, _BF16), _codes(q), _dense(s_a, (M, (K + 127) // 128), _F32)
     d = x.get_device()
     _here(d if d == q.get_device() == s_a.get_device() else -1, "bi_quantize_act_f8")
     _check(lib.bi_quantize_act_f8(x.data_ptr(), ld, M, K, at_q, at_s, flags, _stream_at(d, stream)), "bi_quantize_act_f8")
@@ -536,7 +553,7 @@ def bi_gated_quantize_f8(gu: torch.Tensor, gate: int, q: torch.Tensor, s_a: torc
     """gu: bf16 [M, >= 2K] packed gate|up (row stride gu.stride(0)); gate: BI_GATE_RELU or BI_GATE_SILU; q: e4m3 [M, K];
     s_a: fp32 [M, ceil(K / 128)]."""
     M, K = q.shape
-    ld, at_q, at_s = _rows(gu, M, 2 * K, 2), _flat(q, 1), _dense(s_a, (M, (K + 127) // 128), 4)
+    ld, at_q, at_s = _matrix(gu, M, 2 * K, _BF16), _codes(q), _dense(s_a, (M, (K + 127) // 128), _F32)
     d = gu.get_device()
     _here(d if d == q.get_device() == s_a.get_device() else -1, "bi_gated_quantize_f8")
     _check(lib.bi_gated_quantize_f8(gu.data_ptr(), ld, M, K, gate, at_q, at_s, flags, _stream_at(d, stream)),
@@ -546,8 +563,7 @@ def bi_gated_quantize_f8(gu: torch.Tensor, gate: int, q: torch.Tensor, s_a: torc
 def bi_quantize_weight_f8(w: torch.Tensor, w_q: torch.Tensor, s_w: torch.Tensor, stream=None) -> None:
     """w: fp32 [N, K] (row stride w.stride(0)); w_q: e4m3 [N, K]; s_w: fp32 [ceil(N / 128), ceil(K / 128)]."""
     N, K = w_q.shape
-    assert w.dtype == torch.float32
-    ld, at_q, at_s = _rows(w, N, K, 4), _flat(w_q, 1), _dense(s_w, (_blocks(N), _blocks(K)), 4)
+    ld, at_q, at_s = _matrix(w, N, K, _F32), _codes(w_q), _dense(s_w, (_blocks(N), _blocks(K)), _F32)
     d = w.get_device()
     _here(d if d == w_q.get_device() == s_w.get_device() else -1, "bi_quantize_weight_f8")
     _check(lib.bi_quantize_weight_f8(w.data_ptr(), ld, N, K, at_q, at_s, _stream_at(d, stream)), "bi_quantize_weight_f8")
@@ -569,8 +585,8 @@ def bi_linear_f8(q: torch.Tensor, s_a: torch.Tensor, w: torch.Tensor, s_w: torch
     (M, K), (N, k) = q.shape, w.shape
     assert k == K
     kb = _blocks(K)
-    at_q, at_sa, at_w = _flat(q, 1), _dense(s_a, (M, kb), 4), _flat(w, 1)
-    at_sw, at_y = _dense(s_w, (_blocks(N), kb), 4), _dense(y, (M, N), 2)
+    at_q, at_sa, at_w = _codes(q), _dense(s_a, (M, kb), _F32), _codes(w)
+    at_sw, at_y = _dense(s_w, (_blocks(N), kb), _F32), _dense(y, (M, N), _BF16)
     d = q.get_device()
     _here(d if d == s_a.get_device() == w.get_device() == s_w.get_device() == y.get_device() == ws.get_device() else -1,
           "bi_linear_f8")
@@ -585,10 +601,9 @@ def bi_linear_f8_grouped(q: torch.Tensor, s_a: torch.Tensor, src: torch.Tensor |
     (n, K), (R, N), (E, _, k) = q.shape, y.shape, w.shape
     assert w.shape[1] == N and k == K
     kb = _blocks(K)
-    assert offsets.dtype == torch.int32 and (src is None or src.dtype == torch.int32)
-    at_src = None if src is None else _dense(src, (R,), 4)
-    at_q, at_sa, at_off, at_w = _flat(q, 1), _dense(s_a, (n, kb), 4), _dense(offsets, (E + 1,), 4), _flat(w, 1)
-    at_sw, at_y = _dense(s_w, (E, _blocks(N), kb), 4), _flat(y, 2)
+    at_src = None if src is None else _dense(src, (R,), _I32)
+    at_q, at_sa, at_off, at_w = _codes(q), _dense(s_a, (n, kb), _F32), _dense(offsets, (E + 1,), _I32), _codes(w)
+    at_sw, at_y = _dense(s_w, (E, _blocks(N), kb), _F32), _flat(y, _BF16)
     d = q.get_device()
     _here(d if d == s_a.get_device() == offsets.get_device() == w.get_device() == s_w.get_device() == y.get_device() ==
           ws.get_device() and (src is None or d == src.get_device()) else -1, "bi_linear_f8_grouped")
@@ -611,19 +626,16 @@ def bi_moe_route(logits: torch.Tensor, score: int, renorm: bool, scale: float, i
     """logits: fp32 or bf16 [M, E] (row stride logits.stride(0)); score: BI_ROUTE_SOFTMAX or BI_ROUTE_SIGMOID; ids: int32
     [M, k]; weights: fp32 [M, k]; offsets: int32 [E + 1]; src: int32 [M k]; pos: int32 [M, k]."""
     (M, E), k = logits.shape, ids.shape[1]
-    half = logits.dtype == torch.bfloat16
-    assert half or logits.dtype == torch.float32
-    for t in (ids, offsets, src, pos):
-        assert t.dtype == torch.int32
-    assert weights.dtype == torch.float32
-    ld = _rows(logits, M, E, 2 if half else 4)
-    at_ids, at_w, at_off = _dense(ids, (M, k), 4), _dense(weights, (M, k), 4), _dense(offsets, (E + 1,), 4)
-    at_src, at_pos = _dense(src, (M * k,), 4), _dense(pos, (M, k), 4)
+    half = logits.dtype is _BF16
+    ld = _matrix(logits, M, E, _BF16 if half else _F32)
+    at_ids, at_w, at_off = _dense(ids, (M, k), _I32), _dense(weights, (M, k), _F32), _dense(offsets, (E + 1,), _I32)
+    at_src, at_pos = _dense(src, (M * k,), _I32), _dense(pos, (M, k), _I32)
     d = logits.get_device()
     _here(d if d == ids.get_device() == weights.get_device() == offsets.get_device() == src.get_device() ==
           pos.get_device() == ws.get_device() else -1, "bi_moe_route")
-    _check(lib.bi_moe_route(logits.data_ptr(), ld, BI_TYPE_BF16 if half else BI_TYPE_F32, M, E, k, score, renorm, scale, at_ids,
-                            at_w, at_off, at_src, at_pos, ws.data_ptr(), ws.nbytes, flags, _stream_at(d, stream)), "bi_moe_route")
+    _check(lib.bi_moe_route(logits.data_ptr(), ld, BI_TYPE_BF16 if half else BI_TYPE_F32, M, E, k, score, renorm, scale,
+                            at_ids, at_w, at_off, at_src, at_pos, ws.data_ptr(), ws.nbytes, flags, _stream_at(d, stream)),
+           "bi_moe_route")
 
 
 def bi_moe_combine(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, base: torch.Tensor | None, y: torch.Tensor,
@@ -631,9 +643,8 @@ def bi_moe_combine(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
     """rows: bf16 [R, N]; pos: int32 [M, k]; weights: fp32 [M, k]; base: bf16 [M, N] or None; y: bf16 [M, N], it may be
     base."""
     (M, k), (R, N) = pos.shape, rows.shape
-    assert pos.dtype == torch.int32 and weights.dtype == torch.float32
-    at_rows, at_pos, at_w = _flat(rows, 2), _flat(pos, 4), _dense(weights, (M, k), 4)
-    at_base, at_y = None if base is None else _dense(base, (M, N), 2), _dense(y, (M, N), 2)
+    at_rows, at_pos, at_w = _flat(rows, _BF16), _flat(pos, _I32), _dense(weights, (M, k), _F32)
+    at_base, at_y = None if base is None else _dense(base, (M, N), _BF16), _dense(y, (M, N), _BF16)
     d = rows.get_device()
     _here(d if d == pos.get_device() == weights.get_device() == y.get_device() and
           (base is None or d == base.get_device()) else -1, "bi_moe_combine")

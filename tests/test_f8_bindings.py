@@ -87,3 +87,30 @@ def test_tensors_off_the_gpu_reach_no_kernel(bi, monkeypatch, name):
     assert not lib.names
     call(bi, name, on(On, args))
     assert lib.names == [name]
+
+
+# other types of the same size, which would be read as if they were the right one
+WRONG = {torch.bfloat16: (torch.float16, torch.int16), torch.float32: (torch.int32,), torch.int32: (torch.float32,),
+         torch.uint8: (torch.int8, torch.float8_e5m2, torch.bool)}
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_of_other_types_reach_no_kernel(bi, monkeypatch, name):
+    lib = Library()
+    monkeypatch.setattr(bi, "lib", lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    args = on(On, tensors(bi)[name])
+    for k, v in args.items():
+        if not torch.is_tensor(v) or k == "ws":
+            continue
+        for dtype in WRONG[v.dtype]:
+            with pytest.raises(AssertionError):
+                call(bi, name, {**args, k: torch.zeros(v.shape, dtype=dtype).as_subclass(On)})
+    assert not lib.names
+    for k, v in args.items():                        # codes are taken as such too, and logits as bf16
+        if torch.is_tensor(v) and v.dtype == torch.uint8 and k != "ws":
+            args[k] = v.view(torch.float8_e4m3fn)
+    if name == "bi_moe_route":
+        args["logits"] = args["logits"].bfloat16()
+    call(bi, name, args)
+    assert lib.names == [name]
