@@ -570,7 +570,7 @@ BI_API bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, i
  * below (|g| + 8) 2^-23.  A block with an infinity or a NaN has that as its
  * scale and NaN in its codes, so that it shows in its own row alone.
  *   x   bf16 [M, ldx], first K columns (2 K behind a gate) read, 16-byte aligned, ldx % 8 == 0
- *   q   e4m3 [M, K] out, 16-byte aligned;  s_a fp32 [M, KB] out;  1 <= M <= 2^20
+ *   q   e4m3 [M, K] out, 16-byte aligned;  s_a fp32 [M, KB] out;  1 <= M <= 2^20, M KB < 2^31
  * Outputs overlap neither each other nor the input.  With BI_FLAG_PDL the kernel
  * waits for the preceding kernel first.
  */

@@ -52,7 +52,9 @@ bi_status quantize(const uint16_t *x, int64_t ldx, int M, int K, int gate, uint8
                    bi_stream_t stream)
 {
     const int64_t width = gate < 0 ? K : 2 * static_cast<int64_t>(K);
-    if (!x || !q || !s_a || M < 1 || M > kMaxRows || !k_ok(K) || ldx < width) return BI_ERR_INVALID_ARG;
+    if (!x || !q || !s_a || M < 1 || M > kMaxRows || !k_ok(K) || ldx < width ||
+        static_cast<int64_t>(M) * bi::f8_blocks(K) > 0x7FFFFFFF)
+        return BI_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(q) || !aligned4(s_a) || ldx % 8 != 0) return BI_ERR_ALIGNMENT;
     const Span written[] = {{q, bytes(M, K, 1)}, {s_a, bytes(M, bi::f8_blocks(K), 4)}};
     const Span read[] = {{x, strided(M, ldx, width, 2)}};

@@ -114,3 +114,15 @@ def test_tensors_of_other_types_reach_no_kernel(bi, monkeypatch, name):
         args["logits"] = args["logits"].bfloat16()
     call(bi, name, args)
     assert lib.names == [name]
+
+
+@pytest.mark.parametrize("gate", [None, 0, 1])
+def test_quantisers_count_their_blocks_in_32_bits(bi, gate):
+    """2^31 blocks are more than any memory holds, and refused; one row less gets past the limit, to an unaligned pointer."""
+    def quantise(M):
+        K, at = 1 << 20, (1 << 44) + 8
+        if gate is None:
+            return bi.lib.bi_quantize_act_f8(at, K, M, K, 1 << 50, 1 << 52, 0, None)
+        return bi.lib.bi_gated_quantize_f8(at, 2 * K, M, K, gate, 1 << 50, 1 << 52, 0, None)
+    assert quantise(1 << 18) == bi.BI_ERR_INVALID_ARG
+    assert quantise((1 << 18) - 1) == bi.BI_ERR_ALIGNMENT
