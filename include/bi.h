@@ -567,8 +567,9 @@ BI_API bi_status bi_logits_process(const uint16_t *logits, int64_t ldl, int M, i
  *   q = e4m3(x / s): fp32 division, round to nearest even, 448 at most
  * x is bf16, or the fp32 gated product act(g) * u of packed rows gate|up:
  * relu(g) = g > 0 ? g : 0, silu(g) = g / (1 + exp(-g)) with a relative error
- * below (|g| + 8) 2^-23.  A block with an infinity or a NaN has that as its
- * scale and NaN in its codes, so that it shows in its own row alone.
+ * below (|g| + 8) 2^-23 for g >= -131; below that, where it is 2^-181 and less, it
+ * may be 0.  A block with an infinity or a NaN has that as its scale and NaN in its
+ * codes, so that it shows in its own row alone.
  *   x   bf16 [M, ldx], first K columns (2 K behind a gate) read, 16-byte aligned, ldx % 8 == 0
  *   q   e4m3 [M, K] out, 16-byte aligned;  s_a fp32 [M, KB] out;  1 <= M <= 2^20, M KB < 2^31
  * Outputs overlap neither each other nor the input.  With BI_FLAG_PDL the kernel

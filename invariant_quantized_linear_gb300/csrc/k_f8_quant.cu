@@ -8,9 +8,11 @@
 //
 // Bound: HBM; 3 bytes an element read and written, 5 behind the gate.  Half a warp
 // takes a block, 8 elements (16 bytes) a lane, so that the block's largest is four
-// shuffles away and its elements stay in registers.  8192 x 12288 behind silu: 106 us,
-// 4.8 TB/s (0.71 of the copy rate): the codes' and the gate's instructions show beside
-// the stream.  One row of 4096: 1.9 us, a launch and one read's latency.
+// shuffles away and its elements stay in registers.  8192 x 12288 behind silu: 101 us,
+// 5.0 TB/s (0.74 of the copy rate); behind relu 91; as it is 74, 4.1 TB/s.  The plain
+// form moves 3/5 of the bytes in 3/4 of the time, so instructions show beside the
+// stream; a division that each thread does no more took 10 us of it.  8192 x 4096 as it
+// is: 24.9 us.  One row of 4096: 1.9 us, a launch and one read's latency.
 #include "f8.cuh"
 #include "ptx.cuh"
 #include "row_ops.cuh"
@@ -54,26 +56,31 @@ __device__ __forceinline__ uint2 codes8(const float (&t)[8], float s, bool plain
 }
 
 // act(g) u in fp32.  silu by the hardware's exponential and reciprocal: relative
-// error below (|g| + 8) 2^-23, far below a code's 2^-4.
-template <int GATE>
+// error below (|g| + 8) 2^-23, far below a code's 2^-4.  Both flush what is not a
+// normal number, and 1 / (1 + exp(-g)) is none from g = -87.4 on, where g times it
+// still is.  LOW: for g below kLowGate the exponential is taken as 2^-64 of itself
+// (the 1 beside it is nothing there, either way) and the product scaled back, which
+// holds to g = -131; for other g the bits are the same as without LOW.
+constexpr float kLowGate = -80.0f;
+
+template <int GATE, bool LOW>
 __device__ __forceinline__ float gated(float g, float u)
 {
     if (GATE == BI_GATE_RELU) return __fmul_rn(relu_pos(g), u);
+    const bool low = LOW && g < kLowGate;
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(g, -1.4426950408889634f, low ? -64.0f : -0.0f)));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
-    return __fmul_rn(__fmul_rn(g, r), u);
+    const float t = __fmul_rn(__fmul_rn(g, r), u);
+    return low ? __fmul_rn(t, 0x1p-64f) : t;
 }
 
-// GATE -1: x as it is.  Blocks are counted in 32 bits: their division by kb costs 5 us of 106 in 64 (8192 x 12288 behind
-// silu).
-template <int GATE, int AHEAD>
-__global__ void __launch_bounds__(kThreads) quantize_f8_kernel(F8QuantArgs a, unsigned kb, unsigned blocks, int pdl)
+// GATE -1: x as it is.  Blocks are counted in 32 bits: their division by kb in 64 cost 7 us of 106 (8192 x 12288 behind
+// silu) and 10 of 84 (as it is).  Returns the largest of this thread's gates as whole numbers, 16 bits each: the negative one farthest from 0, if any.
+template <int GATE, int AHEAD, bool LOW>
+__device__ __forceinline__ uint32_t quantize_blocks(const F8QuantArgs &a, unsigned kb, unsigned blocks)
 {
-    if (pdl) {
-        pdl_launch_dependents();
-        pdl_wait();
-    }
+    uint32_t lowest = 0;
     const int sub = threadIdx.x & 15;
     const unsigned step = gridDim.x * (kThreads / 16);
     for (unsigned at = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);; at += AHEAD * step) {
@@ -100,12 +107,13 @@ __global__ void __launch_bounds__(kThreads) quantize_f8_kernel(F8QuantArgs a, un
         for (int i = 0; i < AHEAD; ++i) {
             const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             const uint32_t v[4] = {up[i].x, up[i].y, up[i].z, up[i].w};
+            if (GATE == BI_GATE_SILU && !LOW) lowest = __vimax3_u16x2(__vimax3_u16x2(lowest, w[0], w[1]), w[2], w[3]);
             float t[8];
             uint32_t top = 0;   // bits of the largest magnitude: NaN is above infinity, and is kept
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 t[e] = (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-                if (GATE >= 0) t[e] = gated<GATE>(t[e], (e & 1) ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]));
+                if (GATE >= 0) t[e] = gated<GATE, LOW>(t[e], (e & 1) ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]));
                 top = max(top, __float_as_uint(t[e]) & 0x7FFFFFFFu);
             }
 #pragma unroll
@@ -116,6 +124,31 @@ __global__ void __launch_bounds__(kThreads) quantize_f8_kernel(F8QuantArgs a, un
             *reinterpret_cast<uint2 *>(a.q + row[i] * a.K + col[i]) = codes8(t, s, plain, __fdiv_rn(1.0f, s));
             if (sub == 0) a.s[row[i] * kb + col[i] / kF8Block] = s;
         }
+    }
+    return lowest;
+}
+
+// The warp's blocks once more, for gates below kLowGate.  Not inlined: its registers would be the kernel's (8 us more).
+template <int GATE>
+__device__ __noinline__ void quantize_low(const F8QuantArgs &a, unsigned kb, unsigned blocks)
+{
+    quantize_blocks<GATE, 1, true>(a, kb, blocks);
+}
+
+// Gates that low are rare.  A warp that has met one goes over its blocks a second time: 101 us for 8192 x 12288 without any
+// (99 if they were not looked for), 121 with one a row.  With the counts in 64 bits, when this took 109: a choice for each
+// element 120, a branch for each block 111.
+template <int GATE, int AHEAD>
+__global__ void __launch_bounds__(kThreads) quantize_f8_kernel(F8QuantArgs a, unsigned kb, unsigned blocks, int pdl)
+{
+    if (pdl) {
+        pdl_launch_dependents();
+        pdl_wait();
+    }
+    const uint32_t lowest = quantize_blocks<GATE, AHEAD, false>(a, kb, blocks);
+    if (GATE == BI_GATE_SILU) {
+        constexpr uint32_t kBits = 0xC2A0;                           // kLowGate as bf16
+        if (__any_sync(0xffffffffu, (lowest >> 16) > kBits || (lowest & 0xFFFF) > kBits)) quantize_low<GATE>(a, kb, blocks);
     }
 }
 

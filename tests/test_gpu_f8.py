@@ -119,6 +119,43 @@ def test_gated_silu(bi, M, K):
         assert (np.abs(v - exact) <= np.abs(exact) * (2.0 ** -4 + off[at] + 2.0 ** -22) + 2.0 ** -10).all()
 
 
+@pytest.mark.parametrize("u_top", [1.0, 1e5, 1e38])
+@pytest.mark.parametrize("g_lo, g_hi", [(-95, -85), (-84, -76), (-131, -95)])
+def test_gated_silu_of_low_gates(bi, g_lo, g_hi, u_top):
+    """Blocks whose gates are all so low that exp(-g), its reciprocal or the product leaves fp32's normal range.  The bounds
+    of test_gated_silu, and half a subnormal step (2^-150) for each product, scale and quotient that is one."""
+    rng = np.random.default_rng(-g_lo)
+    K = 400
+    x = np.concatenate((rng.uniform(g_lo, g_hi, (6, K)), rng.uniform(-1, 1, (6, K)) * u_top), 1)
+    xd, x = bf16(x)
+    q, s = empty_codes(6, K)
+    bi.bi_gated_quantize_f8(xd, bi.BI_GATE_SILU, q, s)
+    g, u = x[:, :K].astype(np.float64), x[:, K:].astype(np.float64)
+    t = g / (1 + np.exp(-g)) * u
+    off = (np.abs(g) + 8) * 2.0 ** -23
+    got_s, got = s.cpu().numpy().astype(np.float64), ref.decode(q.cpu().numpy())
+    for b in range(ref.blocks(K)):
+        at = np.s_[:, b * 128:(b + 1) * 128]
+        amax = np.abs(t[at]).max(1)
+        want = amax / 448
+        # where the largest product rounds to at least one subnormal step a scale has, else the scale is 1
+        seen = amax / 448 > 2.0 ** -149
+        assert (np.abs(got_s[:, b] - want) <= want * (off[at].max(1) + 2.0 ** -23) + 2.0 ** -149)[seen].all()
+        assert (got_s[amax / 448 < 2.0 ** -151, b] == 1).all()
+        exact = np.clip(t[at] / got_s[:, b:b + 1], -448, 448)
+        bound = np.abs(exact) * (2.0 ** -4 + off[at] + 2.0 ** -22) + 2.0 ** -10 + 2.0 ** -149 / got_s[:, b:b + 1]
+        assert (np.abs(got[at] - exact) <= bound)[seen].all()
+
+
+def test_gated_silu_of_gates_below_all(bi):
+    """Gates whose silu no fp32 product can see: zeros with a scale of 1."""
+    x = np.concatenate((np.linspace(-3e38, -300, 256).reshape(2, 128), np.full((2, 128), 3e38)), 1)
+    xd, _ = bf16(x)
+    q, s = empty_codes(2, 128)
+    bi.bi_gated_quantize_f8(xd, bi.BI_GATE_SILU, q, s)
+    assert (s == 1).all() and not (q & 127).any()
+
+
 @pytest.mark.parametrize("N, K, ld", [(1, 16, 16), (127, 128, 128), (300, 400, 404), (1024, 1040, 1040)])
 def test_quantize_weight(bi, N, K, ld):
     rng = np.random.default_rng(N + K)
