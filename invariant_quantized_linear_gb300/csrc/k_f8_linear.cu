@@ -101,7 +101,7 @@ constexpr int kBarBytes = 512;
 template <class C>
 constexpr size_t smem_bytes(int E)
 {
-    static_assert(C::kStages * C::kStage + C::kScales * 4 + kBarBytes + 12 * (kMaxExperts + 1) + 1024 <= 227 * 1024, "fits an SM");
+    static_assert(1024 + C::kStages * C::kStage + C::kScales * 4 + kBarBytes + 12 * (kMaxExperts + 1) <= 227 * 1024, "fits");
     return 1024 + C::kStages * C::kStage + C::kScales * 4 + kBarBytes + 8 * (E + 1) + 4 * (E + 1);
 }
 
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             // ------------------------------------------------ MMAs
             Ring<C::kStages> ring;
             Ring<C::kAccs> accs;
-            bool ok = true;
+            bool ok = true, sound = true;
             const uint64_t dw0 = tc::sdesc_kmajor_sw128(smem_u32(smem));
             const uint64_t dq0 = tc::sdesc_kmajor_sw128(smem_u32(smem) + C::P * kBlockW);
             Tile t;
@@ -541,15 +541,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 };
                 auto stage = [&](auto nb) {
                     const int a = accs.s, s = ring.s;
-                    // Half the lanes look at each barrier: one look's latency for both.  A wait that gave up is
-                    // noted and the tile's MMAs are issued all the same, on what is there: the call's results mean
-                    // nothing then, and the loop is spared a vote and a branch (16 x 12288 x 64: 20.7 us with them,
-                    // 17.7 without).
-                    const bool odd = lane & 1;
-                    if (!mbar_wait_short(odd ? &full[s] : &acc_empty[a], odd ? ring.phase : accs.phase ^ 1u, abort_flag)) fail();
-                    __syncwarp();
+                    // Half the lanes look at each barrier: one look's latency for both.  After a wait that gave up nothing is
+                    // issued or committed any more: `done` would let a producer arrive at a barrier whose phase is still
+                    // open.  The loop goes on to the tile's end without a way out (16 x 12288 x 64: 17.8 us so, 19.6 with
+                    // a branch out of it), a microsecond a block.
+                    uint64_t *bar = lane & 1 ? &full[s] : &acc_empty[a];
+                    const bool there = mbar_wait_short(bar, lane & 1 ? ring.phase : accs.phase ^ 1u, abort_flag);
+                    if (!there) fail();
+                    sound &= __all_sync(0xffffffffu, there);
                     tc::fence_after();
-                    if (elect_one()) {
+                    if (elect_one() & sound) {
 #pragma unroll
                         for (int b = 0; b < decltype(nb)::value; ++b) block(s, a, b);
                         tc::commit(&done[s]);
