@@ -29,7 +29,8 @@
 // together share weight and token tiles in L2.
 //
 // Every wait is bounded: a role that gives up sets the status word and all
-// return; copies in flight are waited for and TMEM is freed.
+// return.  What each has in flight is waited for before (the copies of warp 0 for 1 ms
+// at most, since a stage's barrier counts other warps too), and TMEM is freed.
 //
 // Bound.  8 x 4096 x 24576: 19.6 us, 5.2 TB/s of weights (0.76 of the copy rate),
 // the stream and a CTA's start and end.  Few rows of weights: the chain of blocks,
@@ -55,6 +56,7 @@ namespace {
 constexpr int kTileRows = 128;
 constexpr int kAhead = 8;                 // blocks of K in a scale table
 constexpr int kBlockW = kTileRows * kF8Block;
+constexpr unsigned long long kDrainNs = 1000000;   // for copies in flight after a wait has given up
 
 // T: token columns of a tile at most.  GATHER: token rows are fetched by src.
 template <int T_, bool GATHER_>
@@ -515,10 +517,18 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 }
             }
             if (!ok) fail();
-            // every copy that was issued lands before the CTA can exit
-            volatile int never = 0;
-            for (int s = 0; ok && s < C::kStages; ++s)
-                if (s < ring.s || wrapped) mbar_wait_short(&full[s], s < ring.s ? ring.phase : ring.phase ^ 1u, &never);
+            // Every copy that was issued lands before the CTA can exit.  After a failure the rows by src may never be handed
+            // over, and a stage's barrier not turn: kDrainNs in all then.
+            unsigned long long t0 = 0;
+            for (int s = 0; s < C::kStages; ++s) {
+                if (s >= ring.s && !wrapped) continue;
+                const uint32_t parity = s < ring.s ? ring.phase : ring.phase ^ 1u;
+                while (!mbar_try_wait(&full[s], parity)) {
+                    const unsigned long long t = global_timer_ns();
+                    if (t0 == 0) t0 = t;
+                    if (t - t0 > (*abort_flag ? kDrainNs : kWaitLimitNs)) break;
+                }
+            }
         } else if (warp == 1) {
             // ------------------------------------------------ MMAs
             Ring<C::kStages> ring;
@@ -723,11 +733,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
     }
     __syncwarp();
-    if (*abort_flag) {
-        // copies that were issued around the failure land within this time
-        const unsigned long long t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 100000ull) {}
-    }
     tc::fence_before();
     __syncthreads();
     if (warp == 1) {
