@@ -81,6 +81,10 @@ struct Cfg {
     static constexpr int kScaleLd = T + 4;                     // floats between a table's rows: bank-free for its writers
     static constexpr int kTable = kAhead * kScaleLd;
     static constexpr int kScales = 2 * kTables * kTable;       // floats, two tables in turn
+    // 16 warps share 65,536 registers; the sums get what the others do not need.  An increase waits, without a limit, for
+    // registers of the launch that were given up: launch() checks that the compiler gave it as many.
+    static constexpr bool kSplit = kWide && GATHER;
+    static constexpr int kRoleRegs = 72, kFetchRegs = 56, kSumRegs = 192;
     // a stage's MMAs are waited for by its producers and by the sums: no stage comes round twice before its sums are taken
     static_assert(kStages >= kAccs, "the sums see every phase of done[]");
     static_assert(kTmemCols <= 512 && kAhead % P == 0 && kStage % 1024 == 0, "layout");
@@ -445,8 +449,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     };
 
     if (warp < 4) {
-        // with 16 warps: 4 x 32 x 72 + 4 x 32 x 56 + 8 x 32 x 192 = 16 x 32 x 128, the launch's registers
-        if (C::kWide && C::GATHER) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRoleRegs));
         if (warp == 0) {
             // ------------------------------------------------ copies
             Ring<C::kStages> ring;
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     const uint32_t bytes = NW * 16 * kF8Block + bytes_q;
                     auto copy = [&](int s, int b, int k) {
                         uint8_t *sw = smem + s * C::kStage + b * kBlockW;
-                        uint8_t *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
+                        [[maybe_unused]] uint8_t *sq = smem + s * C::kStage + C::P * kBlockW + b * C::kBlockQ;
                         if constexpr (NW == 8) {
                             tma_load_2d(sw, &map_w, &full[s], k, wy, pol_w);
                         } else {
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     const int a = accs.s, s = ring.s;
                     // Half the lanes look at each barrier: one look's latency for both.  After a wait that gave up nothing is
                     // issued or committed any more: `done` would let a producer arrive at a barrier whose phase is still
-                    // open.  The loop goes on to the tile's end without a way out (16 x 12288 x 64: 17.8 us so, 19.6 with
+                    // open.  The loop goes on to the tile's end without a way out (16 x 12288 x 64: 18.0 us so, 19.6 with
                     // a branch out of it), a microsecond a block.
                     uint64_t *bar = lane & 1 ? &full[s] : &acc_empty[a];
                     const bool there = mbar_wait_short(bar, lane & 1 ? ring.phase : accs.phase ^ 1u, abort_flag);
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // Four rows an instruction, a lane 16 bytes: rows 16 i + 4 (warp % 4) + lane / 8.  A stage is handed over when
         // its copies have landed, kDepth - 1 stages later.  (Gathers of four rows by TMA took 32 cycles each, 1,530 a
         // block of 192.)
-        if (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFetchRegs));
         constexpr int kDepth = C::kStages - 1;
         const int quarter = warp & 3, r4 = 4 * quarter + (lane >> 3), chunk = lane & 7;
         const uint32_t to = smem_u32(smem) + C::P * kBlockW + r4 * 128 + ((chunk ^ (r4 & 7)) << 4);
@@ -692,7 +695,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         while (flying > 0) hand_over();
     } else {
         // ------------------------------------------------ sums and results
-        if (C::kWide && C::GATHER) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        if (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSumRegs));
         const int qd = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
         Ring<C::kStages> ring;
         Ring<C::kAccs> accs;
@@ -750,6 +753,14 @@ cudaError_t launch(const F8LinearArgs &a, bool pdl, cudaStream_t stream)
     cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem_bytes<C>(kMaxExperts)));
     if (e != cudaSuccess) return e;
+    if constexpr (C::kSplit) {
+        static const int regs = [] {
+            cudaFuncAttributes f = {};
+            return cudaFuncGetAttributes(&f, linear_f8_kernel<C>) == cudaSuccess ? f.numRegs : 0;
+        }();
+        if (regs * C::kThreads < 32 * (4 * C::kRoleRegs + 4 * C::kFetchRegs + C::kEpiWarps * C::kSumRegs))
+            return cudaErrorLaunchOutOfResources;
+    }
     Params p;
     p.q = a.q;
     p.s_a = a.s_a;
