@@ -193,8 +193,7 @@ bi_status bi_moe_route(const void *logits, int64_t ldl, int type, int M, int E, 
                             {ws, bi::moe_route_workspace(M, E)}};
     const Span read[] = {{logits, strided(M, ldl, E, type == BI_TYPE_F32 ? 4 : 2)}};
     if (!apart(written, read)) return BI_ERR_INVALID_ARG;
-    int sms = 0;
-    const bi_status st = device_info(&sms);
+    const bi_status st = device_info(nullptr);
     if (st != BI_OK) return st;
     bi::RouteArgs a;
     a.logits = logits;
@@ -212,7 +211,7 @@ bi_status bi_moe_route(const void *logits, int64_t ldl, int type, int M, int E, 
     a.src = src;
     a.pos = pos;
     a.ws = ws;
-    return from_cuda(bi::launch_moe_route(a, sms, (flags & BI_FLAG_PDL) != 0, stream));
+    return from_cuda(bi::launch_moe_route(a, (flags & BI_FLAG_PDL) != 0, stream));
 }
 
 bi_status bi_moe_combine(const uint16_t *rows, int R, const int32_t *pos, const float *weights, int M, int k, int N,
@@ -227,8 +226,7 @@ bi_status bi_moe_combine(const uint16_t *rows, int R, const int32_t *pos, const 
     const Span read[] = {{rows, bytes(R, N, 2)}, {pos, bytes(M, k, 4)}, {weights, bytes(M, k, 4)},
                          {base == y ? nullptr : base, bytes(M, N, 2)}};
     if (!apart(written, read)) return BI_ERR_INVALID_ARG;
-    int sms = 0;
-    const bi_status st = device_info(&sms);
+    const bi_status st = device_info(nullptr);
     if (st != BI_OK) return st;
     bi::CombineArgs a;
     a.rows = rows;
@@ -240,7 +238,7 @@ bi_status bi_moe_combine(const uint16_t *rows, int R, const int32_t *pos, const 
     a.M = M;
     a.k = k;
     a.N = N;
-    return from_cuda(bi::launch_moe_combine(a, sms, (flags & BI_FLAG_PDL) != 0, stream));
+    return from_cuda(bi::launch_moe_combine(a, (flags & BI_FLAG_PDL) != 0, stream));
 }
 
 }  // extern "C"

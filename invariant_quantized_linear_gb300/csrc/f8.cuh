@@ -74,7 +74,7 @@ struct RouteArgs {
 };
 
 size_t moe_route_workspace(int M, int E);
-cudaError_t launch_moe_route(const RouteArgs &a, int sms, bool pdl, cudaStream_t stream);
+cudaError_t launch_moe_route(const RouteArgs &a, bool pdl, cudaStream_t stream);
 
 struct CombineArgs {
     const uint16_t *rows;
@@ -86,6 +86,6 @@ struct CombineArgs {
     int M, k, N;
 };
 
-cudaError_t launch_moe_combine(const CombineArgs &a, int sms, bool pdl, cudaStream_t stream);
+cudaError_t launch_moe_combine(const CombineArgs &a, bool pdl, cudaStream_t stream);
 
 }  // namespace bi

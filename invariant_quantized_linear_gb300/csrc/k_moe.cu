@@ -26,7 +26,7 @@ namespace {
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kChunk = 64;                        // tokens of a chunk, where that gives at most kMostChunks
-constexpr int kMostChunks = 152;
+constexpr int kMostChunks = 152;                  // the SMs; a constant, as the workspace for their counts is sized without a device
 constexpr size_t kPlainSmem = 47 * 1024;          // dynamic shared memory that needs no opt-in, the static share beside it
 
 int chunk_tokens(int M)
@@ -374,9 +374,8 @@ size_t moe_route_workspace(int M, int E)
     return (static_cast<size_t>(chunks) * E * 4 + 255) / 256 * 256;
 }
 
-cudaError_t launch_moe_route(const RouteArgs &a, int sms, bool pdl, cudaStream_t stream)
+cudaError_t launch_moe_route(const RouteArgs &a, bool pdl, cudaStream_t stream)
 {
-    (void)sms;
     if (a.E <= 32) return route<1>(a, pdl, stream);
     if (a.E <= 64) return route<2>(a, pdl, stream);
     if (a.E <= 128) return route<4>(a, pdl, stream);
@@ -384,9 +383,8 @@ cudaError_t launch_moe_route(const RouteArgs &a, int sms, bool pdl, cudaStream_t
     return route<32>(a, pdl, stream);
 }
 
-cudaError_t launch_moe_combine(const CombineArgs &a, int sms, bool pdl, cudaStream_t stream)
+cudaError_t launch_moe_combine(const CombineArgs &a, bool pdl, cudaStream_t stream)
 {
-    (void)sms;
     auto aligned16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const bool vec = a.N % 8 == 0 && aligned16(a.rows) && aligned16(a.y) && (!a.base || aligned16(a.base));
     const int per_row = vec ? a.N / 8 : a.N;
