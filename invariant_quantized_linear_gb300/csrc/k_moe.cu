@@ -26,7 +26,7 @@ namespace {
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kChunk = 64;                        // tokens of a chunk, where that gives at most kMostChunks
-constexpr int kMostChunks = 152;                  // the SMs; a constant, as the workspace for their counts is sized without a device
+constexpr int kMostChunks = 152;                  // the SMs; a constant, as the counts' workspace is sized without a device
 constexpr size_t kPlainSmem = 47 * 1024;          // dynamic shared memory that needs no opt-in, the static share beside it
 
 int chunk_tokens(int M)
