@@ -641,7 +641,9 @@ BI_API bi_status bi_linear_f8_grouped(const uint8_t *q, const float *s_a, int q_
  *   ws       workspace of at least bi_moe_route_workspace_size(M, E) bytes, 16-byte
  *            aligned, scratch: calls that may overlap must not share one
  * 1 <= M <= 65535, 1 <= E <= 1024, 1 <= k <= min(E, 32), scale finite.  Outputs and
- * workspace overlap neither one another nor the logits.
+ * workspace overlap neither one another nor the logits.  More than 2^20 slots are more
+ * rows than the quantisers and the grouped linear take: such a prompt goes in parts, each
+ * with a routing of its own, and has the same bits.
  */
 enum { BI_TYPE_F32 = 0, BI_TYPE_BF16 = 1 };
 enum { BI_ROUTE_SOFTMAX = 0, BI_ROUTE_SIGMOID = 1 };

@@ -7,7 +7,7 @@
 // One order for every form.  A row's bits may not depend on the rows that share
 // the call, and d_b is not an exact sum, so every form issues the same
 // instructions for an element: weights are the MMA's M = 128 rows, tokens its N
-// columns (16 .. 256 of them), a block is four K = 32 slices in order into an
+// columns (16 .. 192 of them), a block is four K = 32 slices in order into an
 // accumulator that starts at 0, and no form splits K.  Work is split over weight
 // rows and tokens alone.
 //
@@ -23,8 +23,9 @@
 // are bound by the weight stream cut the weight rows into units of 16, order the
 // units by expert, token tile and row, and give each CTA an equal run of them, in
 // tiles of up to 128 rows that are about as high as one another: every SM streams
-// the same bytes, whatever N is, and no tile is so low that its MMAs (350 cycles a
-// block, however few its rows) take longer than its bytes.  Calls that are bound
+// the same bytes, whatever N is.  A block's MMAs take about as long however few its
+// rows are, so tiles of less than some 50 rows are bound by them and not by their
+// bytes (16 and 32 rows for 1 x 4096 x 4096).  Calls that are bound
 // by the tensor cores have units of 128 rows, dealt in turn, so that CTAs that run
 // together share weight and token tiles in L2.
 //
@@ -32,16 +33,24 @@
 // return.  What each has in flight is waited for before (the copies of warp 0 for 1 ms
 // at most, since a stage's barrier counts other warps too), and TMEM is freed.
 //
-// Bound.  8 x 4096 x 24576: 19.6 us, 5.2 TB/s of weights (0.76 of the copy rate),
-// the stream and a CTA's start and end.  Few rows of weights: the chain of blocks,
-// of which the MMAs take 345 cycles each (16 x 12288 x 64: 17.7 us for 96 blocks).
-// 2048 x 4096 x 12288: 125 us, 1,650 TFLOP/s, 0.42 of twice the bf16 rate: the roles'
-// own instructions around each block, of the MMA warp above all (400 cycles to issue
-// four MMAs and a commit, 250 of looks and loop), where the tensor cores need 384 for
-// 128 x 192 x 128.  Fewer bytes, fewer MMAs or fewer sums do not shorten it (8, 12 or
-// 16 warps of sums: 127, 134, 134 us).  Each role runs as a whole warp that elects a thread for the issue, without
-// branches in its loop: single-thread loops and branches around copies, MMAs or TMEM
-// loads cost two to four times as much.
+// Bound.  8 x 4096 x 24576: 20.0 us, 5.0 TB/s of weights (0.74 of the copy rate),
+// the stream and a CTA's start and end.  Few rows of weights: the chain of a CTA's
+// blocks, one after another (1 x 4096 x 4096: 10.0 us, of which 16 stages of two blocks
+// are 5, at 610 cycles; 16 x 12288 x 64: 18.0 for 96 blocks).  Nothing in the order of
+// sums asks for that: several CTAs could compute the sums of blocks side by side, and
+// one join them in order.
+// 2048 x 4096 x 12288: 125 us, 1,650 TFLOP/s, 0.42 of twice the bf16 rate.  A CTA has
+// seven tiles of 32 blocks, about 1,000 cycles a block and 2,200 to 2,600 from a tile's
+// last block to the next one's first, where the tensor cores need 384 for 128 x 192 x
+// 128.  By time stamps, which add a few tens of cycles to each part: the MMA warp waits
+// 540, issues for 310, loops for 160; a warp of sums waits 140, reads 550, adds the
+// rest for 80, loops for 155; the copies wait 665.  So the round of the two
+// accumulators that TMEM holds is the period: 310 to issue, 760 until the sums see the
+// commit, 550 to read, and back.  8, 12 or 16 warps of sums: 127, 134, 134 us.  This
+// width spills: 24 bytes stored and 104 loaded a thread, 160 and 208 with src.
+// Each role runs as a whole warp that elects a thread for the issue, without branches
+// in its loop: single-thread loops and branches around copies, MMAs or TMEM loads cost
+// two to four times as much.
 #include "f8.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
