@@ -156,6 +156,26 @@ def test_gated_silu_of_gates_below_all(bi):
     assert (s == 1).all() and not (q & 127).any()
 
 
+@pytest.mark.parametrize("M, K", [(3, 1040), (3000, 1408)])
+def test_low_gates_change_no_other_block(bi, M, K):
+    """A gate below -80 sends its warp over all its blocks again: those without one keep their bits, in short calls and in
+    those that read two blocks ahead."""
+    rng = np.random.default_rng(M)
+    x = rng.normal(size=(M, 2 * K)).astype(np.float32) * 5
+    low = x.copy()
+    block = rng.integers(0, K // 128, M)
+    low[np.arange(M), block * 128 + rng.integers(0, 128, M)] = rng.uniform(-300, -81, M)
+    low[M // 2:, :K] = x[M // 2:, :K]                # rows without any
+    (q, s), (q2, s2) = empty_codes(M, K), empty_codes(M, K)
+    bi.bi_gated_quantize_f8(bf16(x)[0], bi.BI_GATE_SILU, q, s)
+    bi.bi_gated_quantize_f8(bf16(low)[0], bi.BI_GATE_SILU, q2, s2)
+    same = np.ones((M, ref.blocks(K)), bool)
+    same[np.arange(M // 2), block[:M // 2]] = False
+    assert (s.cpu().numpy() == s2.cpu().numpy())[same].all()
+    codes = (q.cpu().numpy() == q2.cpu().numpy())
+    assert codes[np.repeat(same, 128, 1)[:, :K]].all()
+
+
 @pytest.mark.parametrize("N, K, ld", [(1, 16, 16), (127, 128, 128), (300, 400, 404), (1024, 1040, 1040)])
 def test_quantize_weight(bi, N, K, ld):
     rng = np.random.default_rng(N + K)
